@@ -1,0 +1,438 @@
+"""The operators of the quantised key / value cache, as they are measured.
+
+A layer that runs on this library's INT4 codes keeps its keys and values per head
+in INT4 too: a row of head_dim values is multiplied by a full factor of its head
+(P for keys and values, P^-T for queries, so that scores are unchanged) and stored
+as 4-bit codes with one fp32 scale.  The cases are the calls around that cache:
+
+  append     new tokens of q, k, v: rotary positions, the per-head factors, INT4,
+             and the scatter into the pages of the cache; then the appended rows are
+             read back as the values that the codes stand for
+  attention  queries against the pages of their sequences: one token per sequence,
+             a few (verification of drafted tokens), or a chunk of a prompt
+  shared     the same for a batch whose sequences begin with one common prefix
+
+Cache layout: codes [pages, kv_heads, page, head_dim / 2], two per byte, element 2i
+in the low nibble; scales [pages, kv_heads, page].  With ``own`` false everything
+below is elementary torch in fp32; the transform and rounding of keys and values is
+in fp64, because a value next to a rounding border decides a whole code.
+"""
+import math
+import random
+
+import torch
+
+own = False
+
+POSITIONS = 131072  # rows of the rotary table
+
+
+# ---- cases ---------------------------------------------------------------------
+
+def listed():
+    return [
+        # One request decoding: 32 query heads on 8 key heads, one token.
+        dict(name="append_1", kind="append", T=1, q_heads=32, kv_heads=8, D=128, page=16, rope=128, inter=False,
+             alpha=0.9, pad=0),
+        # A decoding batch replayed at a fixed size: 61 of 256 rows are padding (slot -1).
+        dict(name="append_256", kind="append", T=256, q_heads=64, kv_heads=8, D=128, page=32, rope=128, inter=False,
+             alpha=0.88, pad=61),
+        # A short prompt of a model with 64-wide heads, as many key as query heads, half rotated in neighbouring pairs.
+        dict(name="append_777_d64", kind="append", T=777, q_heads=12, kv_heads=12, D=64, page=16, rope=32, inter=True,
+             alpha=1.0, pad=0),
+        # A prompt of 8192 tokens at hidden size 8192.
+        dict(name="append_8192", kind="append", T=8192, q_heads=64, kv_heads=8, D=128, page=64, rope=128, inter=False,
+             alpha=0.9, pad=0),
+        # One request decoding after a prompt of ordinary length.
+        dict(name="decode_1", kind="attention", B=1, nq=1, lo=1531, hi=1531, empty=0, q_heads=32, kv_heads=8, D=128,
+             page=16, window=0, softcap=0.0),
+        # A serving batch: lengths from 60 to 8192, three slots of it idle.
+        dict(name="decode_64", kind="attention", B=64, nq=1, lo=60, hi=8192, empty=3, q_heads=64, kv_heads=8, D=128,
+             page=16, window=0, softcap=0.0),
+        # Four requests with long documents.
+        dict(name="decode_long", kind="attention", B=4, nq=1, lo=65000, hi=131072, empty=0, q_heads=32, kv_heads=8,
+             D=128, page=64, window=0, softcap=0.0),
+        # Up to five drafted tokens each are verified; 64-wide heads, a window, scores capped by a tanh.
+        dict(name="verify_24", kind="attention", B=24, nq=5, lo=3, hi=4100, empty=1, q_heads=16, kv_heads=4, D=64,
+             page=32, window=1024, softcap=30.0),
+        # Two prompts arriving in chunks of up to 1024 tokens, far into their texts.
+        dict(name="chunk_1024", kind="attention", B=2, nq=1024, lo=2500, hi=6001, empty=0, q_heads=32, kv_heads=8,
+             D=128, page=16, window=0, softcap=0.0),
+        # Eight continuations of one prompt, just begun.
+        dict(name="shared_8", kind="shared", B=8, nq=1, prefix=1000, lo=1, hi=64, empty=0, q_heads=32, kv_heads=8,
+             D=128, page=16, window=0, softcap=0.0),
+        # 64 requests behind one long system prompt.
+        dict(name="shared_64", kind="shared", B=64, nq=1, prefix=16384, lo=16, hi=512, empty=2, q_heads=64, kv_heads=8,
+             D=128, page=16, window=0, softcap=0.0),
+        # 200 samples of one problem, 64-wide heads without grouping, two tokens a step, capped scores.
+        dict(name="shared_200_d64", kind="shared", B=200, nq=2, prefix=6007, lo=2, hi=300, empty=0, q_heads=16,
+             kv_heads=16, D=64, page=32, window=0, softcap=50.0),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    kind = rng.choice(["append", "attention", "attention", "shared"])
+    D = rng.choice([64, 128, 128])
+    kv_heads = rng.choice([1, 2, 4, 5, 8, 16])
+    q_heads = kv_heads * rng.choice([g for g in (1, 2, 3, 4, 5, 7, 8, 16) if kv_heads * g <= 64])
+    page = rng.choice([16, 32, 64, 128])
+    c = dict(kind=kind, q_heads=q_heads, kv_heads=kv_heads, D=D, page=page)
+    if kind == "append":
+        T = _log(rng, 1, 8192)
+        rope = rng.choice([0, D // 4, D // 2, D, D, D])
+        return dict(c, T=T, rope=rope, inter=rng.random() < 0.3, alpha=round(rng.uniform(0.7, 1.0), 3),
+                    pad=rng.choice([0, 0, T // 4]))
+    softcap = rng.choice([0.0, 0.0, 20.0, 50.0])
+    if kind == "shared":
+        B, nq = _log(rng, 2, 256), rng.choice([1, 1, 1, 2])
+        prefix = _log(rng, 20, min(16384, 16384 * 64 * 64 // (B * nq * q_heads)))
+        return dict(c, B=B, nq=nq, prefix=prefix, lo=rng.randint(1, 30), hi=_log(rng, 32, 512),
+                    empty=rng.choice([0, 0, B // 8]), window=0, softcap=softcap)
+    sort = rng.choice(["one", "one", "few", "chunk"])
+    window = rng.choice([0, 0, _log(rng, 64, 4096)])
+    if sort == "chunk":  # pairs of queries and keys over all heads are bounded by the listed chunk's
+        B = rng.randint(1, 3)
+        nq = _log(rng, 48, 1024)
+        hi = nq + rng.randint(0, min(5000, 2 * 1024 * 32 * 6000 * 128 // (B * nq * q_heads * D) - nq))
+        lo = rng.randint(nq, hi)
+    else:
+        B = _log(rng, 1, 128)
+        nq = 1 if sort == "one" else rng.randint(2, 8)
+        hi = max(40, min(131072, _log(rng, 40, 500000 // B)) * 8 // max(8, kv_heads))
+        lo = max(1, hi // rng.choice([1, 4, 50]))
+    return dict(c, B=B, nq=nq, lo=lo, hi=hi, empty=rng.choice([0, 0, B // 6]), window=window, softcap=softcap)
+
+
+def _lens(case):
+    """Keys and queries of each sequence: part of the case, the same for every seed."""
+    r = random.Random("%(B)d %(nq)d %(lo)d %(hi)d" % case)
+    keys = [case["hi"]] + [_log(r, case["lo"], case["hi"]) for _ in range(case["B"] - 1)]
+    if case["nq"] == 1:
+        nqs = [1] * case["B"]
+    elif case["nq"] <= 8:
+        nqs = [r.randint(1, case["nq"]) for _ in keys]
+        nqs[0] = case["nq"]
+    else:
+        nqs = [case["nq"]] + [r.randint(case["nq"] // 2, case["nq"]) for _ in keys[1:]]
+    for i in range(case["empty"]):  # idle slots of a padded batch: a query row, no keys
+        keys[-1 - i] = 0
+    if case["kind"] == "attention":
+        nqs = [min(q, n) if n else q for q, n in zip(nqs, keys)]
+    return keys, nqs
+
+
+# ---- inputs --------------------------------------------------------------------
+
+def _factor(g, D):
+    """An orthogonal factor times a mild diagonal, as learned ones are, and its inverse transpose; bf16."""
+    a = torch.randn(D, D, generator=g, device="cuda", dtype=torch.float64)
+    q = torch.linalg.qr(a)[0]
+    d = torch.exp(0.1 * torch.randn(D, generator=g, device="cuda", dtype=torch.float64))
+    return (q * d).to(torch.bfloat16), (q / d).to(torch.bfloat16)
+
+
+# Sixteen equally likely values of a normal distribution, quantised as a row of 128 is.
+_CODES = (-7, -5, -4, -3, -2, -2, -1, 0, 0, 1, 2, 2, 3, 4, 5, 7)
+
+
+def _pool(g, pages, heads, page, D):
+    lut = torch.tensor([((_CODES[b >> 4] & 15) << 4) | (_CODES[b & 15] & 15) for b in range(256)], dtype=torch.uint8,
+                       device="cuda")
+    n = (pages, heads, page, D // 2)
+    codes = torch.empty(n, dtype=torch.uint8, device="cuda").random_(0, 256, generator=g)
+    for i in range(0, pages, 4096):  # the lookup's index is eight bytes per code byte
+        codes[i:i + 4096] = lut[codes[i:i + 4096].to(torch.int32)]
+    scale = 0.3 * torch.exp(0.25 * torch.randn(n[:3], generator=g, device="cuda"))
+    return codes, scale
+
+
+def prepare(case, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    H, Hk, D, page = case["q_heads"], case["kv_heads"], case["D"], case["page"]
+    s = dict(case=case)
+    if case["kind"] == "append":
+        T = case["T"]
+        # q, k, v of one projection, side by side; a few large channels per key head
+        qkv = torch.randn(T, H + 2 * Hk, D, generator=g, device="cuda")
+        big = torch.randint(0, D, (Hk, 3), generator=g, device="cuda")
+        qkv[:, H:H + Hk].scatter_(2, big[None].expand(T, Hk, 3),
+                                  15.0 * torch.randn(T, Hk, 3, generator=g, device="cuda"))
+        qkv = qkv.to(torch.bfloat16)
+        Pk, Pq = _factor(g, D)
+        Pv, _ = _factor(g, D)
+        one = torch.arange(T, device="cuda")
+        if T <= 512:  # a step of as many sequences, each at a page and a position of its own
+            pages = T + 3
+            slots = torch.randperm(pages, generator=g, device="cuda")[:T] * page
+            slots += torch.randint(0, page, (T,), generator=g, device="cuda")
+            positions = torch.randint(0, POSITIONS, (T,), generator=g, device="cuda").to(torch.int32)
+        else:  # a prompt: consecutive positions, whole pages in any order
+            pages = (T + page - 1) // page + 3
+            slots = torch.randperm(pages, generator=g, device="cuda")[one // page] * page + one % page
+            positions = (torch.randint(0, POSITIONS - T, (1,), generator=g, device="cuda") + one).to(torch.int32)
+        if case["pad"]:
+            slots[T - case["pad"]:] = -1
+        table = None
+        if case["rope"]:
+            half = case["rope"] // 2
+            inv = 500000.0 ** (-torch.arange(half, device="cuda", dtype=torch.float64) / half)
+            ang = torch.arange(POSITIONS, device="cuda", dtype=torch.float64)[:, None] * inv
+            table = torch.cat([torch.cos(ang), torch.sin(ang)], 1).float()
+        s.update(q=qkv[:, :H], k=qkv[:, H:H + Hk], v=qkv[:, H + Hk:], Pq=Pq, Pk=Pk, Pv=Pv, positions=positions,
+                 slots=slots, table=table,
+                 pool=[x for _ in range(2) for x in (torch.zeros(pages, Hk, page, D // 2, dtype=torch.uint8, device="cuda"),
+                                                     torch.zeros(pages, Hk, page, device="cuda"))],
+                 q_out=torch.empty(T, H, D, dtype=torch.bfloat16, device="cuda"),
+                 k_out=torch.empty(T, Hk, D, dtype=torch.bfloat16, device="cuda"),
+                 v_out=torch.empty(T, Hk, D, dtype=torch.bfloat16, device="cuda"))
+    else:
+        keys, nqs = _lens(case)
+        B, T = case["B"], sum(nqs)
+        need = [(n + page - 1) // page for n in keys]
+        width = max(1, max(need))
+        pre = (case.get("prefix", 0) + page - 1) // page
+        total = sum(need) + pre + 2
+        perm = torch.randperm(total, generator=g, device="cuda").to(torch.int32)
+        table = torch.full((B, width), -1, dtype=torch.int32, device="cuda")
+        at = torch.tensor([0] + need, device="cuda").cumsum(0)
+        col = torch.arange(width, device="cuda")
+        idx = at[:-1, None] + col
+        used = col < torch.tensor(need, device="cuda")[:, None]
+        table[used] = perm[idx[used]]
+        row = [b * max(nqs) + j for b in range(B) for j in range(nqs[b])]
+        s.update(row=torch.tensor(row, device="cuda"), pool=[x for _ in range(2) for x in _pool(g, total, Hk, page, D)], table=table, width=width,
+                 prefix_pages=perm[sum(need):sum(need) + pre].contiguous(),
+                 kv_len=torch.tensor(keys, dtype=torch.int32, device="cuda"),
+                 q_start=torch.tensor([0] + nqs, device="cuda").cumsum(0).to(torch.int32), T=T, max_q=max(nqs),
+                 q=(1.5 * torch.randn(T, H, D, generator=g, device="cuda")).to(torch.bfloat16),
+                 scale=1.0 / math.sqrt(D),
+                 out=torch.zeros(T, H, D, dtype=torch.bfloat16, device="cuda"),
+                 lse=torch.zeros(T, H, device="cuda"))
+    if own:  # the handles and the workspace that a program keeps beside its buffers
+        from kronecker_factored_transforms_b200 import _lib as kq
+        s["cache"] = kq.kv_cache(*s["pool"])
+        if case["kind"] == "append":
+            s["transform"] = kq.kv_transform(s["Pq"], s["Pk"], s["Pv"], case["alpha"], case["alpha"], rope=s["table"],
+                                             interleaved=case["inter"])
+        else:
+            n = kq.kq_kv_attention_workspace_bytes(s["T"], case["B"], H, Hk, D, s["max_q"])
+            s["workspace"] = torch.empty(n, dtype=torch.uint8, device="cuda")
+    return s
+
+
+# ---- one pass ------------------------------------------------------------------
+
+def run(s):
+    c = s["case"]
+    if own:
+        from kronecker_factored_transforms_b200 import _lib as kq
+        if c["kind"] == "append":
+            q, k, v = s["q"], s["k"], s["v"]
+            kq.kq_kv_append(s["cache"], s["transform"], q, q.stride(0), k, k.stride(0), v, v.stride(0),
+                            s["positions"], s["slots"], s["q_out"], c["T"], c["q_heads"])
+            kq.kq_kv_gather(s["cache"], s["slots"], s["k_out"], s["v_out"], c["T"])
+            return {"q": s["q_out"], "k": s["k_out"], "v": s["v_out"]}
+        w = s["workspace"]
+        if c["kind"] == "attention":
+            kq.kq_kv_attention(s["cache"], s["q"], s["q_start"], s["table"], s["width"], s["kv_len"], s["scale"],
+                               c["softcap"], c["window"], s["out"], s["lse"], w, w.numel(), s["T"], c["B"],
+                               c["q_heads"], s["max_q"])
+        else:
+            kq.kq_kv_attention_shared(s["cache"], s["q"], s["q_start"], s["prefix_pages"], c["prefix"], s["table"],
+                                      s["width"], s["kv_len"], s["scale"], c["softcap"], c["window"], s["out"],
+                                      s["lse"], w, w.numel(), s["T"], c["B"], c["q_heads"], s["max_q"])
+        return {"out": s["out"], "lse": s["lse"]}
+    return _plain_append(s) if c["kind"] == "append" else _plain_attention(s)
+
+
+def _rotate(x, s):
+    """x [T, heads, D] by the angles of its tokens, in x's type."""
+    r = s["case"]["rope"]
+    if not r:
+        return x
+    cs = s["table"][s["positions"].long()].to(x.dtype)[:, None]
+    cos, sin = cs[..., :r // 2], cs[..., r // 2:]
+    if s["case"]["inter"]:
+        a, b = x[..., 0:r:2], x[..., 1:r:2]
+        turned = torch.stack([a * cos - b * sin, a * sin + b * cos], -1).flatten(-2)
+    else:
+        a, b = x[..., :r // 2], x[..., r // 2:r]
+        turned = torch.cat([a * cos - b * sin, a * sin + b * cos], -1)
+    return torch.cat([turned, x[..., r:]], -1)
+
+
+def _plain_append(s):
+    alpha = float(torch.tensor(s["case"]["alpha"], dtype=torch.float32))
+    keep = (s["slots"] >= 0)[:, None, None]
+
+    def stored(y):
+        scale = alpha * y.abs().amax(-1, keepdim=True) / 7
+        code = torch.clamp(torch.round(y / torch.where(scale > 0, scale, 1.0)), -8, 7)
+        return torch.where(keep, code.float() * scale.float(), 0.0).to(torch.bfloat16)
+
+    return {"q": (_rotate(s["q"].float(), s) @ s["Pq"].float()).to(torch.bfloat16),
+            "k": stored(_rotate(s["k"].double(), s) @ s["Pk"].double()),
+            "v": stored(s["v"].double() @ s["Pv"].double())}
+
+
+def _values(codes, scale):
+    lo, hi = codes & 15, codes >> 4
+    q = torch.stack([lo, hi], -1).flatten(-2).to(torch.float32)
+    return torch.where(q > 7, q - 16, q) * scale[..., None]
+
+
+def _rows(pages, codes, scale):
+    """[..., P] page numbers -> [..., heads, P * page, D] values."""
+    at = pages.clamp(min=0).long()
+    x = _values(codes[at], scale[at])  # [..., P, heads, page, D]
+    return x.transpose(-4, -3).flatten(-3, -2)
+
+
+def _plain_attention(s):
+    c = s["case"]
+    H, Hk, D, nq, B = c["q_heads"], c["kv_heads"], c["D"], s["max_q"], c["B"]
+    G = H // Hk
+    kc, ks, vc, vs = s["pool"]
+    n_q = s["q_start"][1:] - s["q_start"][:-1]
+    i = torch.arange(nq, device="cuda")
+    tok = (s["q_start"][:-1, None] + i).clamp(max=s["T"] - 1).long()  # [B, nq], the last ones repeated
+    q = s["q"].float()[tok].reshape(B, nq, Hk, G, D).permute(0, 2, 1, 3, 4).reshape(B, Hk, nq * G, D)
+    K, V = _rows(s["table"], kc, ks), _rows(s["table"], vc, vs)
+    score = q @ K.transpose(-1, -2)  # [B, Hk, nq * G, L]
+    at = torch.arange(K.shape[-2], device="cuda")
+    last = (s["kv_len"] - n_q)[:, None] + i  # [B, nq]: the query's own place among its sequence's keys
+    see = (at <= last[..., None]) & (at < s["kv_len"][:, None, None])
+    if c["window"]:
+        see &= at > last[..., None] - c["window"]
+    see = see.repeat_interleave(G, 1)[:, None]
+    if c["kind"] == "shared":
+        Kp, Vp = _rows(s["prefix_pages"], kc, ks)[:, :c["prefix"]], _rows(s["prefix_pages"], vc, vs)[:, :c["prefix"]]
+        score = torch.cat([q @ Kp.transpose(-1, -2), score], -1)
+        see = torch.cat([torch.ones_like(see[..., :1]).expand(*see.shape[:-1], c["prefix"]), see], -1)
+    score = score * s["scale"]
+    if c["softcap"]:
+        score = c["softcap"] * torch.tanh(score / c["softcap"])
+    score = torch.where(see, score, -math.inf)
+    top = score.amax(-1, keepdim=True)
+    p = torch.exp(score - torch.where(top > -math.inf, top, 0.0))
+    total = p.sum(-1, keepdim=True)
+    part = p[..., :-K.shape[-2]] @ Vp if c["kind"] == "shared" else 0.0
+    o = (part + p[..., -K.shape[-2]:] @ V) / torch.where(total > 0, total, 1.0)
+    lse = (top + torch.log(total))[..., 0]
+    o = o.reshape(B, Hk, nq, G, D).permute(0, 2, 1, 3, 4).reshape(B, nq, H, D)
+    lse = lse.reshape(B, Hk, nq, G).permute(0, 2, 1, 3).reshape(B, nq, H)
+    return {"out": o.flatten(0, 1)[s["row"]].to(torch.bfloat16), "lse": lse.flatten(0, 1)[s["row"]]}
+
+
+# ---- what a pass cannot do without -------------------------------------------------
+
+def work(case):
+    H, Hk, D = case["q_heads"], case["kv_heads"], case["D"]
+    row = D // 2 + 4  # a row of the cache
+    if case["kind"] == "append":
+        T, kept = case["T"], case["T"] - case["pad"]
+        io = T * (H + 2 * Hk) * D * 2 + T * H * D * 2 + T * (12 + 4 * case["rope"]) + 3 * D * D * 2
+        # the appended rows are written once, read once for the read-back, and come back in bf16
+        return {"bytes": io + kept * 2 * Hk * row * 2 + T * 2 * Hk * D * 2, "flops": T * (H + 2 * Hk) * 2 * D * D}
+    keys, nqs = _lens(case)
+    w = case["window"]
+    pairs = seen = 0
+    for n, m in zip(keys, nqs):
+        first = max(0, n - m + 1 - w) if w else 0
+        seen += n - first
+        for j in range(m):
+            end = max(0, min(n, n - m + j + 1))
+            pairs += min(end, w) if w else end
+    pre = case.get("prefix", 0)
+    pairs += pre * sum(nqs)
+    T = sum(nqs)
+    return {"bytes": (seen + pre) * 2 * Hk * row + T * H * (4 * D + 4), "flops": 4 * D * H * pairs}
+
+
+# ---- from the definitions, in 64 bits ------------------------------------------------
+
+def _nibbles(codes):
+    v = torch.empty(*codes.shape[:-1], codes.shape[-1] * 2, dtype=torch.float64, device=codes.device)
+    signed = torch.tensor([0, 1, 2, 3, 4, 5, 6, 7, -8, -7, -6, -5, -4, -3, -2, -1], dtype=torch.float64, device=codes.device)
+    v[..., 0::2] = signed[(codes & 15).to(torch.int32)]
+    v[..., 1::2] = signed[(codes >> 4).to(torch.int32)]
+    return v
+
+
+def _exact_append(s):
+    c = s["case"]
+    D, r, T = c["D"], c["rope"], c["T"]
+    alpha = float(torch.tensor(c["alpha"], dtype=torch.float32))
+    # the rotation of each pair as a complex product
+    turn = None
+    if r:
+        t = s["table"][s["positions"].long()].double()
+        turn = torch.complex(t[:, :r // 2].contiguous(), t[:, r // 2:].contiguous())
+    pairs = torch.arange(r, device="cuda").reshape(-1, 2) if c["inter"] else torch.arange(r, device="cuda").reshape(2, -1).T
+
+    def one(x, P, rotated):
+        x = x.double().clone()  # [T, D], one head
+        if rotated and r:
+            z = torch.complex(x[:, pairs[:, 0]], x[:, pairs[:, 1]]) * turn
+            x[:, pairs[:, 0]], x[:, pairs[:, 1]] = z.real, z.imag
+        return torch.einsum("td,de->te", x, P.double())
+
+    def cached(y):
+        top = y.abs().max(dim=1).values
+        step = alpha * top / 7
+        code = torch.round(y / torch.where(step > 0, step, torch.ones_like(step))[:, None]).clamp(-8, 7)
+        return code * step[:, None] * (s["slots"] >= 0).double()[:, None]
+
+    q = torch.stack([one(s["q"][:, h], s["Pq"], True) for h in range(c["q_heads"])], 1)
+    k = torch.stack([cached(one(s["k"][:, h], s["Pk"], True)) for h in range(c["kv_heads"])], 1)
+    v = torch.stack([cached(one(s["v"][:, h], s["Pv"], False)) for h in range(c["kv_heads"])], 1)
+    return {"q": q, "k": k, "v": v}
+
+
+def _exact_attention(s):
+    c = s["case"]
+    H, Hk, D, page = c["q_heads"], c["kv_heads"], c["D"], c["page"]
+    G, pre = H // Hk, c.get("prefix", 0)
+    kc, ks, vc, vs = s["pool"]
+    keys, nqs = _lens(c)
+    out = torch.zeros(s["T"], H, D, dtype=torch.float64, device="cuda")
+    lse = torch.full((s["T"], H), -math.inf, dtype=torch.float64, device="cuda")
+
+    def fetch(codes, scale, pages, n, h):
+        v = _nibbles(codes[pages, h].reshape(-1, D // 2)[:n])
+        return v * scale[pages, h].reshape(-1)[:n].double()[:, None]
+
+    prefix_at = s["prefix_pages"].long()
+    for h in range(Hk):
+        kp, vp = fetch(kc, ks, prefix_at, pre, h), fetch(vc, vs, prefix_at, pre, h)
+        first = 0
+        for b, (n, m) in enumerate(zip(keys, nqs)):
+            at = s["table"][b, :(n + page - 1) // page].long()
+            K = torch.cat([kp, fetch(kc, ks, at, n, h)])
+            V = torch.cat([vp, fetch(vc, vs, at, n, h)])
+            if K.shape[0]:
+                q = s["q"][first:first + m, h * G:(h + 1) * G].double()
+                x = torch.einsum("mgd,nd->mgn", q, K) * s["scale"]
+                if c["softcap"]:
+                    x = torch.tanh(x / c["softcap"]) * c["softcap"]
+                place = torch.arange(K.shape[0], device="cuda")
+                mine = pre + n - m + torch.arange(m, device="cuda")[:, None, None]
+                hidden = (place > mine) & (place >= pre)
+                if c["window"]:
+                    hidden |= place <= mine - c["window"]
+                x = x.masked_fill(hidden, -math.inf)
+                z = torch.logsumexp(x, -1)
+                weight = torch.exp(x - torch.where(torch.isfinite(z), z, torch.zeros_like(z))[..., None])
+                out[first:first + m, h * G:(h + 1) * G] = torch.einsum("mgn,nd->mgd", weight, V)
+                lse[first:first + m, h * G:(h + 1) * G] = z
+            first += m
+    return {"out": out, "lse": lse}
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    return _exact_append(s) if case["kind"] == "append" else _exact_attention(s)
