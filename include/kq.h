@@ -271,10 +271,176 @@ kq_status kq_transform_quant_two_stage_static(const uint16_t *x, const uint16_t 
 uint64_t kq_two_stage_workspace_bytes(int64_t T, int n1, int n2);
 
 /*
+ * ---- The quantised key / value cache ------------------------------------------
+ *
+ * Pages of INT4 key and value rows (the per-head rows of
+ * kq_headwise_transform_quant, kept where a serving program keeps them), the
+ * call that appends new tokens to them and the attention that reads them.
+ *
+ * A cache row is head_dim codes of one (token, key head), two per byte with
+ * element 2k in the low nibble, and one fp32 scale s; it stands for code * s.
+ * Keys are stored as k P_k and queries are given as q P_k^-T, so their products
+ * are those of q and k; values are stored as v P_v, and the attention's output
+ * is in the same basis (P_v^-1 belongs into the output projection: see
+ * fold_value_factor in weights.py).
+ *
+ * The struct is a host-side description that the caller fills in once; the
+ * memory is the caller's.  A slot is page * page_size + place in the page.
+ */
+typedef struct kq_kv_cache {
+    uint8_t *k_codes;  /* device [num_pages, kv_heads, page_size, head_dim / 2], 16-byte aligned */
+    float *k_scale;    /* device [num_pages, kv_heads, page_size], 16-byte aligned               */
+    uint8_t *v_codes;  /* as k_codes                                                             */
+    float *v_scale;    /* as k_scale                                                             */
+    int64_t num_pages; /* 1 .. 2^31 - 1                                                          */
+    int page_size;     /* 16, 32, 64, 128 or 256                                                 */
+    int kv_heads;      /* 1 .. 1024                                                              */
+    int head_dim;      /* 64 or 128                                                              */
+} kq_kv_cache;
+
+/* What a layer applies to its q, k, v before they are stored or used. */
+typedef struct kq_kv_transform {
+    const uint16_t *Pq; /* device [head_dim, head_dim] bf16: P_k^-T (may be NULL when no q is given) */
+    const uint16_t *Pk; /* device [head_dim, head_dim] bf16                                       */
+    const uint16_t *Pv; /* device [head_dim, head_dim] bf16; all three 16-byte aligned            */
+    float alpha_k;      /* clip ratios in [2^-19, 1]                                              */
+    float alpha_v;
+    const float *rope;      /* device [rope_positions, rope_dim] fp32, 16-byte aligned: the cosines of
+                               a position's rope_dim / 2 angles, then their sines; NULL: no rotation  */
+    int64_t rope_positions; /* rows of that table                                                 */
+    int rope_dim;           /* rotated leading elements of a row: a multiple of 16 up to head_dim */
+    int rope_interleaved;   /* 0: element i turns with i + rope_dim / 2; else 2i with 2i + 1      */
+} kq_kv_transform;
+
+/*
+ * kq_kv_append -- for T new tokens: rotate the queries and keys by their
+ * positions, multiply every head's row by its factor, write the queries out in
+ * bf16 and store keys and values as INT4 rows at their slots.
+ *
+ *     q_out = R(pos) q Pq,  y = R(pos) k Pk  or  v Pv,
+ *     s = alpha max|y| / 7,  code = clamp(round_half_even(y / s), -8, 7)
+ *
+ * The rotation is not rounded before the product.  Codes are those of exact
+ * arithmetic: rows with a value too near a rounding border for fp32 are redone
+ * in fp64.
+ *
+ * cache     the pages; written only at the slots given.
+ * tf        factors, clip ratios, rotary table.
+ * q         device bf16 rows [T][q_heads, head_dim], q_stride elements from one
+ *           token to the next (a multiple of 8, at least q_heads * head_dim);
+ *           NULL with q_heads = 0.  k, v: the same with the cache's kv_heads.
+ *           So q, k and v may be parts of one packed projection.  All 16-byte
+ *           aligned.
+ * positions [T] device int32 rows of the rotary table; may be NULL without one.
+ * slots     [T] device int64.  A negative slot marks a padding token: its keys
+ *           and values are not stored (its queries are still written).  The
+ *           slots of one call are distinct, or which token's row stays is not
+ *           defined, and codes and scale may come from different ones.
+ * q_out     [T, q_heads, head_dim] device bf16, dense, 16-byte aligned, written;
+ *           must not overlap any input.
+ * T         0 is a no-op; T * (q_heads + kv_heads) < 2^31.
+ * A slot past the last page, or a position outside the table, is never followed:
+ * nothing of that token is stored (and, for a bad position, its queries are
+ * written as zeros), and kq_device_error reports 65536.
+ * A row with a NaN or an infinity gets unspecified codes, in that row alone.
+ * Returns KQ_ERR_SHAPE, KQ_ERR_UNSUPPORTED (head_dim, page_size, rope_dim, an
+ * alpha below 2^-19), KQ_ERR_NULL, KQ_ERR_ALIGN, KQ_ERR_ARG (alpha outside
+ * (0, 1], a stride too short, overlapping buffers), KQ_ERR_CUDA.  Asynchronous
+ * on `stream`; allocates nothing; can be captured into a graph.
+ */
+kq_status kq_kv_append(const kq_kv_cache *cache, const kq_kv_transform *tf, const uint16_t *q, int64_t q_stride,
+                       const uint16_t *k, int64_t k_stride, const uint16_t *v, int64_t v_stride,
+                       const int32_t *positions, const int64_t *slots, uint16_t *q_out, int64_t T, int q_heads,
+                       kq_stream_t stream);
+
+/*
+ * kq_kv_gather -- the rows at T slots as the values they stand for: k_out and
+ * v_out [T, kv_heads, head_dim] device bf16, 16-byte aligned, code * s rounded
+ * once (for handing cached tokens to another program, and for checks).  A
+ * negative slot gives zeros; a slot past the last page too, and kq_device_error
+ * then reports 65536.  Slots may repeat.  Outputs must not overlap the cache,
+ * the slots or one another.  Asynchronous on `stream`; allocates nothing.
+ */
+kq_status kq_kv_gather(const kq_kv_cache *cache, const int64_t *slots, uint16_t *k_out, uint16_t *v_out, int64_t T,
+                       kq_stream_t stream);
+
+/*
+ * kq_kv_attention -- softmax attention of B sequences over their pages.
+ *
+ * Sequence b has n = kv_len[b] keys, key t in page page_table[b][t / page_size],
+ * and the queries of tokens q_start[b] .. q_start[b + 1] - 1; these are its last
+ * m = q_start[b + 1] - q_start[b] positions, so query i sees the keys t with
+ * t <= n - m + i and, with a window w > 0, t > n - m + i - w.  For query head h
+ * and key head h / (q_heads / kv_heads), with k_t, v_t the values of the rows:
+ *
+ *     x_t = scale q.k_t, or softcap tanh(scale q.k_t / softcap) with softcap > 0
+ *     lse = log sum_t exp(x_t),  out = sum_t exp(x_t - lse) v_t
+ *
+ * A query that sees no key gets out = 0 and lse = -infinity.
+ *
+ * q           [T, q_heads, head_dim] device bf16, 16-byte aligned (kq_kv_append's
+ *             q_out).
+ * q_start     [B + 1] device int32, ascending from 0; NULL: one query per
+ *             sequence (T = B).  Rows of q past q_start[B] are padding: their
+ *             rows of out and lse stay as they were.
+ * page_table  [B, max_pages] device int32.  Only the entries of pages that a
+ *             query sees are read (the rest may hold anything).
+ * kv_len      [B] device int32 (below 0 counts as 0).
+ * scale       finite; softcap finite and >= 0 (0: none); window >= 0 (0: none).
+ * out         [T, q_heads, head_dim] device bf16, 16-byte aligned, written.
+ * lse         [T, q_heads] device fp32, written, or NULL.
+ * workspace   device scratch of kq_kv_attention_workspace_bytes(...) bytes,
+ *             16-byte aligned, overwritten; it needs no initial contents and is
+ *             free again once the work on `stream` has finished.  Two calls that
+ *             may run at the same time (other streams, other graphs) need one each.
+ * max_q       an upper bound of m, at least 1.  Queries past it are not computed
+ *             (their rows stay as they were) and kq_device_error reports 131072.
+ * A page number outside the cache, or a kv_len past the table, is never followed:
+ * such keys count as masked and kq_device_error reports 131072.
+ * Sizes: T, B >= 0 (0 is a no-op), q_heads a multiple of kv_heads with at most
+ * 1024 heads, T * q_heads < 2^31, max_pages * page_size < 2^31.
+ * Scores and softmax sums are fp32, and the products' accumulators too.  The same
+ * inputs give the same bits.  Nothing is read back to the host: sequences may
+ * grow between replays of a captured graph.
+ * Returns KQ_ERR_SHAPE, KQ_ERR_UNSUPPORTED (head_dim, page_size), KQ_ERR_NULL,
+ * KQ_ERR_ALIGN, KQ_ERR_ARG (scale, softcap, window, max_q, workspace too small,
+ * overlapping buffers), KQ_ERR_CUDA.  Asynchronous on `stream`.
+ */
+kq_status kq_kv_attention(const kq_kv_cache *cache, const uint16_t *q, const int32_t *q_start,
+                          const int32_t *page_table, int64_t max_pages, const int32_t *kv_len, float scale,
+                          float softcap, int window, uint16_t *out, float *lse, void *workspace,
+                          uint64_t workspace_bytes, int64_t T, int64_t B, int q_heads, int max_q,
+                          kq_stream_t stream);
+
+/*
+ * kq_kv_attention_shared -- kq_kv_attention for sequences that all begin with
+ * the same prefix_len keys (one system prompt, one problem sampled many times):
+ * the prefix is read and multiplied once for the queries of all sequences, and
+ * joined with each sequence's own keys.
+ *
+ * prefix_pages [ceil(prefix_len / page_size)] device int32: the prefix's pages.
+ * prefix_len   host; 0 is kq_kv_attention.
+ * kv_len and page_table describe the keys after the prefix: key t of sequence b
+ * is at position prefix_len + t.  Every query sees the whole prefix, except that
+ * a window counts over both: query i of m, at p = prefix_len + n - m + i, sees
+ * the positions above p - window.
+ * Everything else as kq_kv_attention (same workspace size).
+ */
+kq_status kq_kv_attention_shared(const kq_kv_cache *cache, const uint16_t *q, const int32_t *q_start,
+                                 const int32_t *prefix_pages, int64_t prefix_len, const int32_t *page_table,
+                                 int64_t max_pages, const int32_t *kv_len, float scale, float softcap, int window,
+                                 uint16_t *out, float *lse, void *workspace, uint64_t workspace_bytes, int64_t T,
+                                 int64_t B, int q_heads, int max_q, kq_stream_t stream);
+
+/* Workspace bytes of the two calls above (0 for sizes they refuse). */
+uint64_t kq_kv_attention_workspace_bytes(int64_t T, int64_t B, int q_heads, int kv_heads, int head_dim, int max_q);
+
+/*
  * kq_device_error -- read and clear the device-side status word that the
  * kernels set when a bounded wait gives up (they then skip their remaining
  * work instead of hanging).  Synchronises `stream`.  *code receives 0 when
- * no wait timed out since the last call, else a nonzero site code.
+ * no wait timed out and no index was refused since the last call, else the sum
+ * of the site codes (65536 and 131072: the cache's calls, see there).
  * Returns KQ_ERR_NULL for a NULL code, KQ_ERR_CUDA if the read fails.
  */
 kq_status kq_device_error(kq_stream_t stream, int *code);

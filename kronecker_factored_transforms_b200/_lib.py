@@ -30,6 +30,18 @@ class KQError(RuntimeError):
         self.status = status
 
 
+class _KVCacheStruct(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int)]
+
+
+class _KVTransformStruct(ctypes.Structure):
+    _fields_ = [("Pq", ctypes.c_void_p), ("Pk", ctypes.c_void_p), ("Pv", ctypes.c_void_p),
+                ("alpha_k", ctypes.c_float), ("alpha_v", ctypes.c_float), ("rope", ctypes.c_void_p),
+                ("rope_positions", ctypes.c_int64), ("rope_dim", ctypes.c_int), ("rope_interleaved", ctypes.c_int)]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError("libkq.so not built at %s; run __graft_entry__.build() "
@@ -47,6 +59,15 @@ def _load() -> ctypes.CDLL:
     lib.kq_transform_quant_two_stage.argtypes = [P, P, P, P, F32, P, P, P, ctypes.c_uint64, I64, I32, I32, P]
     lib.kq_transform_quant_two_stage_static.argtypes = [P, P, P, P, F32, P, P, I64, I32, I32, P]
     lib.kq_headwise_transform_quant_nvfp4.argtypes = [P, P, P, P, P, I64, I32, I32, P]
+    lib.kq_kv_append.argtypes = [P, P, P, I64, P, I64, P, I64, P, P, P, I64, I32, P]
+    lib.kq_kv_gather.argtypes = [P, P, P, P, I64, P]
+    lib.kq_kv_attention.argtypes = [P, P, P, P, I64, P, F32, F32, I32, P, P, P, ctypes.c_uint64, I64, I64, I32, I32, P]
+    lib.kq_kv_attention_shared.argtypes = [P, P, P, P, I64, P, I64, P, F32, F32, I32, P, P, P, ctypes.c_uint64, I64,
+                                           I64, I32, I32, P]
+    lib.kq_kv_attention_workspace_bytes.argtypes = [I64, I64, I32, I32, I32, I32]
+    lib.kq_kv_attention_workspace_bytes.restype = ctypes.c_uint64
+    for f in (lib.kq_kv_append, lib.kq_kv_gather, lib.kq_kv_attention, lib.kq_kv_attention_shared):
+        f.restype = ctypes.c_int
     for f in (lib.kq_transform_quant, lib.kq_transform, lib.kq_dequant_inverse, lib.kq_device_error,
               lib.kq_selftest_bounded_wait, lib.kq_w4a4_gemm, lib.kq_w4a4_gemm_bf16, lib.kq_headwise_transform_quant,
               lib.kq_transform_quant_two_stage, lib.kq_transform_quant_two_stage_static,
@@ -71,7 +92,9 @@ EXPORTED = ("kq_transform_quant", "kq_transform", "kq_dequant_inverse", "kq_devi
             "kq_selftest_bounded_wait", "kq_status_string", "kq_kernel_name", "kq_kernel_for", "kq_version", "kq_w4a4_gemm",
             "kq_w4a4_gemm_bf16",
             "kq_headwise_transform_quant", "kq_transform_quant_two_stage", "kq_two_stage_workspace_bytes",
-            "kq_transform_quant_two_stage_static", "kq_headwise_transform_quant_nvfp4")
+            "kq_transform_quant_two_stage_static", "kq_headwise_transform_quant_nvfp4",
+            "kq_kv_append", "kq_kv_gather", "kq_kv_attention", "kq_kv_attention_shared",
+            "kq_kv_attention_workspace_bytes")
 
 STATIC_WORKSPACE_BYTES = 64 * 1024 * 1024
 
@@ -149,6 +172,101 @@ def kq_w4a4_gemm_bf16(qx, sx, qw, sw, y, M: int, N: int, K: int, stream=None) ->
     _check("kq_w4a4_gemm_bf16",
            lib.kq_w4a4_gemm_bf16(_ptr(qx), _ptr(sx), _ptr(qw), _ptr(sw), _ptr(y), int(M), int(N), int(K),
                                  _stream(stream)))
+
+
+class _Handle:
+    """A C struct the caller fills in once: its address, and the tensors it points into."""
+
+    def __init__(self, struct, tensors):
+        self._struct = struct
+        self._tensors = [t for t in tensors if t is not None]  # kept alive with the handle
+        self.ptr = ctypes.addressof(struct)
+        devices = {t.device for t in self._tensors}
+        if len(devices) != 1 or next(iter(devices)).type != "cuda":
+            raise ValueError("the tensors of a handle lie on one CUDA device, got %s" % sorted(map(str, devices)))
+        if not all(t.is_contiguous() for t in self._tensors):
+            raise ValueError("the tensors of a handle are contiguous")
+        self.device = next(iter(devices)).index
+
+
+def kv_cache(k_codes, k_scale, v_codes, v_scale) -> _Handle:
+    """The kq_kv_cache of four tensors: codes [pages, kv_heads, page_size, head_dim / 2] uint8 and
+    scales [pages, kv_heads, page_size] fp32, for keys and for values."""
+    import torch
+    if k_codes.dim() != 4 or k_codes.shape != v_codes.shape or k_codes.dtype != torch.uint8 \
+            or v_codes.dtype != torch.uint8:
+        raise ValueError("k_codes and v_codes are uint8 [pages, kv_heads, page_size, head_dim / 2]")
+    pages, heads, page, half = k_codes.shape
+    for s in (k_scale, v_scale):
+        if tuple(s.shape) != (pages, heads, page) or s.dtype != torch.float32:
+            raise ValueError("k_scale and v_scale are float32 [pages, kv_heads, page_size]")
+    st = _KVCacheStruct(k_codes.data_ptr(), k_scale.data_ptr(), v_codes.data_ptr(), v_scale.data_ptr(), pages, page,
+                        heads, 2 * half)
+    return _Handle(st, [k_codes, k_scale, v_codes, v_scale])
+
+
+def kv_transform(Pq, Pk, Pv, alpha_k: float, alpha_v: float, rope=None, interleaved: bool = False) -> _Handle:
+    """The kq_kv_transform of bf16 factors [head_dim, head_dim] (as bf16 or 16-bit integer tensors; Pq may be None)
+    and a rotary table fp32 [positions, rotated elements] (cosines, then sines) or None."""
+    import torch
+    for P in (Pq, Pk, Pv):
+        if P is not None and (P.shape != Pk.shape or P.dim() != 2 or P.shape[0] != P.shape[1] or P.element_size() != 2):
+            raise ValueError("the factors are square matrices of one size, in bf16")
+    if rope is not None and (rope.dim() != 2 or rope.dtype != torch.float32):
+        raise ValueError("the rotary table is float32 [positions, rotated elements]")
+    n, r = (0, 0) if rope is None else rope.shape
+    st = _KVTransformStruct(_ptr(Pq), _ptr(Pk), _ptr(Pv), float(alpha_k), float(alpha_v), _ptr(rope), n, r,
+                            int(bool(interleaved)))
+    return _Handle(st, [Pq, Pk, Pv, rope])
+
+
+def _on_device(fn: str, cache, call, *tensors) -> None:
+    """Calls with the cache's device current (the C entries work on the current one); the tensors lie there too."""
+    import torch
+    for t in tensors:
+        if t is not None and not isinstance(t, int) and t.get_device() != cache.device:
+            raise ValueError("%s: a tensor on %s, the cache on cuda:%d" % (fn, t.device, cache.device))
+    if torch.cuda.current_device() == cache.device:
+        _check(fn, call())
+    else:
+        with torch.cuda.device(cache.device):
+            _check(fn, call())
+
+
+def kq_kv_append(cache, tf, q, q_stride: int, k, k_stride: int, v, v_stride: int, positions, slots, q_out, T: int,
+                 q_heads: int, stream=None) -> None:
+    _on_device("kq_kv_append", cache, lambda: lib.kq_kv_append(
+        cache.ptr, tf.ptr, _ptr(q), int(q_stride), _ptr(k), int(k_stride), _ptr(v), int(v_stride), _ptr(positions),
+        _ptr(slots), _ptr(q_out), int(T), int(q_heads), _stream(stream)), q, k, v, positions, slots, q_out)
+
+
+def kq_kv_gather(cache, slots, k_out, v_out, T: int, stream=None) -> None:
+    _on_device("kq_kv_gather", cache, lambda: lib.kq_kv_gather(
+        cache.ptr, _ptr(slots), _ptr(k_out), _ptr(v_out), int(T), _stream(stream)), slots, k_out, v_out)
+
+
+def kq_kv_attention_workspace_bytes(T: int, B: int, q_heads: int, kv_heads: int, head_dim: int, max_q: int) -> int:
+    return int(lib.kq_kv_attention_workspace_bytes(int(T), int(B), int(q_heads), int(kv_heads), int(head_dim),
+                                                   int(max_q)))
+
+
+def kq_kv_attention(cache, q, q_start, page_table, max_pages: int, kv_len, scale: float, softcap: float, window: int,
+                    out, lse, workspace, workspace_bytes: int, T: int, B: int, q_heads: int, max_q: int,
+                    stream=None) -> None:
+    _on_device("kq_kv_attention", cache, lambda: lib.kq_kv_attention(
+        cache.ptr, _ptr(q), _ptr(q_start), _ptr(page_table), int(max_pages), _ptr(kv_len), float(scale),
+        float(softcap), int(window), _ptr(out), _ptr(lse), _ptr(workspace), int(workspace_bytes), int(T), int(B),
+        int(q_heads), int(max_q), _stream(stream)), q, q_start, page_table, kv_len, out, lse, workspace)
+
+
+def kq_kv_attention_shared(cache, q, q_start, prefix_pages, prefix_len: int, page_table, max_pages: int, kv_len,
+                           scale: float, softcap: float, window: int, out, lse, workspace, workspace_bytes: int,
+                           T: int, B: int, q_heads: int, max_q: int, stream=None) -> None:
+    _on_device("kq_kv_attention_shared", cache, lambda: lib.kq_kv_attention_shared(
+        cache.ptr, _ptr(q), _ptr(q_start), _ptr(prefix_pages), int(prefix_len), _ptr(page_table), int(max_pages),
+        _ptr(kv_len), float(scale), float(softcap), int(window), _ptr(out), _ptr(lse), _ptr(workspace),
+        int(workspace_bytes), int(T), int(B), int(q_heads), int(max_q), _stream(stream)),
+        q, q_start, prefix_pages, page_table, kv_len, out, lse, workspace)
 
 
 def kq_transform(x, P1, P2, cinv, y_out, T: int, n1: int, n2: int, stream=None) -> None:

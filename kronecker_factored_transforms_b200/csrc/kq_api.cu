@@ -345,6 +345,242 @@ kq_status kq_transform_quant_two_stage_static(const uint16_t *x, const uint16_t 
                                         n1, n2, stream);
 }
 
+// ---- the quantised key / value cache --------------------------------------------
+namespace {
+
+int log2_page(int page_size) {
+    for (int s = 4; s <= 8; ++s)
+        if (page_size == 1 << s) return s;
+    return -1;
+}
+
+// The cache's description, checked: sizes, then support, then pointers.
+kq_status check_cache(const kq_kv_cache *c) {
+    if (!c) return KQ_ERR_NULL;
+    if (c->num_pages < 1 || c->num_pages > INT32_MAX || c->kv_heads < 1 || c->kv_heads > 1024 || c->head_dim < 1 ||
+        c->page_size < 1)
+        return KQ_ERR_SHAPE;
+    if ((c->head_dim != 64 && c->head_dim != 128) || log2_page(c->page_size) < 0) return KQ_ERR_UNSUPPORTED;
+    if (!c->k_codes || !c->k_scale || !c->v_codes || !c->v_scale) return KQ_ERR_NULL;
+    if (!aligned(c->k_codes, 16) || !aligned(c->k_scale, 16) || !aligned(c->v_codes, 16) || !aligned(c->v_scale, 16))
+        return KQ_ERR_ALIGN;
+    return KQ_OK;
+}
+
+struct CacheRanges {
+    Range r[4];
+};
+CacheRanges cache_ranges(const kq_kv_cache *c) {
+    const uint64_t rows = uint64_t(c->num_pages) * uint64_t(c->kv_heads) * uint64_t(c->page_size);
+    const uint64_t codes = rows * uint64_t(c->head_dim / 2);
+    return CacheRanges{{range_of(c->k_codes, codes), range_of(c->k_scale, rows * 4), range_of(c->v_codes, codes),
+                        range_of(c->v_scale, rows * 4)}};
+}
+
+kq::KvCache cache_view(const kq_kv_cache *c) {
+    return kq::KvCache{c->k_codes, c->k_scale, c->v_codes, c->v_scale, c->num_pages, log2_page(c->page_size),
+                       c->kv_heads, c->head_dim};
+}
+
+bool any_overlap(const Range *a, int na, const Range *b, int nb) {
+    for (int i = 0; i < na; ++i)
+        for (int j = 0; j < nb; ++j)
+            if (overlap(a[i], b[j])) return true;
+    return false;
+}
+
+// [T] rows of `width` elements, `stride` elements apart.
+Range rows_range(const void *p, int64_t T, int64_t stride, int64_t width) {
+    return range_of(p, p ? (uint64_t(T - 1) * uint64_t(stride) + uint64_t(width)) * 2 : 0);
+}
+
+}  // namespace
+
+kq_status kq_kv_append(const kq_kv_cache *cache, const kq_kv_transform *tf, const uint16_t *q, int64_t q_stride,
+                       const uint16_t *k, int64_t k_stride, const uint16_t *v, int64_t v_stride,
+                       const int32_t *positions, const int64_t *slots, uint16_t *q_out, int64_t T, int q_heads,
+                       kq_stream_t stream) {
+    if (T < 0 || q_heads < 0 || q_heads > 1024) return KQ_ERR_SHAPE;
+    if (T == 0) return KQ_OK;
+    kq_status st = check_cache(cache);
+    if (st != KQ_OK) return st;
+    if (!tf) return KQ_ERR_NULL;
+    const int D = cache->head_dim, Hk = cache->kv_heads;
+    if (T >= (int64_t(1) << 31) / (q_heads + Hk)) return KQ_ERR_SHAPE;
+    if (check_alpha(tf->alpha_k) != KQ_OK || check_alpha(tf->alpha_v) != KQ_OK) return KQ_ERR_ARG;
+    if (!(tf->alpha_k >= 0x1p-19f) || !(tf->alpha_v >= 0x1p-19f)) return KQ_ERR_UNSUPPORTED;
+    if (tf->rope) {
+        if (tf->rope_positions < 1 || tf->rope_positions > INT32_MAX || tf->rope_dim < 1 || tf->rope_dim > D)
+            return KQ_ERR_SHAPE;
+        if (tf->rope_dim % 16 != 0) return KQ_ERR_UNSUPPORTED;
+    }
+    if (!k || !v || !slots || !tf->Pk || !tf->Pv || (tf->rope && !positions)) return KQ_ERR_NULL;
+    if (q_heads > 0 && (!q || !q_out || !tf->Pq)) return KQ_ERR_NULL;
+    const int64_t wq = int64_t(q_heads) * D, wk = int64_t(Hk) * D, kMaxStride = int64_t(1) << 31;
+    if (k_stride < wk || v_stride < wk || k_stride > kMaxStride || v_stride > kMaxStride) return KQ_ERR_ARG;
+    if (q_heads > 0 && (q_stride < wq || q_stride > kMaxStride)) return KQ_ERR_ARG;
+    if (!aligned(k, 16) || !aligned(v, 16) || k_stride % 8 != 0 || v_stride % 8 != 0 || !aligned(tf->Pk, 16) ||
+        !aligned(tf->Pv, 16) || !aligned(slots, 8) || (tf->rope && (!aligned(tf->rope, 16) || !aligned(positions, 4))))
+        return KQ_ERR_ALIGN;
+    if (q_heads > 0 && (!aligned(q, 16) || !aligned(q_out, 16) || q_stride % 8 != 0 || !aligned(tf->Pq, 16)))
+        return KQ_ERR_ALIGN;
+    const uint64_t DD = uint64_t(D) * D * 2;
+    const Range in[9] = {rows_range(q_heads > 0 ? q : nullptr, T, q_stride, wq),
+                         rows_range(k, T, k_stride, wk),
+                         rows_range(v, T, v_stride, wk),
+                         range_of(tf->Pk, DD),
+                         range_of(tf->Pv, DD),
+                         range_of(q_heads > 0 ? tf->Pq : nullptr, q_heads > 0 ? DD : 0),
+                         range_of(tf->rope, tf->rope ? uint64_t(tf->rope_positions) * uint64_t(tf->rope_dim) * 4 : 0),
+                         range_of(positions, tf->rope ? uint64_t(T) * 4 : 0),
+                         range_of(slots, uint64_t(T) * 8)};
+    const CacheRanges cr = cache_ranges(cache);
+    const Range out[5] = {cr.r[0], cr.r[1], cr.r[2], cr.r[3],
+                          range_of(q_heads > 0 ? q_out : nullptr, q_heads > 0 ? uint64_t(T) * uint64_t(wq) * 2 : 0)};
+    if (any_overlap(in, 9, out, 5)) return KQ_ERR_ARG;
+    for (int i = 0; i < 5; ++i)
+        if (any_overlap(out + i, 1, out + i + 1, 4 - i)) return KQ_ERR_ARG;
+    DeviceInfo info;
+    if ((st = device_info(info)) != KQ_OK) return st;
+    kq::KvAppendArgs a;
+    a.c = cache_view(cache);
+    a.Pq = tf->Pq;
+    a.Pk = tf->Pk;
+    a.Pv = tf->Pv;
+    a.alpha_k = tf->alpha_k;
+    a.alpha_v = tf->alpha_v;
+    a.rope = tf->rope;
+    a.rope_positions = tf->rope_positions;
+    a.rope_dim = tf->rope ? tf->rope_dim : 0;
+    a.rope_interleaved = tf->rope_interleaved != 0;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.positions = positions;
+    a.slots = slots;
+    a.q_out = q_out;
+    a.T = T;
+    a.q_heads = q_heads;
+    if (kq::device_error_word(info.device, &a.err) != cudaSuccess) return KQ_ERR_CUDA;
+    cudaError_t err = kq::launch_kv_append(a, info.num_sms, info.device, reinterpret_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? KQ_OK : KQ_ERR_CUDA;
+}
+
+kq_status kq_kv_gather(const kq_kv_cache *cache, const int64_t *slots, uint16_t *k_out, uint16_t *v_out, int64_t T,
+                       kq_stream_t stream) {
+    if (T < 0) return KQ_ERR_SHAPE;
+    if (T == 0) return KQ_OK;
+    kq_status st = check_cache(cache);
+    if (st != KQ_OK) return st;
+    if (T >= (int64_t(1) << 31) / cache->kv_heads) return KQ_ERR_SHAPE;
+    if (!slots || !k_out || !v_out) return KQ_ERR_NULL;
+    if (!aligned(slots, 8) || !aligned(k_out, 16) || !aligned(v_out, 16)) return KQ_ERR_ALIGN;
+    const CacheRanges cr = cache_ranges(cache);
+    const Range in[5] = {cr.r[0], cr.r[1], cr.r[2], cr.r[3], range_of(slots, uint64_t(T) * 8)};
+    const uint64_t bytes = uint64_t(T) * uint64_t(cache->kv_heads) * uint64_t(cache->head_dim) * 2;
+    const Range out[2] = {range_of(k_out, bytes), range_of(v_out, bytes)};
+    if (any_overlap(in, 5, out, 2) || overlap(out[0], out[1])) return KQ_ERR_ARG;
+    DeviceInfo info;
+    if ((st = device_info(info)) != KQ_OK) return st;
+    unsigned int *err_word = nullptr;
+    if (kq::device_error_word(info.device, &err_word) != cudaSuccess) return KQ_ERR_CUDA;
+    cudaError_t err = kq::launch_kv_gather(cache_view(cache), slots, k_out, v_out, T, err_word,
+                                           reinterpret_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? KQ_OK : KQ_ERR_CUDA;
+}
+
+namespace {
+kq_status kv_attention(const kq_kv_cache *cache, const uint16_t *q, const int32_t *q_start,
+                       const int32_t *prefix_pages, int64_t prefix_len, const int32_t *page_table, int64_t max_pages,
+                       const int32_t *kv_len, float scale, float softcap, int window, uint16_t *out, float *lse,
+                       void *workspace, uint64_t workspace_bytes, int64_t T, int64_t B, int q_heads, int max_q,
+                       kq_stream_t stream) {
+    if (T < 0 || B < 0 || q_heads < 1 || q_heads > 1024 || prefix_len < 0 || max_pages < 1) return KQ_ERR_SHAPE;
+    if (T == 0 || B == 0) return KQ_OK;
+    kq_status st = check_cache(cache);
+    if (st != KQ_OK) return st;
+    if (q_heads % cache->kv_heads != 0 || T >= (int64_t(1) << 31) / q_heads || B > T || B > 65535 ||
+        (!q_start && T != B) || max_pages >= (int64_t(1) << 31) / cache->page_size ||
+        prefix_len >= (int64_t(1) << 30) || max_pages > INT64_MAX / (4 * B))
+        return KQ_ERR_SHAPE;
+    if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.0f || window < 0 || max_q < 1)
+        return KQ_ERR_ARG;
+    if (!q || !page_table || !kv_len || !out || !workspace || (prefix_len > 0 && !prefix_pages)) return KQ_ERR_NULL;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16) || !aligned(page_table, 4) ||
+        !aligned(kv_len, 4) || (q_start && !aligned(q_start, 4)) || (lse && !aligned(lse, 4)) ||
+        (prefix_len > 0 && !aligned(prefix_pages, 4)))
+        return KQ_ERR_ALIGN;
+    if (!q_start) max_q = 1;
+    if (max_q > T) max_q = int(T);
+    const uint64_t need =
+        kq::kv_attention_workspace_bytes(T, B, q_heads, cache->kv_heads, cache->head_dim, max_q);
+    if (workspace_bytes < need) return KQ_ERR_ARG;
+    const uint64_t rows = uint64_t(T) * uint64_t(q_heads);
+    const CacheRanges cr = cache_ranges(cache);
+    const uint64_t ppages = (uint64_t(prefix_len) + uint64_t(cache->page_size) - 1) / uint64_t(cache->page_size);
+    const Range in[9] = {cr.r[0], cr.r[1], cr.r[2], cr.r[3], range_of(q, rows * uint64_t(cache->head_dim) * 2),
+                         range_of(page_table, uint64_t(B) * uint64_t(max_pages) * 4),
+                         range_of(kv_len, uint64_t(B) * 4),
+                         range_of(q_start, q_start ? (uint64_t(B) + 1) * 4 : 0),
+                         range_of(prefix_pages, ppages * 4)};
+    const Range res[3] = {range_of(out, rows * uint64_t(cache->head_dim) * 2), range_of(lse, lse ? rows * 4 : 0),
+                          range_of(workspace, need)};
+    if (any_overlap(in, 9, res, 3) || any_overlap(res, 1, res + 1, 2) || overlap(res[1], res[2])) return KQ_ERR_ARG;
+    DeviceInfo info;
+    if ((st = device_info(info)) != KQ_OK) return st;
+    kq::KvAttnArgs a;
+    a.c = cache_view(cache);
+    a.q = q;
+    a.q_start = q_start;
+    a.prefix_pages = prefix_len > 0 ? prefix_pages : nullptr;
+    a.prefix_len = prefix_len;
+    a.page_table = page_table;
+    a.max_pages = max_pages;
+    a.kv_len = kv_len;
+    a.scale = scale;
+    a.softcap = softcap;
+    a.window = window;
+    a.out = out;
+    a.lse = lse;
+    a.workspace = static_cast<unsigned char *>(workspace);
+    a.T = T;
+    a.B = B;
+    a.q_heads = q_heads;
+    a.max_q = max_q;
+    if (kq::device_error_word(info.device, &a.err) != cudaSuccess) return KQ_ERR_CUDA;
+    cudaError_t err = kq::launch_kv_attention(a, info.num_sms, info.device, reinterpret_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? KQ_OK : KQ_ERR_CUDA;
+}
+}  // namespace
+
+kq_status kq_kv_attention(const kq_kv_cache *cache, const uint16_t *q, const int32_t *q_start,
+                          const int32_t *page_table, int64_t max_pages, const int32_t *kv_len, float scale,
+                          float softcap, int window, uint16_t *out, float *lse, void *workspace,
+                          uint64_t workspace_bytes, int64_t T, int64_t B, int q_heads, int max_q,
+                          kq_stream_t stream) {
+    return kv_attention(cache, q, q_start, nullptr, 0, page_table, max_pages, kv_len, scale, softcap, window, out, lse,
+                        workspace, workspace_bytes, T, B, q_heads, max_q, stream);
+}
+
+kq_status kq_kv_attention_shared(const kq_kv_cache *cache, const uint16_t *q, const int32_t *q_start,
+                                 const int32_t *prefix_pages, int64_t prefix_len, const int32_t *page_table,
+                                 int64_t max_pages, const int32_t *kv_len, float scale, float softcap, int window,
+                                 uint16_t *out, float *lse, void *workspace, uint64_t workspace_bytes, int64_t T,
+                                 int64_t B, int q_heads, int max_q, kq_stream_t stream) {
+    return kv_attention(cache, q, q_start, prefix_pages, prefix_len, page_table, max_pages, kv_len, scale, softcap,
+                        window, out, lse, workspace, workspace_bytes, T, B, q_heads, max_q, stream);
+}
+
+uint64_t kq_kv_attention_workspace_bytes(int64_t T, int64_t B, int q_heads, int kv_heads, int head_dim, int max_q) {
+    if (T <= 0 || B <= 0 || q_heads < 1 || q_heads > 1024 || kv_heads < 1 || q_heads % kv_heads != 0 || max_q < 1 ||
+        (head_dim != 64 && head_dim != 128) || T >= (int64_t(1) << 31) / q_heads)
+        return 0;
+    return kq::kv_attention_workspace_bytes(T, B, q_heads, kv_heads, head_dim, int(max_q > T ? T : max_q));
+}
+
 kq_status kq_device_error(kq_stream_t stream, int *code) {
     if (!code) return KQ_ERR_NULL;
     unsigned int v = 0;
@@ -368,9 +604,10 @@ const char *kq_status_string(int status) {
     case KQ_ERR_SHAPE: return "bad shape (T < 0, n1 <= 0, n2 <= 0 or size overflow)";
     case KQ_ERR_UNSUPPORTED:
         return "unsupported size or parameter for this entry (factors: multiples of 16 up to 128, or up to 256 for "
-               "the two-stage entries; head_dim 64 or 128; alpha of at least 2^-19 where the entry requires it)";
+               "the two-stage entries; head_dim 64 or 128; pages of 16 to 256 rows; rotated elements a multiple of 16; alpha of at least 2^-19 where the entry requires it)";
     case KQ_ERR_ALIGN: return "misaligned pointer";
-    case KQ_ERR_ARG: return "bad argument (alpha outside (0, 1] or outputs overlap inputs)";
+    case KQ_ERR_ARG: return "bad argument (alpha outside (0, 1], a scale, bound or stride out of range, a workspace too small, or "
+                            "outputs overlap inputs)";
     case KQ_ERR_CUDA: return "CUDA runtime error";
     case KQ_ERR_TIMEOUT: return "a bounded wait inside a kernel timed out";
     default: return "unknown status";

@@ -75,4 +75,63 @@ cudaError_t launch_two_stage(const LaunchArgs &a, void *workspace);
 constexpr uint64_t kStaticScratchBytes = uint64_t(64) << 20;
 cudaError_t static_scratch(int device, void **ptr);
 
+// ---- the quantised key / value cache ------------------------------------------
+
+// Pages of INT4 rows (see kq_kv_cache in kq.h), as the kernels take them.
+struct KvCache {
+    uint8_t *k_codes;
+    float *k_scale;
+    uint8_t *v_codes;
+    float *v_scale;
+    int64_t pages;
+    int page_shift;  // log2 of the page size
+    int heads;
+    int D;
+};
+
+struct KvAppendArgs {
+    KvCache c;
+    const uint16_t *Pq, *Pk, *Pv;
+    float alpha_k, alpha_v;
+    const float *rope;  // nullptr: no rotation
+    int64_t rope_positions;
+    int rope_dim;
+    int rope_interleaved;
+    const uint16_t *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    const int32_t *positions;
+    const int64_t *slots;
+    uint16_t *q_out;
+    int64_t T;
+    int q_heads;
+    unsigned int *err;  // device status word
+};
+cudaError_t launch_kv_append(const KvAppendArgs &a, int num_sms, int device, cudaStream_t stream);
+cudaError_t launch_kv_gather(const KvCache &c, const int64_t *slots, uint16_t *k_out, uint16_t *v_out, int64_t T,
+                             unsigned int *err, cudaStream_t stream);
+
+struct KvAttnArgs {
+    KvCache c;
+    const uint16_t *q;
+    const int32_t *q_start;       // nullptr: one query per sequence
+    const int32_t *prefix_pages;  // nullptr: no shared prefix
+    int64_t prefix_len;
+    const int32_t *page_table;
+    int64_t max_pages;
+    const int32_t *kv_len;
+    float scale, softcap;
+    int window;  // 0: none
+    uint16_t *out;
+    float *lse;  // may be nullptr
+    unsigned char *workspace;
+    int64_t T, B;
+    int q_heads, max_q;
+    unsigned int *err;
+};
+uint64_t kv_attention_workspace_bytes(int64_t T, int64_t B, int q_heads, int kv_heads, int head_dim, int max_q);
+cudaError_t launch_kv_attention(const KvAttnArgs &a, int num_sms, int device, cudaStream_t stream);
+
+// Site codes of the status word for indexes that are not followed.
+enum : unsigned { kSiteKvAppend = 65536u, kSiteKvAttention = 131072u };
+
 }  // namespace kq

@@ -54,3 +54,23 @@ def weight_transform_quant(W, F1, F2, c, alpha: float, q_out, scale_out, n1: int
     q_out [N_out, n/2] uint8, scale_out [N_out] fp32, all device tensors."""
     from . import _lib
     _lib.kq_transform_quant(W, F1, F2, c, alpha, q_out, scale_out, W.shape[0], n1, n2, stream=stream)
+
+
+def query_factor_bf16(Pk_bits: np.ndarray) -> np.ndarray:
+    """bf16 bit patterns of Pk^-T, the factor of the queries that meet keys stored as k Pk:
+    (q Pk^-T).(k Pk) = q.k.  The inverse is that of the bf16 factor the keys use."""
+    Pk = workloads.bf16_bits_to_f32(Pk_bits).astype(np.float64)
+    return workloads.f32_to_bf16_bits(svd_inverse(Pk).T.astype(np.float32))
+
+
+def fold_value_factor(Wo: np.ndarray, Pv_bits: np.ndarray) -> np.ndarray:
+    """The output projection that takes attention over values stored as v Pv.
+
+    Wo [n_out, q_heads * head_dim] multiplies the concatenated heads o; with values in the basis of Pv the
+    attention gives o Pv per head, and Wo' = Wo Pv^-T per head (columns of a head) restores Wo o.  fp64."""
+    Pv = workloads.bf16_bits_to_f32(Pv_bits).astype(np.float64)
+    Wo = np.asarray(Wo, dtype=np.float64)
+    D = Pv.shape[0]
+    if Wo.ndim != 2 or Wo.shape[1] % D != 0:
+        raise ValueError("Wo is [n_out, heads * %d], got %s" % (D, Wo.shape))
+    return (Wo.reshape(Wo.shape[0], -1, D) @ svd_inverse(Pv).T).reshape(Wo.shape)

@@ -1,0 +1,446 @@
+"""kq_kv_attention and kq_kv_attention_shared against their 64-bit forms."""
+import math
+
+import pytest
+import torch
+
+from kv_testutil import attention, check_attention
+
+pytestmark = pytest.mark.gpu
+CODES = torch.tensor([-8, -7, -5, -4, -3, -2, -1, -1, 0, 0, 1, 2, 3, 4, 5, 7])
+
+
+@pytest.fixture(scope="module")
+def kq():
+    from kronecker_factored_transforms_b200 import _lib
+    return _lib
+
+
+def make(keys, nqs, G, Hk, D, page, seed, prefix=0, q_std=1.5, spare=2, scale_mid=0.3, scale_spread=0.25, mean=0.0):
+    """Pools with NaN scales everywhere that no key lies, page tables in any order with
+    out-of-range numbers behind the used entries, padded rows behind the last sequence."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    B, T = len(keys), sum(nqs)
+    need = [(n + page - 1) // page for n in keys]
+    pre = (prefix + page - 1) // page
+    total = sum(need) + pre + spare
+    perm = torch.randperm(total, generator=g, device="cuda").cpu()
+    lut = (CODES & 15).to(torch.uint8).cuda()
+    pool = []
+    used = torch.zeros(total, page, dtype=torch.bool)
+    tables, at = [], 0
+    for n, k in zip(keys, need):
+        tables.append(perm[at:at + k].tolist())
+        for j, p in enumerate(tables[-1]):
+            used[p, :min(page, n - j * page)] = True
+        at += k
+    prefix_pages = perm[at:at + pre].tolist()
+    for j, p in enumerate(prefix_pages):
+        used[p, :min(page, prefix - j * page)] = True
+    hide = ~used.cuda()[:, None, :].expand(total, Hk, page)
+    for _ in range(2):
+        idx = torch.randint(0, 256, (total, Hk, page, D // 2), generator=g, device="cuda", dtype=torch.int32)
+        pool.append(lut[idx >> 4] << 4 | lut[idx & 15])
+        sc = scale_mid * torch.exp(scale_spread * torch.randn(total, Hk, page, generator=g, device="cuda"))
+        sc[hide] = float("nan")
+        pool.append(sc)
+    width = max(1, max(need)) + 1
+    table = torch.full((B, width), 0x7FFFFFF0, dtype=torch.int32)
+    for b, t in enumerate(tables):
+        table[b, :len(t)] = torch.tensor(t, dtype=torch.int32)
+    q = (mean + q_std * torch.randn(T + 3, G * Hk, D, generator=g, device="cuda")).to(torch.bfloat16)
+    q[T:] = float("nan")
+    return dict(keys=list(keys), nqs=list(nqs), G=G, Hk=Hk, D=D, page=page, B=B, T=T, pool=pool, tables=tables,
+                table=table.cuda(), width=width, q=q, prefix=prefix,
+                prefix_pages=torch.tensor(prefix_pages + [-9], dtype=torch.int32).cuda(), prefix_list=prefix_pages,
+                kv_len=torch.tensor(keys, dtype=torch.int32).cuda(),
+                q_start=torch.tensor([0] + list(nqs)).cumsum(0).to(torch.int32).cuda(),
+                scale=1.0 / math.sqrt(D))
+
+
+def launch(kq, s, softcap=0.0, window=0, lse=True, q_start=True, max_q=None, out=None, workspace=None, T=None,
+           shared=None, stream=None):
+    H, T = s["G"] * s["Hk"], s["T"] + 3 if T is None else T
+    max_q = max(max_q or 0, max(s["nqs"]))
+    s["cache"] = kq.kv_cache(*s["pool"])
+    if out is None:
+        out = torch.full((s["T"] + 3, H, s["D"]), 5.0, dtype=torch.bfloat16, device="cuda")
+    l = torch.full((s["T"] + 3, H), 6.0, device="cuda") if lse else None
+    n = kq.kq_kv_attention_workspace_bytes(T, s["B"], H, s["Hk"], s["D"], max_q)
+    if workspace is None:  # no initial contents are needed: every byte set, as NaN and huge integers
+        workspace = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
+    qs = s["q_start"] if q_start else None
+    if shared is None:
+        shared = s["prefix"] > 0
+    if shared:
+        kq.kq_kv_attention_shared(s["cache"], s["q"], qs, s["prefix_pages"], s["prefix"], s["table"], s["width"],
+                                  s["kv_len"], s["scale"], softcap, window, out, l, workspace, n, T, s["B"], H, max_q,
+                                  stream=stream)
+    else:
+        kq.kq_kv_attention(s["cache"], s["q"], qs, s["table"], s["width"], s["kv_len"], s["scale"], softcap, window,
+                           out, l, workspace, n, T, s["B"], H, max_q, stream=stream)
+    return out, l
+
+
+def verify(kq, s, softcap=0.0, window=0, **kw):
+    out, lse = launch(kq, s, softcap, window, **kw)
+    torch.cuda.synchronize()
+    T = s["T"]
+    assert (out[T:] == 5.0).all() and (lse is None or (lse[T:] == 6.0).all()), "rows behind the last sequence"
+    ref = attention(s["q"][:T], s["pool"], s["tables"], s["keys"], s["nqs"], s["scale"], softcap, window,
+                    (s["prefix_list"], s["prefix"]) if s["prefix"] else None)
+    check_attention(out[:T], None if lse is None else lse[:T], ref)
+    assert kq.kq_device_error() == 0
+    return out, lse
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G", [1, 2, 3, 5, 8, 12, 16, 24])
+def test_single_tokens_of_every_group_size(kq, D, G):
+    keys = [1, 2, 15, 16, 17, 0, 63, 64, 65, 127, 128, 129, 300, 1000]
+    verify(kq, make(keys, [1] * len(keys), G, 2, D, 16, 100 * G + D))
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+def test_page_sizes(kq, page):
+    verify(kq, make([5, 255, 256, 257, 700], [1] * 5, 4, 3, 128, page, page))
+
+
+@pytest.mark.parametrize("keys", [[1], [16], [1531], [4096], [33333], [0], [0, 0, 0], [9000, 1, 1, 1, 1, 1, 0, 40]])
+def test_lengths(kq, keys):
+    verify(kq, make(keys, [1] * len(keys), 4, 8, 128, 16, sum(keys)))
+
+
+def test_long_context(kq):
+    verify(kq, make([131072 + 5, 70001], [1, 1], 4, 2, 128, 64, 3, q_std=0.7))
+
+
+def test_many_sequences(kq):
+    keys = [(i * 37) % 211 for i in range(700)]
+    verify(kq, make(keys, [1] * 700, 2, 1, 64, 16, 4))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G,nqs,keys", [
+    (1, [2, 3, 1, 5, 4], [2, 100, 1, 5, 333]), (4, [5, 1, 2, 4], [700, 64, 2, 4]), (8, [2, 2, 1], [50, 2, 129]),
+    (3, [8, 7, 1, 2], [9, 500, 0, 2]), (2, [16, 9, 0, 1], [77, 12, 30, 5]), (16, [1, 4, 2], [10, 400, 3])])
+def test_a_few_queries(kq, D, G, nqs, keys):
+    verify(kq, make(keys, nqs, G, 2, D, 32, 10 * G + D))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G,nqs,keys", [
+    (1, [200], [200]), (4, [129, 64], [129, 1000]), (8, [33, 100, 1], [4000, 100, 7]), (3, [170], [555]),
+    (16, [40, 41], [41, 41]), (7, [300], [1700]), (2, [1, 400, 0, 30], [900, 401, 10, 31])])
+def test_chunks_of_prompts(kq, D, G, nqs, keys):
+    verify(kq, make(keys, nqs, G, 2, D, 16, 10 * G + D + 1))
+
+
+@pytest.mark.parametrize("nqs,keys", [([4, 3], [2, 0]), ([1, 20], [0, 5]), ([200], [150]), ([64, 64], [0, 1])])
+def test_more_queries_than_keys(kq, nqs, keys):
+    """The first queries see nothing: zeros and -infinity."""
+    verify(kq, make(keys, nqs, 4, 2, 128, 16, 8))
+
+
+@pytest.mark.parametrize("window", [1, 7, 16, 64, 100, 1000, 100000])
+def test_windows(kq, window):
+    verify(kq, make([1, 17, 100, 700, 1500], [1] * 5, 4, 2, 128, 16, window), window=window)
+    verify(kq, make([50, 17, 100, 700], [3, 5, 1, 4], 2, 2, 64, 32, window), window=window)
+    verify(kq, make([150, 900], [150, 200], 4, 2, 128, 16, window), window=window)
+
+
+@pytest.mark.parametrize("softcap", [0.5, 5.0, 30.0])
+def test_capped_scores(kq, softcap):
+    verify(kq, make([1, 17, 100, 700], [1] * 4, 4, 2, 128, 16, 5, q_std=6.0), softcap=softcap)
+    verify(kq, make([150, 900], [150, 200], 4, 2, 64, 16, 6, q_std=6.0), softcap=softcap, window=90)
+
+
+def test_scores_far_apart(kq):
+    """Scores of hundreds: one key takes all the weight; and the largest score last or first."""
+    for seed, keys, nqs in ((1, [400, 37], [1, 1]), (2, [300, 64], [130, 64])):
+        s = make(keys, nqs, 4, 2, 128, 16, seed, q_std=40.0, scale_spread=1.0)
+        verify(kq, s)
+
+
+@pytest.mark.parametrize("mid", [1e-12, 1e-4, 1e3, 1e8])
+def test_value_scales_of_any_size(kq, mid):
+    s = make([300, 20, 1], [1, 1, 1], 4, 2, 128, 16, 9)
+    s["pool"][3] *= mid
+    verify(kq, s)
+    s = make([300, 90], [70, 90], 4, 2, 128, 16, 9)
+    s["pool"][3] *= mid
+    verify(kq, s)
+
+
+def test_scales_that_differ_by_magnitudes_and_zero_rows(kq):
+    for nqs in ([1, 1, 1], [80, 64, 33]):
+        s = make([300, 64, 33], nqs, 4, 2, 128, 16, 10, scale_spread=3.0, q_std=0.05)
+        s["pool"][3][:, :, 3::7] = 0  # rows that were all zero when they were stored
+        s["pool"][1][:, :, 2::5] = 0
+        s["pool"][2][:, :, 3::7] = 0
+        verify(kq, s)
+    s = make([40], [1], 4, 2, 128, 16, 11)
+    s["pool"][3].zero_()
+    s["pool"][2].zero_()
+    verify(kq, s)
+
+
+def test_queries_with_a_mean(kq):
+    """All elements of a query of one sign: sums over the codes that do not cancel."""
+    verify(kq, make([700, 64], [1, 1], 8, 2, 128, 16, 12, mean=3.0, q_std=0.1))
+    verify(kq, make([700], [100], 8, 2, 128, 16, 13, mean=3.0, q_std=0.1))
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1e20])
+def test_queries_of_any_size(kq, scale):
+    """The softmax scale undoes the size of the queries."""
+    for nqs in ([1, 1], [70, 90]):
+        s = make([300, 90], nqs, 4, 2, 128, 16, 14)
+        s["q"] = (s["q"].double() * scale).to(torch.bfloat16)
+        s["scale"] = s["scale"] / scale
+        verify(kq, s)
+
+
+def test_zero_scale_and_negative_scale(kq):
+    for nqs in ([1, 1], [70, 90]):
+        for f in (0.0, -1.0):
+            s = make([300, 90], nqs, 4, 2, 128, 16, 15)
+            s["scale"] *= f
+            verify(kq, s)
+
+
+def test_optional_arguments(kq):
+    s = make([50, 0, 17, 300], [1] * 4, 4, 2, 128, 16, 16)
+    a, _ = verify(kq, s, lse=False)
+    b, _ = verify(kq, s, max_q=7)  # a loose bound
+    out, lse = launch(kq, s, q_start=False, T=4)
+    torch.cuda.synchronize()
+    check_attention(out[:4], lse[:4], attention(s["q"][:4], s["pool"], s["tables"], s["keys"], s["nqs"], s["scale"]))
+    s = make([150, 90], [150, 20], 4, 2, 128, 16, 17)
+    verify(kq, s, lse=False, max_q=153)
+
+
+def test_negative_lengths_count_as_zero(kq):
+    s = make([50, 0], [1, 1], 4, 2, 128, 16, 18)
+    s["kv_len"][1] = -5
+    verify(kq, s)
+
+
+@pytest.mark.parametrize("nqs", [[1, 1, 1], [66, 70, 5]])
+def test_refused_indexes_are_masked(kq, nqs):
+    """Page numbers outside the cache, lengths past the table: those keys do not count, and the status says so."""
+    s = make([200, 100, 300], nqs, 4, 2, 128, 16, 19)
+    s["table"][0, 3] = s["pool"][0].shape[0]
+    s["table"][2, 0] = -1
+    s["table"][2, 18] = 0x7FFFFFFF
+    out, lse = launch(kq, s)
+    torch.cuda.synchronize()
+    assert kq.kq_device_error() == 131072
+    assert torch.isfinite(out[:s["T"]].float()).all()
+    ok = s["q_start"][1:3].tolist()
+    t = make([200, 100, 300], nqs, 4, 2, 128, 16, 19)
+    ref = attention(t["q"][:t["T"]], t["pool"], t["tables"], t["keys"], t["nqs"], t["scale"])
+    check_attention(out[ok[0]:ok[1]], lse[ok[0]:ok[1]], tuple(r[ok[0]:ok[1]] for r in ref))
+    s = make([20], [nqs[0]], 4, 2, 128, 16, 20)
+    s["kv_len"][0] = 10 ** 6
+    s["table"][:] = s["tables"][0][0]
+    s["pool"][1][torch.isnan(s["pool"][1])] = 1.0
+    s["pool"][3][torch.isnan(s["pool"][3])] = 1.0
+    out, _ = launch(kq, s)
+    torch.cuda.synchronize()
+    assert kq.kq_device_error() == 131072 and torch.isfinite(out[:s["T"]].float()).all()
+
+
+def test_queries_past_the_bound_stay(kq):
+    s = make([200, 100], [3, 1], 4, 2, 128, 16, 21)
+    H = 8
+    cache = kq.kv_cache(*s["pool"])
+    n = kq.kq_kv_attention_workspace_bytes(4, 2, H, 2, 128, 2)
+    out = torch.full((4, H, 128), 5.0, dtype=torch.bfloat16, device="cuda")
+    kq.kq_kv_attention(cache, s["q"], s["q_start"], s["table"], s["width"], s["kv_len"], s["scale"], 0.0, 0, out, None,
+                       torch.empty(n, dtype=torch.uint8, device="cuda"), n, 4, 2, H, 2)
+    torch.cuda.synchronize()
+    assert kq.kq_device_error() == 131072
+    ref = attention(s["q"][:4], s["pool"], s["tables"], s["keys"], s["nqs"], s["scale"])
+    keep = [0, 1, 3]
+    check_attention(out[keep], None, tuple(r[keep] for r in ref))
+    assert (out[2] == 5.0).all()
+
+
+# ---- a shared prefix ------------------------------------------------------------------
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G,Hk,B,prefix", [(1, 3, 2, 1), (4, 2, 8, 100), (8, 1, 3, 1000), (8, 2, 40, 515), (1, 4, 150, 300),
+                                           (16, 1, 9, 64), (5, 2, 31, 129)])
+def test_shared_prefix(kq, D, G, Hk, B, prefix):
+    keys = [(i * 53) % 190 for i in range(B)]  # the first has no key of its own
+    verify(kq, make(keys, [1] * B, G, Hk, D, 16, B + D + G, prefix=prefix))
+
+
+@pytest.mark.parametrize("G,nqs,keys,prefix", [(4, [2, 1, 3], [5, 1, 300], 77), (2, [40, 1, 0, 9], [40, 0, 3, 200], 400),
+                                               (8, [100, 30], [100, 500], 1500), (1, [3, 2], [1, 0], 33)])
+def test_shared_prefix_with_several_queries(kq, G, nqs, keys, prefix):
+    verify(kq, make(keys, nqs, G, 2, 128, 32, prefix, prefix=prefix))
+
+
+@pytest.mark.parametrize("window", [1, 60, 200, 700])
+def test_shared_prefix_windows_and_caps(kq, window):
+    verify(kq, make([5, 0, 130, 500], [1, 1, 1, 1], 4, 2, 128, 16, window, prefix=450), window=window, softcap=20.0)
+    verify(kq, make([5, 0, 130, 500] * 12, [1, 2, 1, 1] * 12, 4, 2, 64, 16, window, prefix=450), window=window)
+
+
+def test_prefix_of_length_zero_and_equal_results(kq):
+    s = make([50, 0, 17, 300], [1] * 4, 4, 2, 128, 16, 22)
+    a, la = verify(kq, s)
+    b, lb = verify(kq, s, shared=True)
+    assert torch.equal(a, b) and torch.equal(la, lb)
+
+
+def test_shared_prefix_long(kq):
+    verify(kq, make([20, 300, 77, 0], [1, 1, 1, 1], 8, 2, 128, 16, 23, prefix=20000))
+    verify(kq, make([20 + i for i in range(64)], [1] * 64, 8, 1, 128, 64, 24, prefix=9001))
+
+
+def test_refused_prefix_pages(kq):
+    s = make([5, 30], [1, 1], 4, 2, 128, 16, 25, prefix=200)
+    s["prefix_pages"][4] = -1
+    out, _ = launch(kq, s)
+    torch.cuda.synchronize()
+    assert kq.kq_device_error() == 131072 and torch.isfinite(out[:2].float()).all()
+
+
+# ---- streams, graphs, order -----------------------------------------------------------
+
+CASES = [dict(keys=[900, 33, 0, 410], nqs=[1] * 4, prefix=0), dict(keys=[700, 300], nqs=[90, 150], prefix=0),
+         dict(keys=[20, 33, 0, 300] * 10, nqs=[1] * 40, prefix=600)]
+
+
+@pytest.mark.parametrize("case", CASES)
+def test_same_inputs_same_bits(kq, case):
+    s = make(G=8, Hk=2, D=128, page=16, seed=30, **case)
+    first = launch(kq, s)
+    for _ in range(20):
+        again = launch(kq, s)
+        assert torch.equal(first[0][:s["T"]], again[0][:s["T"]]) and torch.equal(first[1], again[1])
+
+
+@pytest.mark.parametrize("case", CASES)
+def test_two_streams_at_once(kq, case):
+    sets = [make(G=8, Hk=2, D=128, page=16, seed=31 + i, **case) for i in range(2)]
+    want = [launch(kq, s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    n = kq.kq_kv_attention_workspace_bytes(sets[0]["T"] + 3, sets[0]["B"], 16, 2, 128, max(case["nqs"]))
+    ws = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in sets]
+    outs = [torch.zeros_like(want[0][0]) for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, st, w, o in zip(sets, streams, ws, outs):
+            launch(kq, s, lse=False, out=o, workspace=w, stream=st)
+    torch.cuda.synchronize()
+    for o, w, s in zip(outs, want, sets):
+        assert torch.equal(o[:s["T"]], w[0][:s["T"]])
+
+
+@pytest.mark.parametrize("case", CASES)
+def test_captured_call_follows_growing_sequences(kq, case):
+    """A captured call replayed with other lengths, pages and queries, and a second graph on the same workspace."""
+    s = make(G=8, Hk=2, D=128, page=16, seed=40, **case)
+    t = make([max(0, k - 15 - i % 3) if m == 1 else k for i, (k, m) in enumerate(zip(s["keys"], s["nqs"]))], s["nqs"],
+             8, 2, 128, 16, 41, prefix=case["prefix"])
+    n = kq.kq_kv_attention_workspace_bytes(s["T"] + 3, s["B"], 16, 2, 128, max(case["nqs"]))
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    want = [launch(kq, x)[0] for x in (s, t)]
+    out = torch.zeros_like(want[0])
+    graphs = []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            launch(kq, s, lse=False, out=out, workspace=ws)
+        graphs.append(graph)
+    for k, x in enumerate((s, t, s)):
+        if x is t:
+            s["keep"] = [y.clone() for y in (s["q"], s["kv_len"], s["table"], s["prefix_pages"], *s["pool"])]
+            w = min(s["width"], t["width"])
+            s["q"].copy_(t["q"])
+            s["kv_len"].copy_(t["kv_len"])
+            s["table"][:, :w] = t["table"][:, :w]
+            s["prefix_pages"].copy_(t["prefix_pages"])
+            for a, b in zip(s["pool"], t["pool"]):
+                a[:b.shape[0]] = b
+        elif k == 2:
+            for y, z in zip((s["q"], s["kv_len"], s["table"], s["prefix_pages"], *s["pool"]), s["keep"]):
+                y.copy_(z)
+        out.zero_()
+        graphs[k % 2].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out[:s["T"]], want[1 if x is t else 0][:s["T"]]), k
+
+
+def test_pages_past_32_bits(kq):
+    D, Hk, page, G = 128, 8, 256, 4
+    s = make([700, 33], [1, 1], G, Hk, D, page, 50)
+    want = launch(kq, s)
+    s3 = make([700], [90], G, Hk, D, page, 51)
+    want3 = launch(kq, s3)
+    pages = 2 ** 32 // (Hk * page * 64) + 40
+    big = [torch.empty(pages, Hk, page, D // 2, dtype=torch.uint8, device="cuda"), torch.empty(pages, Hk, page, device="cuda"),
+           torch.empty(pages, Hk, page, D // 2, dtype=torch.uint8, device="cuda"), torch.empty(pages, Hk, page, device="cuda")]
+    for x, w in ((s, want), (s3, want3)):
+        k = x["pool"][0].shape[0]
+        for a, b in zip(big, x["pool"]):
+            a[pages - k:] = b
+        y = dict(x, pool=big, table=x["table"] + (pages - k))
+        y["table"][x["table"] > 10 ** 6] = -1
+        got = launch(kq, y)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0][:x["T"]], w[0][:x["T"]]) and torch.equal(got[1], w[1])
+
+
+def test_append_then_attend(kq):
+    """The calls in the order of use, with no synchronisation between them: prompt, then single tokens, each
+    appended and attended to, then a batch behind the prompt as a shared prefix; against the 64-bit form over the
+    rows that the cache holds, and against attention over the unquantised tokens to INT4's accuracy."""
+    from test_kv_append_gpu import append, make as make_tokens
+    H, Hk, D, page, T = 16, 4, 128, 16, 333
+    p = make_tokens(T, H, Hk, D, page, 128, 60, extra_pages=30)
+    order = torch.randperm(p["pool"][0].shape[0])
+    table = order[:28].to(torch.int32).cuda()[None].contiguous()
+    place = lambda a, b: (table[0, torch.arange(a, b, device="cuda") // page].long() * page
+                          + torch.arange(a, b, device="cuda") % page)
+    p["positions"] = torch.arange(T, device="cuda", dtype=torch.int32)
+    p["slots"] = place(0, T)
+    scale = 1.0 / math.sqrt(D)
+    calls = []
+
+    def attend(tok, n, m):
+        ws = torch.empty(kq.kq_kv_attention_workspace_bytes(m, 1, H, Hk, D, m), dtype=torch.uint8, device="cuda")
+        out = torch.empty(m, H, D, dtype=torch.bfloat16, device="cuda")
+        kq.kq_kv_attention(tok["cache"], tok["q_out"], torch.tensor([0, m], dtype=torch.int32, device="cuda"), table, 28,
+                           torch.tensor([n], dtype=torch.int32, device="cuda"), scale, 0.0, 0, out, None, ws, ws.numel(),
+                           m, 1, H, m)
+        calls.append((out, tok, n, m))
+
+    append(kq, p)
+    attend(p, T, T)
+    for j in range(3):
+        d = make_tokens(1, H, Hk, D, page, 128, 61 + j)
+        d.update(pool=p["pool"], slots=place(T + j, T + j + 1), Pq=p["Pq"], Pk=p["Pk"], Pv=p["Pv"], table=p["table"],
+                 positions=torch.tensor([T + j], dtype=torch.int32, device="cuda"))
+        append(kq, d)
+        attend(d, T + j + 1, 1)
+    torch.cuda.synchronize()
+    pages = table[0].tolist()
+    for out, tok, n, m in calls:
+        # rows appended later lie past n, so the final cache serves every call's reference
+        check_attention(out, None, attention(tok["q_out"][:m], p["pool"], [pages], [n], [m], scale))
+    # the prompt alone, unquantised: R q.R k over the tokens themselves
+    from kv_testutil import rotate
+    ang = p["table"][p["positions"].long()].double()
+    q, k = rotate(p["q"].double(), ang, 128, False), rotate(p["k"].double(), ang, 128, False)
+    v = p["v"].double() @ p["Pv"].double()
+    x = torch.einsum("qhd,khd->hqk", q, k.repeat_interleave(H // Hk, 1)) * scale
+    x = x.masked_fill(torch.ones(T, T, device="cuda").triu(1).bool(), -math.inf)
+    full = torch.einsum("hqk,khd->qhd", torch.softmax(x, -1), v.repeat_interleave(H // Hk, 1))
+    err = float((calls[0][0].double() - full).norm() / full.norm())
+    assert err < 0.5, err  # INT4 keys with one large channel and INT4 values: a tenth to a quarter; nonsense is above 1
