@@ -216,7 +216,8 @@ def prepare(case, seed):
         from kronecker_factored_transforms_b200 import _lib as kq
         s["cache"] = kq.kv_cache(*s["pool"])
         if case["kind"] == "append":
-            s["transform"] = kq.kv_transform(s["Pq"], s["Pk"], s["Pv"], case["alpha"], case["alpha"], rope=s["table"],
+            factors = [s[name].contiguous() for name in ("Pq", "Pk", "Pv")]
+            s["transform"] = kq.kv_transform(*factors, case["alpha"], case["alpha"], rope=s["table"],
                                              interleaved=case["inter"])
         else:
             n = kq.kq_kv_attention_workspace_bytes(s["T"], case["B"], H, Hk, D, s["max_q"])
