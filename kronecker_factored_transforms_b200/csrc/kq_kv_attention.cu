@@ -1,118 +1,780 @@
 // kq_kv_attention.cu -- softmax attention over the pages of the INT4 key / value
-// cache, behind a prefix that all sequences share or none.
+// cache (kq_kv_attention, kq_kv_attention_shared).
+//
+// For a query row q (one token, one head) and the keys t that it sees, with c_t
+// and s_t the codes and scales of the cache's rows:
+//
+//     x_t = scale s_t (q . c_t), capped by a tanh where asked,
+//     out = sum_t exp(x_t) s'_t c'_t / sum_t exp(x_t),   lse = log sum_t exp(x_t)
+//
+// The scales never meet the codes: s_t multiplies a score, s'_t a weight.  So the
+// matrix products run on the codes themselves, which 16-bit floats hold exactly.
+//
+// The row kernel (kq_kv_rows_kernel) serves few query rows per key head (one token
+// of each sequence, with its group of heads; a few drafted tokens).  There the
+// bytes of the cache bound it: head_dim / 2 + 4 for 4 head_dim flops per row of
+// queries.  Its products run in the warps' own mma (m16n8k16): 16 keys are the M
+// side, 8 rows of queries the N side, so that one group of heads fills the tile,
+// which a 128-row tcgen05 tile would leave 15/16 empty, and the codes go from
+// shared memory straight into the registers of the A operand:
+//   - a 16-bit word (w ^ 0x8) & 0xf is code + 8 as a subnormal fp16 (times 2^-24),
+//     so two codes cost one LOP3; codes in the next nibble come out times 16.
+//   - scores: the + 8 is taken back by starting the accumulator at -8 sum(q), the
+//     factors 16 and 2^24 by the query operand and the score's multiplier.  The query
+//     row is brought to fp16 by a power of two: exact, as bf16 has 8 bits.
+//   - values: here the + 8 is taken off every code (one HFMA2 for two), because
+//     weights all have one sign: 8 sum(p) would outgrow sum(p c) in the sum.
+//   - the order of head_dim within the products is free, so a lane takes 16
+//     consecutive bytes of a key row, and 8 of a value row, as they lie.
+// Weights go to fp16 as 2^(x + log2 s' - r): relative to a running reference r that
+// follows the maximum of x + log2 s', so they keep 11 bits whatever the scales'
+// size, with r moved only when a weight would pass 2^14 (rounded to 2^6 under it).
+// The sum of exp(x) is fp32 with unrounded terms.
+//
+// Work is split evenly: the (sequence, key head, row tile) units are laid in a row,
+// 64 keys a chunk, and every block takes the same number of chunks wherever that
+// cuts; its four warps take 16 keys of each chunk, each with its own ring of
+// cp.async stages and its own softmax state, joined at a unit's end.  A unit cut
+// by block borders leaves partial rows in the workspace, at most two per block,
+// which kq_kv_combine_kernel joins in a fixed order.
+#include <cuda_fp16.h>
+
+#include <mutex>
+
 #include "kq_common.cuh"
 #include "kq_internal.h"
 
 namespace kq {
 namespace {
 
-constexpr int S_THREADS = 128;
+constexpr int CH = 64;          // keys per chunk
+constexpr int WARPS = 4;        // warps per block, 16 keys of a chunk each
+constexpr int R_THREADS = 32 * WARPS;
+constexpr int STAGES = 4;       // cp.async stages per warp
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNone = -1e30f;  // reference of a row that has seen no key
+static_assert(CH == 16 * WARPS, "a chunk is one step of every warp");
 
-// One query row and head per block: a thread per key for the scores, a thread per
-// output element for the values, 128 keys at a time with a running maximum and sum.
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// tanh as 1 - 2 / (e^2z + 1): off by about 2^-22, absolutely.
+__device__ __forceinline__ float tanh_exp(float z) {
+    return 1.0f - __fdividef(2.0f, ex2(z * (2.0f * kLog2e)) + 1.0f);
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+    uint32_t d;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t *>(&v);
+}
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+// Codes of nibbles 0 and 4 (lo) and 1 and 5 (hi, times 16) of a word, plus 8, times 2^-24, as fp16 pairs.
+__device__ __forceinline__ uint32_t nib_lo(uint32_t w) { return (w ^ 0x88888888u) & 0x000f000fu; }
+__device__ __forceinline__ uint32_t nib_hi(uint32_t w) { return (w ^ 0x88888888u) & 0x00f000f0u; }
+
+// ---- which keys and rows a unit has ---------------------------------------------
+
+// The launch as both kernels see it.  "Sequence" B, where there is a shared prefix,
+// is the prefix with the queries of all sequences.
+struct Plan {
+    KvAttnArgs a;
+    int G;             // query heads per key head
+    int shared;        // a prefix is there
+    int ctas;          // blocks of the row kernel
+    int64_t *cum;      // [B + 1 (+ 1)] chunks before a sequence, in the workspace
+    float *slot_o;     // [ctas][2][R][D] partial rows: a block's first unit, its last unit
+    float *slot_l;     // [ctas][2][R]
+    float *whole_o;    // [2][T * H][D] rows whose keys lay in one block (own keys; the prefix's)
+    float *whole_l;    // [2][T * H]
+};
+
+struct Seq {
+    int n;         // keys
+    int m;         // queries that are computed
+    int q0;        // first query token
+    int shift;     // query i sees the keys t <= shift + i
+    int c0, N;     // first chunk, chunks
+    int tiles;     // row tiles
+    const int32_t *pages;
+};
+
+// First query token and number of queries of sequence b, within the T tokens whatever q_start holds.
+__device__ __forceinline__ void queries_of(const KvAttnArgs &a, int64_t b, int &q0, int &m) {
+    q0 = int(b);
+    m = 1;
+    if (a.q_start) {
+        const int T = int(a.T);
+        q0 = min(max(a.q_start[b], 0), T);
+        m = max(min(a.q_start[b + 1], T) - q0, 0);
+    }
+}
+__device__ __forceinline__ int all_queries(const KvAttnArgs &a) {
+    return a.q_start ? min(max(a.q_start[a.B], 0), int(a.T)) : int(a.T);
+}
+
+template <int R>
+__device__ __forceinline__ Seq load_seq(const Plan &p, int64_t b, bool report) {
+    const KvAttnArgs &a = p.a;
+    Seq s;
+    int lo = 0;
+    if (b == a.B) {  // the shared prefix: every row sees all of it, but for a window
+        s.n = int(a.prefix_len);
+        s.q0 = 0;
+        s.m = all_queries(a);
+        s.shift = s.n;
+        s.pages = a.prefix_pages;
+    } else {
+        int m;
+        queries_of(a, b, s.q0, m);
+        const int given = max(a.kv_len[b], 0);
+        const int most = int(a.max_pages) << a.c.page_shift;
+        s.n = min(given, most);
+        s.m = min(m, a.max_q);
+        if (report && (given > most || m > a.max_q)) atomicOr(a.err, kSiteKvAttention);
+        s.shift = given - m;
+        s.pages = a.page_table + b * a.max_pages;
+        if (a.window) lo = max(0, s.shift - a.window + 1);
+    }
+    const int hi = min(s.n, max(0, s.shift + s.m));
+    s.c0 = min(lo, max(hi - 1, 0)) / CH;
+    s.N = max(1, (hi + CH - 1) / CH - s.c0);  // a unit without keys still has its rows to write
+    s.tiles = (s.m * p.G + R - 1) / R;
+    return s;
+}
+
+// A walk over the chunks of a block: sequence, head, row tile, chunk.
+template <int R>
+struct Walk {
+    int64_t b;
+    int h, tile, c;
+    Seq s;
+    __device__ __forceinline__ void next(const Plan &p, int64_t seqs) {
+        if (++c < s.c0 + s.N) return;
+        if (++tile == s.tiles) {
+            tile = 0;
+            if (++h == p.a.c.heads) {
+                h = 0;
+                do {
+                    if (++b >= seqs) return;
+                    s = load_seq<R>(p, b, false);
+                } while (s.tiles == 0);
+            }
+        }
+        c = s.c0;
+    }
+};
+
+// Position of token t's queries among the keys of its sequence (for windows over a prefix).
+__device__ __forceinline__ int query_shift(const KvAttnArgs &a, int t) {
+    if (!a.q_start) return a.kv_len[t] > 0 ? a.kv_len[t] - 1 : -1;
+    int lo = 0, hi = int(a.B);
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (a.q_start[mid + 1] <= t) lo = mid + 1;
+        else hi = mid;
+    }
+    if (lo == int(a.B)) return -1;
+    return max(a.kv_len[lo], 0) - (a.q_start[lo + 1] - a.q_start[lo]) + t - a.q_start[lo];
+}
+
+// ---- the row kernel ----------------------------------------------------------------
+
+template <int D, int NT>
+struct RCfg {
+    static constexpr int R = 8 * NT;              // query rows per tile
+    static constexpr int KB = 16 * D / 2;         // a step's key codes: 16 rows
+    static constexpr int STAGE = 2 * KB + 128;    // keys, values, 16 scales of each
+    static constexpr int RING = STAGES * STAGE;
+    static constexpr int PART = R * (D + 2) * 4;  // a warp's rows when a unit ends: values, reference, sum
+    static constexpr int OFF_PART = WARPS * RING;
+    static constexpr int OFF_SCAN = OFF_PART + WARPS * PART;
+    static constexpr int SMEM = OFF_SCAN + 16 * WARPS;
+    static constexpr int OCC = NT == 1 ? 4 : 3;   // blocks per SM
+    static_assert((SMEM + 1024) * OCC <= 227 * 1024, "shared memory of the resident blocks");
+};
+
+// The place of 16-byte piece q of value row r in a stage.  A lane reads 8 (or 4) bytes of
+// the rows 2c, 2c + 1, 2c + 8, 2c + 9: even rows first, and pieces exchanged in every
+// second pair of rows, so that a read's rows lie in different banks.
 template <int D>
-__global__ void __launch_bounds__(S_THREADS) kq_kv_attention_kernel(const __grid_constant__ KvAttnArgs a) {
-    __shared__ float qs[D], ps[S_THREADS], red[8];
-    __shared__ int64_t row_of[S_THREADS];
-    const int tid = threadIdx.x, H = a.q_heads, Hk = a.c.heads;
+__device__ __forceinline__ uint32_t value_place(int r, int q) {
+    const int p = (r >> 1) | ((r & 1) << 3);
+    return D == 128 ? uint32_t(p * 64 + ((q ^ (p & 2)) << 4)) : uint32_t(p * 32 + (q << 4));
+}
+
+template <int D, int NT, bool CAP>
+__global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel(const __grid_constant__ Plan p) {
+    using C = RCfg<D, NT>;
+    constexpr int R = C::R, KS = D / 16, W = D / 32;  // k steps; words of a lane's part of a key row
+    extern __shared__ __align__(128) unsigned char smem[];
+    const KvAttnArgs &a = p.a;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    const int Hk = a.c.heads, H = a.q_heads, psh = a.c.page_shift;
+    const int64_t seqs = a.B + p.shared;
+    int64_t *scan = reinterpret_cast<int64_t *>(smem + C::OFF_SCAN);  // [4] warp sums, [4] found walk
     griddep_wait();
     griddep_launch_dependents();
-    const int h = int(blockIdx.x % H), kh = h / (H / Hk);
-    const int64_t t = blockIdx.x / H;
+
+    // ---- the block's share: chunks [w0, w1) of all ----
+    const int64_t per = (seqs + R_THREADS - 1) / R_THREADS, s0 = min(per * tid, seqs), s1 = min(s0 + per, seqs);
+    int64_t mine = 0;
+    for (int64_t b = s0; b < s1; ++b) {
+        const Seq s = load_seq<R>(p, b, blockIdx.x == 0);
+        mine += int64_t(s.tiles) * s.N;
+    }
+    mine *= Hk;
+    int64_t before = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += v;
+    }
+    if (lane == 31) scan[warp] = before;
+    __syncthreads();
+    int64_t total = 0;
+    before -= mine;
+    for (int w = 0; w < WARPS; ++w) {
+        if (w < warp) before += scan[w];
+        total += scan[w];
+    }
+    __syncthreads();
+    // no more shares than chunks: every share has one, so a unit's blocks are consecutive
+    const int64_t shares = min(int64_t(p.ctas), total);
+    if (blockIdx.x == 0) {  // for the combining kernel
+        int64_t at = before;
+        for (int64_t b = s0; b < s1; ++b) {
+            const Seq s = load_seq<R>(p, b, false);
+            p.cum[b] = at;
+            at += int64_t(s.tiles) * s.N * Hk;
+        }
+        if (tid == 0) p.cum[seqs] = total;
+    }
+    if (blockIdx.x >= shares) return;
+    const int64_t w0 = blockIdx.x * total / shares, w1 = (blockIdx.x + 1) * total / shares;
+    if (before <= w0 && w0 < before + mine) {
+        int64_t at = before, b = s0;
+        Seq s = load_seq<R>(p, b, false);
+        while (at + int64_t(s.tiles) * s.N * Hk <= w0) {
+            at += int64_t(s.tiles) * s.N * Hk;
+            s = load_seq<R>(p, ++b, false);
+        }
+        scan[0] = b;
+        scan[1] = w0 - at;
+    }
+    __syncthreads();
+    Walk<R> get, use;  // the walk of the loads, and that of the products
+    get.b = scan[0];
+    get.s = load_seq<R>(p, get.b, false);
+    {
+        const int64_t r = scan[1], u = r / get.s.N;
+        get.c = get.s.c0 + int(r % get.s.N);
+        get.tile = int(u % get.s.tiles);
+        get.h = int(u / get.s.tiles);
+    }
+    use = get;
+
+    const uint32_t ring = smem_u32(smem) + uint32_t(warp * C::RING);
+    const unsigned char *ring_p = smem + warp * C::RING;
+    // The page of the walk's step, loaded one step before it is needed; -1 where the step has no key.
+    auto page_of = [&](const Walk<R> &w) -> int {
+        const int t = w.c * CH + 16 * warp;
+        return t < w.s.n ? w.s.pages[t >> psh] : -1;
+    };
+    int page = page_of(get);
+    int64_t left = w1 - w0;  // steps whose loads are still to be issued
+    uint32_t loaded = 0;     // stages that hold keys, one bit each
+    auto issue = [&](int stage) {
+        if (left > 0) {
+            const int t = get.c * CH + 16 * warp;
+            loaded &= ~(1u << stage);
+            if (uint32_t(page) < uint32_t(a.c.pages)) {
+                loaded |= 1u << stage;
+                const int64_t row = ((int64_t(page) * Hk + get.h) << psh) + (t & ((1 << psh) - 1));
+                const uint32_t dst = ring + uint32_t(stage * C::STAGE);
+                const uint8_t *ks = a.c.k_codes + row * (D / 2), *vs = a.c.v_codes + row * (D / 2);
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i) {
+                    const int piece = lane + 32 * i;
+                    constexpr int PR = D / 32;  // pieces per row
+                    cp_async16(dst + 16 * piece, ks + 16 * piece);
+                    cp_async16(dst + C::KB + value_place<D>(piece / PR, piece % PR), vs + 16 * piece);
+                }
+                if (lane < 8)
+                    cp_async16(dst + 2 * C::KB + 16 * lane,
+                               (lane < 4 ? a.c.k_scale : a.c.v_scale) + row + 4 * (lane & 3));
+            } else if (t < get.s.n && lane == 0) {
+                atomicOr(a.err, kSiteKvAttention);
+            }
+            get.next(p, seqs);
+            if (--left > 0) page = page_of(get);
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) issue(s);
+
+    float o[NT][D / 16][4];
+    uint32_t qf[NT][KS][2];
+    float mult[NT][2], start[NT][2], ref[NT][2], sum[NT][2];
+    int lo[NT][2], hi[NT][2];   // keys that the rows of this lane's columns see: [lo, hi)
+    int lo_all = 0, hi_all = 0;  // keys that all rows see
+    bool fresh = true;
+    int seg = 0;  // units begun
+
+    for (int64_t step = w0; step < w1; ++step) {
+        const int stage = int((step - w0) % STAGES);
+        if (fresh) {
+            // ---- a unit begins: its queries ----
+            fresh = false;
+            lo_all = 0;
+            hi_all = INT_MAX;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const int j = use.tile * R + 8 * nt + g;
+                const bool real = j < use.s.m * p.G;
+                const int i = real ? j / p.G : 0;
+                const uint16_t *qr = a.q + (int64_t(use.s.q0 + i) * H + use.h * p.G + (real ? j - i * p.G : 0)) * D;
+                uint4 v[W];
+                float big = 0.0f;
+#pragma unroll
+                for (int w = 0; w < W; ++w) {  // eight consecutive elements per word of codes
+                    v[w] = real ? *reinterpret_cast<const uint4 *>(qr + c * (D / 4) + 8 * w) : make_uint4(0, 0, 0, 0);
+                    const uint32_t u[4] = {v[w].x, v[w].y, v[w].z, v[w].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        big = fmaxf(big, fmaxf(fabsf(__uint_as_float(u[e] << 16)), fabsf(__uint_as_float(u[e] & 0xffff0000u))));
+                }
+                big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+                big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+                // 2^(14 - e) for a largest element in [2^e, 2^(e + 1)): it stays under 2^15
+                const int e = int(__float_as_uint(big) >> 23) - 127;
+                const int up = big > 0.0f && e < 128 ? min(14 - e, 120) : 0;
+                const float f = __uint_as_float(uint32_t(up + 127) << 23);
+                float tot = 0.0f;
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    const uint32_t u[4] = {v[w].x, v[w].y, v[w].z, v[w].w};
+                    float x[8];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        x[2 * k] = __uint_as_float(u[k] << 16) * f;
+                        x[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u) * f;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t b0 = pack_f16x2(x[2 * k], x[2 * k + 4]);
+                        const uint32_t b1 = pack_f16x2(x[2 * k + 1] * 0.0625f, x[2 * k + 5] * 0.0625f);
+                        qf[nt][2 * w + k][0] = b0;
+                        qf[nt][2 * w + k][1] = b1;
+                        const float2 y0 = __half22float2(*reinterpret_cast<const __half2 *>(&b0));
+                        const float2 y1 = __half22float2(*reinterpret_cast<const __half2 *>(&b1));
+                        tot += (y0.x + y0.y) + 16.0f * (y1.x + y1.y);
+                    }
+                }
+                tot += __shfl_xor_sync(0xffffffffu, tot, 1);
+                tot += __shfl_xor_sync(0xffffffffu, tot, 2);
+                // The score's multiplier: the softmax scale, and what the operands were scaled by.
+                const float back = __uint_as_float(uint32_t(127 - up) << 23);  // 1 / f
+                const float mul = (CAP ? a.scale / a.softcap : a.scale * kLog2e) * back * 0x1p24f;
+                int rl = 0, rh = 0;
+                if (real) {
+                    rh = min(use.s.n, max(0, use.s.shift + i + 1));
+                    if (a.window) {
+                        const int64_t pos = use.b == a.B ? a.prefix_len + query_shift(a, use.s.q0 + i)
+                                                         : int64_t(use.s.shift) + i;
+                        rl = int(min(int64_t(rh), max(int64_t(0), pos - a.window + 1)));
+                    }
+                }
+                // rows lie in the lanes of group g; the scores' columns in those of c
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int src = 4 * (2 * c + k);
+                    mult[nt][k] = __shfl_sync(0xffffffffu, mul, src);
+                    start[nt][k] = __shfl_sync(0xffffffffu, tot, src) * (-8.0f * 0x1p-24f);
+                    lo[nt][k] = __shfl_sync(0xffffffffu, rl, src);
+                    hi[nt][k] = __shfl_sync(0xffffffffu, rh, src);
+                    ref[nt][k] = kNone;
+                    sum[nt][k] = 0.0f;
+                }
+                // rows past the last one see nothing, and are not looked at
+                lo_all = max(lo_all, __reduce_max_sync(0xffffffffu, real ? rl : 0));
+                hi_all = min(hi_all, __reduce_min_sync(0xffffffffu, real ? rh : INT_MAX));
+#pragma unroll
+                for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) o[nt][mt][k] = 0.0f;
+            }
+        }
+        cp_async_wait<STAGES - 2>();
+        __syncwarp();
+        const int t0 = use.c * CH + 16 * warp;
+        if (loaded & (1u << stage)) {
+            const unsigned char *st = ring_p + stage * C::STAGE;
+            // ---- scores: S^T[key][row] ----
+            float x[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                x[nt][0] = x[nt][2] = start[nt][0];
+                x[nt][1] = x[nt][3] = start[nt][1];
+            }
+            uint32_t k0[W], k1[W];  // this lane's parts of the key rows g and g + 8
+            if constexpr (D == 128) {
+                const uint4 u = *reinterpret_cast<const uint4 *>(st + 64 * g + 16 * c);
+                const uint4 v = *reinterpret_cast<const uint4 *>(st + 64 * (g + 8) + 16 * c);
+                k0[0] = u.x, k0[1] = u.y, k0[2] = u.z, k0[3] = u.w;
+                k1[0] = v.x, k1[1] = v.y, k1[2] = v.z, k1[3] = v.w;
+            } else {
+                const uint2 u = *reinterpret_cast<const uint2 *>(st + 32 * g + 8 * c);
+                const uint2 v = *reinterpret_cast<const uint2 *>(st + 32 * (g + 8) + 8 * c);
+                k0[0] = u.x, k0[1] = u.y;
+                k1[0] = v.x, k1[1] = v.y;
+            }
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                const uint32_t u = k0[w], v = k1[w], u8 = u >> 8, v8 = v >> 8;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    mma_f16(x[nt], nib_lo(u), nib_lo(v), nib_hi(u), nib_hi(v), qf[nt][2 * w][0], qf[nt][2 * w][1]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    mma_f16(x[nt], nib_lo(u8), nib_lo(v8), nib_hi(u8), nib_hi(v8), qf[nt][2 * w + 1][0],
+                            qf[nt][2 * w + 1][1]);
+            }
+            // ---- weights ----
+            const float *sc = reinterpret_cast<const float *>(st + 2 * C::KB);
+            const bool in0 = t0 + g < use.s.n, in1 = t0 + g + 8 < use.s.n;  // past the end a page may hold anything
+            const float ks0 = in0 ? sc[g] : 0.0f, ks1 = in1 ? sc[g + 8] : 0.0f;
+            // a scale of 0 (a row of zeros) counts as 2^-100 here: its codes are 0 anyway
+            const float lv0 = in0 ? fmaxf(lg2(sc[16 + g]), -100.0f) : 0.0f;
+            const float lv1 = in1 ? fmaxf(lg2(sc[16 + g + 8]), -100.0f) : 0.0f;
+            const bool inner = t0 >= lo_all && t0 + 16 <= hi_all;
+            bool grow = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float v = x[nt][k] * (k < 2 ? ks0 : ks1) * mult[nt][k & 1];
+                    if (CAP) v = a.softcap * kLog2e * tanh_exp(v);
+                    if (!inner) {
+                        const int t = t0 + g + (k < 2 ? 0 : 8);
+                        v = t >= lo[nt][k & 1] && t < hi[nt][k & 1] ? v : -INFINITY;
+                    }
+                    x[nt][k] = v;
+                    grow |= v + (k < 2 ? lv0 : lv1) > ref[nt][k & 1] + 14.0f;
+                }
+            }
+            if (__any_sync(0xffffffffu, grow)) {
+                // move the references to 6 under the maxima so far
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        float top = fmaxf(x[nt][k] + lv0, x[nt][k + 2] + lv1);
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                        const float r = fmaxf(ref[nt][k], top - 6.0f), f = ex2(ref[nt][k] - r);
+                        ref[nt][k] = r;
+                        sum[nt][k] *= f;
+#pragma unroll
+                        for (int mt = 0; mt < D / 16; ++mt) {
+                            o[nt][mt][k] *= f;
+                            o[nt][mt][k + 2] *= f;
+                        }
+                    }
+            }
+            uint32_t pf[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float d = x[nt][k] - ref[nt][k & 1];
+                    sum[nt][k & 1] += ex2(d);
+                    w[k] = ex2(d + (k < 2 ? lv0 : lv1));
+                }
+                pf[nt][0] = transpose8x8(pack_f16x2(w[0], w[1]));
+                pf[nt][1] = transpose8x8(pack_f16x2(w[2], w[3]));
+            }
+            // ---- values: O^T[element][row] += codes^T weights ----
+            // this lane's elements: D / 8 from g D / 8 on, of the keys 2c, 2c + 1 (first) and 2c + 8, 2c + 9
+            const unsigned char *vt = st + C::KB;
+            uint32_t v[4][D / 64];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int r = 2 * c + (k & 1) + 8 * (k >> 1);
+                if constexpr (D == 128) {
+                    const uint2 u = *reinterpret_cast<const uint2 *>(vt + value_place<D>(r, g >> 1) + 8 * (g & 1));
+                    v[k][0] = u.x, v[k][1] = u.y;
+                } else {
+                    v[k][0] = *reinterpret_cast<const uint32_t *>(vt + value_place<D>(r, g >> 2) + 4 * (g & 3));
+                }
+            }
+#pragma unroll
+            for (int w = 0; w < D / 64; ++w)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    // nibbles 4 half .. 4 half + 3 of the word, of a pair of keys
+                    const uint32_t sel = half ? 0x7632u : 0x5410u;
+                    const uint32_t u = __byte_perm(v[0][w], v[1][w], sel), y = __byte_perm(v[2][w], v[3][w], sel);
+                    constexpr uint32_t kEight = 0x80088008u, kOne = 0x3c003c00u, kSixteenth = 0x2c002c00u;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const uint32_t us = q ? u >> 8 : u, ys = q ? y >> 8 : y;
+                        const uint32_t a0 = hfma2(nib_lo(us), kOne, kEight), a1 = hfma2(nib_hi(us), kSixteenth, kEight);
+                        const uint32_t a2 = hfma2(nib_lo(ys), kOne, kEight), a3 = hfma2(nib_hi(ys), kSixteenth, kEight);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma_f16(o[nt][4 * w + 2 * half + q], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+                    }
+                }
+        }
+        __syncwarp();
+        issue((stage + STAGES - 1) % STAGES);
+
+        // ---- the unit's end, or the share's: join the warps ----
+        const bool unit_end = use.c + 1 == use.s.c0 + use.s.N;
+        if (unit_end || step + 1 == w1) {
+            float *part = reinterpret_cast<float *>(smem + C::OFF_PART + warp * C::PART);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int row = 8 * nt + 2 * c + k;
+                    float l = sum[nt][k];
+                    l += __shfl_xor_sync(0xffffffffu, l, 4);
+                    l += __shfl_xor_sync(0xffffffffu, l, 8);
+                    l += __shfl_xor_sync(0xffffffffu, l, 16);
+                    if (g == 0) {
+                        part[R * D + row] = ref[nt][k];
+                        part[R * D + R + row] = l;
+                    }
+#pragma unroll
+                    for (int mt = 0; mt < D / 16; ++mt) {
+                        // elements g D / 8 + 2 mt, + 1
+                        *reinterpret_cast<float2 *>(part + row * D + g * (D / 8) + 2 * mt) =
+                            make_float2(o[nt][mt][k], o[nt][mt][k + 2]);
+                    }
+                }
+            }
+            __syncthreads();
+            const bool whole = unit_end && (seg > 0 || scan[1] % use.s.N == 0);
+            const int slot = seg == 0 && !(whole) && !(scan[1] % use.s.N == 0) ? 0 : 1;
+            const int rows = min(R, use.s.m * p.G - use.tile * R);
+            const float *all = reinterpret_cast<const float *>(smem + C::OFF_PART);
+            for (int u = tid; u < rows * (D / 4); u += R_THREADS) {
+                const int row = u / (D / 4), d = 4 * (u % (D / 4));
+                float top = kNone;
+#pragma unroll
+                for (int w = 0; w < WARPS; ++w) top = fmaxf(top, all[w * (C::PART / 4) + R * D + row]);
+                float l = 0.0f;
+                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int w = 0; w < WARPS; ++w) {
+                    const float *q = all + w * (C::PART / 4);
+                    const float f = ex2(q[R * D + row] - top);
+                    const float4 z = *reinterpret_cast<const float4 *>(q + row * D + d);
+                    l += q[R * D + R + row] * f;
+                    v.x += z.x * f, v.y += z.y * f, v.z += z.z * f, v.w += z.w * f;
+                }
+                const float inv = l > 0.0f ? 0x1p24f / l : l == 0.0f ? 0.0f : l;
+                const float lse = l == 0.0f ? -INFINITY : top + lg2(l);  // in powers of two
+                const int j = use.tile * R + row, i = j / p.G;
+                const int64_t at = int64_t(use.s.q0 + i) * H + use.h * p.G + (j - i * p.G);
+                v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
+                if (whole && !p.shared) {
+                    *reinterpret_cast<uint2 *>(a.out + at * D + d) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+                    if (a.lse && d == 0) a.lse[at] = lse * 0.6931471805599453f;
+                } else {
+                    const int64_t k = whole ? (use.b == a.B ? a.T * H : 0) + at : (int64_t(blockIdx.x) * 2 + slot) * R + row;
+                    *reinterpret_cast<float4 *>((whole ? p.whole_o : p.slot_o) + k * D + d) = v;
+                    if (d == 0) (whole ? p.whole_l : p.slot_l)[k] = lse;
+                }
+            }
+            __syncthreads();
+            ++seg;
+            fresh = true;
+        }
+        use.next(p, seqs);
+    }
+}
+
+// ---- joining partial rows ---------------------------------------------------------
+// A block per output row: its parts are the slots of the blocks that its unit was cut
+// over, in order; behind a prefix, those of both units.  Four warps take every fourth
+// part, then join.
+template <int D, int R>
+__global__ void __launch_bounds__(128) kq_kv_combine_kernel(const __grid_constant__ Plan p) {
+    __shared__ float so[4][D], sl[4], sw[4];
+    const KvAttnArgs &a = p.a;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, H = a.q_heads;
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t at = blockIdx.x;
+    const int t = int(at / H), head = int(at % H), h = head / p.G;
     int64_t b = t;
-    int m = 1, i = 0;
+    int i = 0;
     if (a.q_start) {
-        int64_t lo = 0, hi = a.B;  // the sequence whose rows hold t
+        int lo = 0, hi = int(a.B);
         while (lo < hi) {
-            const int64_t mid = (lo + hi) / 2;
+            const int mid = (lo + hi) >> 1;
             if (a.q_start[mid + 1] <= t) lo = mid + 1;
             else hi = mid;
         }
-        if (lo == a.B) return;
+        if (lo == int(a.B)) return;  // padding behind the last sequence
         b = lo;
-        m = a.q_start[b + 1] - a.q_start[b];
-        i = int(t - a.q_start[b]);
+        i = t - a.q_start[lo];
     }
-    if (i >= a.max_q) {
-        if (tid == 0) atomicOr(a.err, kSiteKvAttention);
-        return;
+    if (i >= a.max_q) return;
+    const int64_t total = p.cum[a.B + p.shared], shares = min(int64_t(p.ctas), total);
+    // of each unit: its first slot (or the row's whole place) and the number of parts
+    int64_t first[2];
+    int parts[2] = {0, 0}, row[2];
+    for (int u = 0; u < 1 + p.shared; ++u) {
+        const int64_t sb = u ? a.B : b, c0 = p.cum[sb], c1 = p.cum[sb + 1];
+        int q0, m;
+        queries_of(a, b, q0, m);
+        m = u ? all_queries(a) : min(m, a.max_q);
+        const int tiles = (m * p.G + R - 1) / R, j = (u ? t : i) * p.G + head - h * p.G;
+        const int64_t N = (c1 - c0) / (int64_t(tiles) * a.c.heads);
+        const int64_t g0 = c0 + (int64_t(h) * tiles + j / R) * N;
+        first[u] = ((g0 + 1) * shares - 1) / total;
+        parts[u] = int(((g0 + N) * shares - 1) / total - first[u]) + 1;
+        row[u] = j % R;
+        if (parts[u] < 1 || first[u] < 0 || first[u] + parts[u] > p.ctas) return;  // q_start is not ascending
     }
-    const int psize = 1 << a.c.page_shift;
-    int64_t n = a.kv_len[b] > 0 ? a.kv_len[b] : 0;
-    if (n > a.max_pages * psize) {
-        if (tid == 0) atomicOr(a.err, kSiteKvAttention);
-        n = a.max_pages * psize;
-    }
-    const int64_t n_given = a.kv_len[b] > 0 ? a.kv_len[b] : 0;
-    if (tid < D) qs[tid] = bf16_bits_to_float(a.q[(t * H + h) * D + tid]);
-    const int64_t pos = a.prefix_len + n_given - m + i;
-    const int64_t low = a.window ? pos - a.window + 1 : 0;
-    float top = -INFINITY, sum = 0.0f, acc = 0.0f;
-    const int64_t total = a.prefix_len + n;
-    for (int64_t k0 = 0; k0 < total; k0 += S_THREADS) {
-        __syncthreads();
-        const int64_t k = k0 + tid;
-        bool see = k < total && k >= low && (k < a.prefix_len || k <= pos);
-        int64_t row = 0;
-        if (see) {
-            const bool pre = k < a.prefix_len;
-            const int64_t kk = pre ? k : k - a.prefix_len;
-            const int64_t page = pre ? a.prefix_pages[kk >> a.c.page_shift]
-                                     : a.page_table[b * a.max_pages + (kk >> a.c.page_shift)];
-            if (page < 0 || page >= a.c.pages) {
-                see = false;
-                atomicOr(a.err, kSiteKvAttention);
-            } else {
-                row = (page * Hk + kh) * psize + (kk & (psize - 1));
-            }
-        }
-        float x = -INFINITY;
-        if (see) {
-            float d = 0.0f;
-            for (int e = 0; e < D / 2; ++e) {
-                const int c = a.c.k_codes[row * (D / 2) + e];
-                d += qs[2 * e] * float(int(uint32_t(c) << 28) >> 28) + qs[2 * e + 1] * float(int(uint32_t(c) << 24) >> 28);
-            }
-            x = d * a.c.k_scale[row] * a.scale;
-            if (a.softcap > 0.0f) x = a.softcap * tanhf(x / a.softcap);
-        }
-        float mx = x;
-        for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        if ((tid & 31) == 0) red[tid >> 5] = mx;
-        __syncthreads();
-        mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-        const float nt = fmaxf(top, mx);
-        if (nt == -INFINITY) continue;
-        const float fix = expf(top - nt), p = expf(x - nt);
+    if (!p.shared && parts[0] == 1) return;  // written by its block
+    float top = -INFINITY, wsum = 0.0f;
+    float v[D / 32];
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) v[e] = 0.0f;
+    for (int k = warp; k < parts[0] + parts[1]; k += 4) {
+        const int u = k >= parts[0];
+        const int n = u ? k - parts[0] : k;
+        const bool whole = parts[u] == 1;
+        // a unit's first block holds it as its last unit, the others as their first
+        const int64_t place = whole ? u * a.T * H + at : ((first[u] + n) * 2 + (n == 0 ? 1 : 0)) * R + row[u];
+        const float l = (whole ? p.whole_l : p.slot_l)[place];
+        const float *src = (whole ? p.whole_o : p.slot_o) + place * D + lane * (D / 32);
+        if (l == -INFINITY) continue;
+        const float nt = fmaxf(top, l);
+        const float f = ex2(top - nt), w = ex2(l - nt);
         top = nt;
-        ps[tid] = see ? p * a.c.v_scale[row] : 0.0f;
-        row_of[tid] = row;
-        float sm = p;
-        for (int o = 16; o; o >>= 1) sm += __shfl_xor_sync(0xffffffffu, sm, o);
-        if ((tid & 31) == 0) red[4 + (tid >> 5)] = sm;
-        __syncthreads();
-        sum = sum * fix + red[4] + red[5] + red[6] + red[7];
-        if (tid < D) {
-            acc *= fix;
-            for (int j = 0; j < S_THREADS && k0 + j < total; ++j)
-                if (ps[j] != 0.0f) {
-                    const int c = a.c.v_codes[row_of[j] * (D / 2) + (tid >> 1)] >> (4 * (tid & 1));
-                    acc += ps[j] * float(int(uint32_t(c) << 28) >> 28);
-                }
-        }
+        wsum = wsum * f + w;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) v[e] = v[e] * f + src[e] * w;
     }
-    if (tid < D) a.out[(t * H + h) * D + tid] = float_to_bf16_bits(sum > 0.0f ? acc / sum : 0.0f);
-    if (tid == 0 && a.lse) a.lse[t * H + h] = sum > 0.0f ? top + logf(sum) : -INFINITY;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) so[warp][lane * (D / 32) + e] = v[e];
+    if (lane == 0) sl[warp] = top, sw[warp] = wsum;
+    __syncthreads();
+    top = fmaxf(fmaxf(sl[0], sl[1]), fmaxf(sl[2], sl[3]));
+    float w = 0.0f, r = 0.0f;
+    for (int k = 0; k < 4; ++k) {
+        if (sw[k] == 0.0f) continue;  // no part with a key
+        const float f = ex2(sl[k] - top);
+        w += sw[k] * f;
+        if (tid < D) r += so[k][tid] * f;
+    }
+    if (tid < D) a.out[at * D + tid] = float_to_bf16_bits(w == 0.0f ? 0.0f : r / w);
+    if (tid == 0 && a.lse) a.lse[at] = w == 0.0f ? -INFINITY : (top + lg2(w)) * 0.6931471805599453f;
+}
+
+// ---- host side ------------------------------------------------------------------------
+
+constexpr int kMaxCtas = 4 * 160;  // blocks of the row kernel, at most
+int row_tile(int G, int max_q) { return int64_t(G) * max_q <= 8 ? 8 : 16; }
+
+uint64_t align256(uint64_t x) { return (x + 255) & ~uint64_t(255); }
+
+// The workspace's parts, from `base`; returns the bytes.
+uint64_t lay_out(Plan *p, unsigned char *base, int64_t T, int64_t B, int H, int D, int R) {
+    uint64_t at = 0;
+    auto take = [&](uint64_t bytes) {
+        unsigned char *r = base + at;
+        at += align256(bytes);
+        return r;
+    };
+    unsigned char *cum = take(uint64_t(B + 2) * 8);
+    unsigned char *so = take(uint64_t(kMaxCtas) * 2 * R * D * 4), *sl = take(uint64_t(kMaxCtas) * 2 * R * 4);
+    unsigned char *wo = take(uint64_t(T) * H * 2 * D * 4), *wl = take(uint64_t(T) * H * 2 * 4);
+    if (p) {
+        p->cum = reinterpret_cast<int64_t *>(cum);
+        p->slot_o = reinterpret_cast<float *>(so);
+        p->slot_l = reinterpret_cast<float *>(sl);
+        p->whole_o = reinterpret_cast<float *>(wo);
+        p->whole_l = reinterpret_cast<float *>(wl);
+    }
+    return at;
+}
+
+template <int D, int NT, bool CAP>
+cudaError_t launch_rows(Plan &p, int num_sms, int device, cudaStream_t stream) {
+    using C = RCfg<D, NT>;
+    auto kern = kq_kv_rows_kernel<D, NT, CAP>;
+    static std::once_flag once[64];
+    static cudaError_t attr_err[64];
+    if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
+    std::call_once(once[device], [&] {
+        attr_err[device] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    });
+    if (attr_err[device] != cudaSuccess) return attr_err[device];
+    p.ctas = num_sms * C::OCC < kMaxCtas ? num_sms * C::OCC : kMaxCtas;
+    cudaError_t e = launch_overlapped(kern, unsigned(p.ctas), R_THREADS, C::SMEM, stream, p);
+    if (e != cudaSuccess) return e;
+    return launch_overlapped(kq_kv_combine_kernel<D, C::R>, unsigned(p.a.T * p.a.q_heads), 128, 0, stream, p);
+}
+
+template <int D, int NT>
+cudaError_t launch_cap(Plan &p, int num_sms, int device, cudaStream_t stream) {
+    return p.a.softcap > 0.0f ? launch_rows<D, NT, true>(p, num_sms, device, stream)
+                              : launch_rows<D, NT, false>(p, num_sms, device, stream);
 }
 
 }  // namespace
 
-uint64_t kv_attention_workspace_bytes(int64_t, int64_t, int, int, int, int) { return 16; }
+uint64_t kv_attention_workspace_bytes(int64_t T, int64_t B, int q_heads, int kv_heads, int head_dim, int max_q) {
+    return lay_out(nullptr, nullptr, T, B, q_heads, head_dim, row_tile(q_heads / kv_heads, max_q));
+}
 
-cudaError_t launch_kv_attention(const KvAttnArgs &a, int, int, cudaStream_t stream) {
-    const unsigned grid = unsigned(a.T * a.q_heads);
-    return a.c.D == 128 ? launch_overlapped(kq_kv_attention_kernel<128>, grid, S_THREADS, 0, stream, a)
-                        : launch_overlapped(kq_kv_attention_kernel<64>, grid, S_THREADS, 0, stream, a);
+cudaError_t launch_kv_attention(const KvAttnArgs &a, int num_sms, int device, cudaStream_t stream) {
+    Plan p;
+    p.a = a;
+    p.G = a.q_heads / a.c.heads;
+    p.shared = a.prefix_pages != nullptr;
+    const int R = row_tile(p.G, a.max_q);
+    lay_out(&p, a.workspace, a.T, a.B, a.q_heads, a.c.D, R);
+    if (a.c.D == 128)
+        return R == 8 ? launch_cap<128, 1>(p, num_sms, device, stream) : launch_cap<128, 2>(p, num_sms, device, stream);
+    return R == 8 ? launch_cap<64, 1>(p, num_sms, device, stream) : launch_cap<64, 2>(p, num_sms, device, stream);
 }
 
 }  // namespace kq

@@ -38,7 +38,8 @@ def quantise(y, alpha):
 
 def attention(q, cache, tables, keys, nqs, scale, softcap=0.0, window=0, prefix=None):
     """out, lse in fp64, with the sums that bound an implementation's rounding:
-    mean = sum_t p_t |v_t| / sum_t p_t per output element, size = max_t scale sum_d |q_d k_td| per row.
+    mean = sum_t p_t |v_t| / sum_t p_t per output element, size = max_t scale sum_d |q_d k_td| per row,
+    floor = n max_t p_t s'_t / sum_t p_t per row of n keys (s' the value scales).
 
     cache = (k_codes, k_scale, v_codes, v_scale); tables[b]: page numbers of sequence b (a list);
     prefix = (pages, length) or None."""
@@ -48,13 +49,15 @@ def attention(q, cache, tables, keys, nqs, scale, softcap=0.0, window=0, prefix=
     G = H // Hk
     out = torch.zeros(T, H, D, dtype=torch.float64, device=q.device)
     mean, lse = torch.zeros_like(out), torch.full((T, H), -math.inf, dtype=torch.float64, device=q.device)
-    size = torch.zeros_like(lse)
+    size, floor = torch.zeros_like(lse), torch.zeros_like(out[..., :1])
 
     def rows(codes, sc, pages, n, h):
+        """[n, D + 1]: the values of n rows, and their scales."""
         if n == 0:
-            return torch.zeros(0, D, dtype=torch.float64, device=q.device)
+            return torch.zeros(0, D + 1, dtype=torch.float64, device=q.device)
         at = torch.as_tensor(list(pages)[:(n + page - 1) // page], device=q.device, dtype=torch.long)
-        return (unpack(codes[at, h]) * sc[at, h].double()[..., None]).reshape(-1, D)[:n]
+        s = sc[at, h].double()[..., None]
+        return torch.cat([unpack(codes[at, h]) * s, s], -1).reshape(-1, D + 1)[:n]
 
     pre = prefix[1] if prefix else 0
     first = 0
@@ -64,6 +67,7 @@ def attention(q, cache, tables, keys, nqs, scale, softcap=0.0, window=0, prefix=
             if pre:
                 K = torch.cat([rows(kc, ks, prefix[0], pre, h), K])
                 V = torch.cat([rows(vc, vs, prefix[0], pre, h), V])
+            K, V, S = K[:, :D], V[:, :D], V[:, D]
             pos = torch.arange(pre + n, device=q.device)
             for i in range(m):
                 p = pre + n - m + i
@@ -82,16 +86,20 @@ def attention(q, cache, tables, keys, nqs, scale, softcap=0.0, window=0, prefix=
                 out[first + i, h * G:(h + 1) * G] = w @ V[see]
                 mean[first + i, h * G:(h + 1) * G] = w @ V[see].abs()
                 lse[first + i, h * G:(h + 1) * G] = z
+                floor[first + i, h * G:(h + 1) * G, 0] = (w * S[see]).amax(-1) * w.shape[-1]
         first += m
-    return out, lse, mean, size
+    return out, lse, mean, size, floor
 
 
 def check_attention(out, lse, ref):
     """The rounding an implementation may have: a score is a sum of D products of 24-bit values (off by at most
     (D + 8) 2^-24 of the products' absolute sum), its exponential and the sums of them are fp32 (2^-18 covers
     thousands of terms with their maxima moved along), every weight is rounded once to no fewer than bf16's bits
-    before it meets the values (half a step: 2^-8 of each term), and the result once to bf16 (2^-8 of it)."""
-    r_out, r_lse, mean, size = ref
+    before it meets the values (half a step: 2^-8 of each term), and the result once to bf16 (2^-8 of it).
+    Weights kept in fp16 with their largest at 2^6 or more have a smallest step besides: 2^-24, half of it
+    2^-25 = 2^-31 2^6, so each of n weights p s' may be off by 2^-31 of the largest, times a code of at most 8:
+    8 2^-31 floor in all (an element that is 0 in every key but those of the smallest weights shows it)."""
+    r_out, r_lse, mean, size, floor = ref
     D = r_out.shape[-1]
     off = (D + 8) * 2.0 ** -24 * size + 2.0 ** -18
     if lse is not None:
@@ -100,7 +108,7 @@ def check_attention(out, lse, ref):
         assert (lse[~fin] == -math.inf).all()
         d = (lse.double() - r_lse).abs()[fin]
         assert (d <= (off + 2.0 ** -23 * r_lse.abs())[fin]).all(), "lse off by %.3g" % float(d.max())
-    bound = 2.0 ** -8 * r_out.abs() + (2.0 ** -8 + 2 * off[..., None]) * mean + 1e-30
+    bound = 2.0 ** -8 * r_out.abs() + (2.0 ** -8 + 2 * off[..., None]) * mean + 8 * 2.0 ** -31 * floor + 1e-30
     d = (out.double() - r_out).abs()
     worst = float((d / bound).max()) if d.numel() else 0.0
     assert worst <= 1.0, "out off by %.3g of its bound" % worst
