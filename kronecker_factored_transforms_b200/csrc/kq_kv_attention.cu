@@ -43,17 +43,17 @@
 
 #include "kq_common.cuh"
 #include "kq_internal.h"
+#include "kq_wait.cuh"
 
 namespace kq {
 namespace {
 
-constexpr int CH = 64;          // keys per chunk
-constexpr int WARPS = 4;        // warps per block, 16 keys of a chunk each
-constexpr int R_THREADS = 32 * WARPS;
-constexpr int STAGES = 4;       // cp.async stages per warp
+constexpr int WARPS = 4;        // multiplying warps per block
+constexpr int MT = 2;           // tiles of 16 keys that each takes of a chunk
+constexpr int CH = 16 * MT * WARPS;  // keys per chunk
+constexpr int R_THREADS = 32 * (WARPS + 1);
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNone = -1e30f;  // reference of a row that has seen no key
-static_assert(CH == 16 * WARPS, "a chunk is one step of every warp");
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -68,14 +68,6 @@ __device__ __forceinline__ float lg2(float x) {
 // tanh as 1 - 2 / (e^2z + 1): off by about 2^-22, absolutely.
 __device__ __forceinline__ float tanh_exp(float z) {
     return 1.0f - __fdividef(2.0f, ex2(z * (2.0f * kLog2e)) + 1.0f);
-}
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -98,8 +90,14 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
     return d;
 }
 // Codes of nibbles 0 and 4 (lo) and 1 and 5 (hi, times 16) of a word, plus 8, times 2^-24, as fp16 pairs.
-__device__ __forceinline__ uint32_t nib_lo(uint32_t w) { return (w ^ 0x88888888u) & 0x000f000fu; }
-__device__ __forceinline__ uint32_t nib_hi(uint32_t w) { return (w ^ 0x88888888u) & 0x00f000f0u; }
+// (w & mask) ^ eight, one LOP3 with the second constant in a register.
+__device__ __forceinline__ uint32_t and_xor(uint32_t w, uint32_t mask, uint32_t eight) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(d) : "r"(w), "r"(mask), "r"(eight));
+    return d;
+}
+__device__ __forceinline__ uint32_t nib_lo(uint32_t w) { return and_xor(w, 0x000f000fu, 0x00080008u); }
+__device__ __forceinline__ uint32_t nib_hi(uint32_t w) { return and_xor(w, 0x00f000f0u, 0x00800080u); }
 
 // ---- which keys and rows a unit has ---------------------------------------------
 
@@ -210,37 +208,62 @@ __device__ __forceinline__ int query_shift(const KvAttnArgs &a, int t) {
 
 template <int D, int NT>
 struct RCfg {
-    static constexpr int R = 8 * NT;              // query rows per tile
-    static constexpr int KB = 16 * D / 2;         // a step's key codes: 16 rows
-    static constexpr int STAGE = 2 * KB + 128;    // keys, values, 16 scales of each
-    static constexpr int RING = STAGES * STAGE;
-    static constexpr int PART = R * (D + 2) * 4;  // a warp's rows when a unit ends: values, reference, sum
-    static constexpr int OFF_PART = WARPS * RING;
-    static constexpr int OFF_SCAN = OFF_PART + WARPS * PART;
-    static constexpr int SMEM = OFF_SCAN + 16 * WARPS;
-    static constexpr int OCC = NT == 1 ? 4 : 3;   // blocks per SM
+    static constexpr int R = 8 * NT;               // query rows per tile
+    static constexpr int STAGES = NT == 1 ? 3 : 4;
+    static constexpr int CODES = CH * D / 2;       // a chunk's codes, of keys or of values
+    static constexpr int STAGE = 2 * CODES + 2 * CH * 4;
+    static constexpr int PART = R * (D + 2) * 4;   // a warp's rows when a unit ends: values, reference, sum
+    static constexpr int OFF_PART = STAGES * STAGE;
+    static constexpr int OFF_DESC = OFF_PART + WARPS * PART;      // a Desc per stage
+    static constexpr int OFF_BAR = OFF_DESC + STAGES * 64;
+    static constexpr int FULL = 0, EMPTY = STAGES, JOIN = 2 * STAGES, NBAR = JOIN + 2;
+    static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;           // abort flag
+    static constexpr int OFF_SCAN = (OFF_MISC + 4 + 15) & ~15;
+    static constexpr int SMEM = OFF_SCAN + 8 * (WARPS + 1) + 16;
+    static constexpr int OCC = NT == 1 ? 3 : 2;    // blocks per SM
     static_assert((SMEM + 1024) * OCC <= 227 * 1024, "shared memory of the resident blocks");
+    static_assert(STAGE % 128 == 0 && OFF_PART % 16 == 0 && OFF_BAR % 8 == 0, "alignment");
 };
 
-// The place of 16-byte piece q of value row r in a stage.  A lane reads 8 (or 4) bytes of
-// the rows 2c, 2c + 1, 2c + 8, 2c + 9: even rows first, and pieces exchanged in every
-// second pair of rows, so that a read's rows lie in different banks.
-template <int D>
-__device__ __forceinline__ uint32_t value_place(int r, int q) {
-    const int p = (r >> 1) | ((r & 1) << 3);
-    return D == 128 ? uint32_t(p * 64 + ((q ^ (p & 2)) << 4)) : uint32_t(p * 32 + (q << 4));
-}
+// What the loading warp says of a stage's chunk to those that multiply.
+struct Desc {
+    int t0, n;        // first key, keys of the sequence
+    uint32_t flags;   // bit s: the 16 keys from t0 + 16 s are there; and those below
+    int shift;
+    int q0, m, h, tile;
+    int place;        // of partial rows: kWhole, or the slot's number
+    int prefix;       // whether this is the shared prefix
+    int pad[6];
+};
+static_assert(sizeof(Desc) == 64, "a stage's description");
+enum : uint32_t { kUnitBegins = 1u << 16, kUnitEnds = 1u << 17 };  // ends: or the block's share does
+constexpr int kWhole = -1;
+enum : unsigned { kSiteKvWait = 262144u };
 
 template <int D, int NT, bool CAP>
 __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel(const __grid_constant__ Plan p) {
     using C = RCfg<D, NT>;
+    using namespace tc;
     constexpr int R = C::R, KS = D / 16, W = D / 32;  // k steps; words of a lane's part of a key row
     extern __shared__ __align__(128) unsigned char smem[];
     const KvAttnArgs &a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int Hk = a.c.heads, H = a.q_heads, psh = a.c.page_shift;
     const int64_t seqs = a.B + p.shared;
-    int64_t *scan = reinterpret_cast<int64_t *>(smem + C::OFF_SCAN);  // [4] warp sums, [4] found walk
+    const uint32_t sbase = smem_u32(smem);
+    auto bar = [&](int i) -> uint32_t { return sbase + uint32_t(C::OFF_BAR + 8 * i); };
+    volatile int *s_abort = reinterpret_cast<volatile int *>(smem + C::OFF_MISC);
+    int64_t *scan = reinterpret_cast<int64_t *>(smem + C::OFF_SCAN);  // warp sums; then the block's first chunk
+    if (tid == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(bar(C::FULL + s), 1);
+            mbar_init(bar(C::EMPTY + s), WARPS);
+        }
+        mbar_init(bar(C::JOIN), WARPS);
+        mbar_init(bar(C::JOIN + 1), WARPS);
+        *s_abort = 0;
+        fence_mbar_init();
+    }
     griddep_wait();
     griddep_launch_dependents();
 
@@ -261,11 +284,10 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
     __syncthreads();
     int64_t total = 0;
     before -= mine;
-    for (int w = 0; w < WARPS; ++w) {
+    for (int w = 0; w <= WARPS; ++w) {
         if (w < warp) before += scan[w];
         total += scan[w];
     }
-    __syncthreads();
     // no more shares than chunks: every share has one, so a unit's blocks are consecutive
     const int64_t shares = min(int64_t(p.ctas), total);
     if (blockIdx.x == 0) {  // for the combining kernel
@@ -279,6 +301,8 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
     }
     if (blockIdx.x >= shares) return;
     const int64_t w0 = blockIdx.x * total / shares, w1 = (blockIdx.x + 1) * total / shares;
+    const int steps = int(w1 - w0);
+    __syncthreads();
     if (before <= w0 && w0 < before + mine) {
         int64_t at = before, b = s0;
         Seq s = load_seq<R>(p, b, false);
@@ -290,78 +314,121 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
         scan[1] = w0 - at;
     }
     __syncthreads();
-    Walk<R> get, use;  // the walk of the loads, and that of the products
-    get.b = scan[0];
-    get.s = load_seq<R>(p, get.b, false);
-    {
-        const int64_t r = scan[1], u = r / get.s.N;
-        get.c = get.s.c0 + int(r % get.s.N);
-        get.tile = int(u % get.s.tiles);
-        get.h = int(u / get.s.tiles);
-    }
-    use = get;
 
-    const uint32_t ring = smem_u32(smem) + uint32_t(warp * C::RING);
-    const unsigned char *ring_p = smem + warp * C::RING;
-    // The page of the walk's step, loaded one step before it is needed; -1 where the step has no key.
-    auto page_of = [&](const Walk<R> &w) -> int {
-        const int t = w.c * CH + 16 * warp;
-        return t < w.s.n ? w.s.pages[t >> psh] : -1;
-    };
-    int page = page_of(get);
-    int64_t left = w1 - w0;  // steps whose loads are still to be issued
-    uint32_t loaded = 0;     // stages that hold keys, one bit each
-    auto issue = [&](int stage) {
-        if (left > 0) {
-            const int t = get.c * CH + 16 * warp;
-            loaded &= ~(1u << stage);
-            if (uint32_t(page) < uint32_t(a.c.pages)) {
-                loaded |= 1u << stage;
-                const int64_t row = ((int64_t(page) * Hk + get.h) << psh) + (t & ((1 << psh) - 1));
-                const uint32_t dst = ring + uint32_t(stage * C::STAGE);
-                const uint8_t *ks = a.c.k_codes + row * (D / 2), *vs = a.c.v_codes + row * (D / 2);
-#pragma unroll
-                for (int i = 0; i < D / 64; ++i) {
-                    const int piece = lane + 32 * i;
-                    constexpr int PR = D / 32;  // pieces per row
-                    cp_async16(dst + 16 * piece, ks + 16 * piece);
-                    cp_async16(dst + C::KB + value_place<D>(piece / PR, piece % PR), vs + 16 * piece);
-                }
-                if (lane < 8)
-                    cp_async16(dst + 2 * C::KB + 16 * lane,
-                               (lane < 4 ? a.c.k_scale : a.c.v_scale) + row + 4 * (lane & 3));
-            } else if (t < get.s.n && lane == 0) {
-                atomicOr(a.err, kSiteKvAttention);
+    if (warp == WARPS) {
+        // ---------------- the loading warp: one chunk per stage, by bulk copies ----------------
+        Walk<R> w;
+        w.b = scan[0];
+        w.s = load_seq<R>(p, w.b, false);
+        const int64_t r0 = scan[1], u0 = r0 / w.s.N;
+        w.c = w.s.c0 + int(r0 % w.s.N);
+        w.tile = int(u0 % w.s.tiles);
+        w.h = int(u0 / w.s.tiles);
+        bool entire = w.c == w.s.c0;  // whether this block has had the unit from its first chunk on
+        bool begins = true, first = true;
+        // lane i copies piece i of a chunk: the keys of a page that lie in it
+        const int gsh = (1 << psh) < CH ? psh : 31 - __clz(CH), pieces = CH >> gsh;
+        static_assert((CH & (CH - 1)) == 0 && 4 * (CH / 16) <= 32, "a lane per piece of a chunk");
+        const int piece = lane & (pieces - 1), what = lane / pieces;  // what: codes and scales of keys, of values
+        auto page_of = [&]() -> int {
+            const int t = w.c * CH + (piece << gsh);
+            return t < w.s.n ? w.s.pages[t >> psh] : -1;
+        };
+        int page = page_of();
+        Ring rg;
+        int issued = 0;
+        for (int i = 0; i < steps; ++i, rg.next(C::STAGES)) {
+            if (!__all_sync(0xffffffffu, wait_bounded_err(bar(C::EMPTY + rg.idx), rg.phase ^ 1u, s_abort, kSiteKvWait,
+                                                          kWaitLimitNs, false, a.err)))
+                break;
+            const int t = w.c * CH + (piece << gsh);
+            const bool there = t < w.s.n && uint32_t(page) < uint32_t(a.c.pages);
+            if (t < w.s.n && !there && what == 0) atomicOr(a.err, kSiteKvAttention);
+            const uint32_t ok = __ballot_sync(0xffffffffu, there && lane < pieces);
+            const int last = w.s.c0 + w.s.N - 1;
+            const bool ends = w.c == last || i + 1 == steps;
+            if (lane == 0) {
+                uint32_t flags = (begins ? uint32_t(kUnitBegins) : 0u) | (ends ? uint32_t(kUnitEnds) : 0u);
+                for (int s = 0; s < CH / 16; ++s)  // 16 keys s lie in piece (16 s) >> gsh
+                    if ((ok >> ((16 * s) >> gsh) & 1u) && w.c * CH + 16 * s < w.s.n) flags |= 1u << s;
+                Desc d;
+                d.t0 = w.c * CH;
+                d.n = w.s.n;
+                d.flags = flags;
+                d.shift = w.s.shift;
+                d.q0 = w.s.q0;
+                d.m = w.s.m;
+                d.h = w.h;
+                d.tile = w.tile;
+                d.place = entire && w.c == last ? kWhole : int(blockIdx.x) * 2 + (first && !entire ? 0 : 1);
+                d.prefix = w.b == a.B;
+                *reinterpret_cast<Desc *>(smem + C::OFF_DESC + 64 * rg.idx) = d;
+                const int n = __popc(ok) << gsh;
+                mbar_arrive_expect_tx(bar(C::FULL + rg.idx), uint32_t(n * (D + 8)));
             }
-            get.next(p, seqs);
-            if (--left > 0) page = page_of(get);
+            __syncwarp();
+            if (there && what < 4) {
+                const int64_t row = ((int64_t(page) * Hk + w.h) << psh) + (t & ((1 << psh) - 1));
+                const bool codes = (what & 1) == 0, val = what >= 2;
+                const unsigned char *src =
+                    codes ? (val ? a.c.v_codes : a.c.k_codes) + row * (D / 2)
+                          : reinterpret_cast<const unsigned char *>((val ? a.c.v_scale : a.c.k_scale) + row);
+                const uint32_t per_key = codes ? D / 2 : 4;
+                const uint32_t dst = sbase + uint32_t(rg.idx * C::STAGE) + (codes ? 0 : 2 * C::CODES) +
+                                     (val ? (codes ? C::CODES : 4 * CH) : 0) + uint32_t(piece << gsh) * per_key;
+                bulk_load(dst, src, per_key << gsh, bar(C::FULL + rg.idx));
+            }
+            ++issued;
+            if (i + 1 < steps) {
+                w.next(p, seqs);
+                begins = w.c == w.s.c0;
+                if (begins) {
+                    entire = true;
+                    first = false;
+                }
+                page = page_of();
+            }
         }
-        cp_async_commit();
-    };
-#pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) issue(s);
+        // every copy in flight lands before the block may end
+        Ring rd;
+        for (int i = 0; i < issued; ++i, rd.next(C::STAGES))
+            if (i + C::STAGES >= issued)
+                wait_bounded_err(bar(C::FULL + rd.idx), rd.phase, s_abort, kSiteKvWait, kWaitLimitNs, true, a.err);
+        return;
+    }
 
+    // ---------------- the multiplying warps: 16 MT keys of every chunk each ----------------
+    // Row r of a tile is key order(r) of its 16: so that a lane's key rows, and the
+    // rows 2c, 2c + 1 of values, start in different banks (rows are 64 or 32 bytes).
+    auto order = [](int r) { return r ^ ((r >> 1) & 1); };
     float o[NT][D / 16][4];
     uint32_t qf[NT][KS][2];
     float mult[NT][2], start[NT][2], ref[NT][2], sum[NT][2];
-    int lo[NT][2], hi[NT][2];   // keys that the rows of this lane's columns see: [lo, hi)
+    int lo[NT][2], hi[NT][2];    // keys that the rows of this lane's columns see: [lo, hi)
     int lo_all = 0, hi_all = 0;  // keys that all rows see
-    bool fresh = true;
-    int seg = 0;  // units begun
-
-    for (int64_t step = w0; step < w1; ++step) {
-        const int stage = int((step - w0) % STAGES);
-        if (fresh) {
+    uint32_t seen = 0;           // columns whose reference is set, one bit each; all once
+    constexpr uint32_t kAllSeen = (1u << 2 * NT) - 1;
+    Ring rg;
+    uint32_t joins = 0;
+    const int og = order(g);
+    for (int step = 0; step < steps; ++step, rg.next(C::STAGES)) {
+        if (!__all_sync(0xffffffffu, wait_bounded_err(bar(C::FULL + rg.idx), rg.phase, s_abort, kSiteKvWait,
+                                                      kWaitLimitNs, false, a.err)))
+            break;
+        const Desc *desc = reinterpret_cast<const Desc *>(smem + C::OFF_DESC + 64 * rg.idx);
+        const uint32_t flags = desc->flags;
+        if (flags & kUnitBegins) {
             // ---- a unit begins: its queries ----
-            fresh = false;
+            const int q0 = desc->q0, m = desc->m, h = desc->h, tile = desc->tile, shift = desc->shift, n = desc->n;
             lo_all = 0;
             hi_all = INT_MAX;
+            seen = 0;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const int j = use.tile * R + 8 * nt + g;
-                const bool real = j < use.s.m * p.G;
+                const int j = tile * R + 8 * nt + g;
+                const bool real = j < m * p.G;
                 const int i = real ? j / p.G : 0;
-                const uint16_t *qr = a.q + (int64_t(use.s.q0 + i) * H + use.h * p.G + (real ? j - i * p.G : 0)) * D;
+                const uint16_t *qr = a.q + (int64_t(q0 + i) * H + h * p.G + (real ? j - i * p.G : 0)) * D;
                 uint4 v[W];
                 float big = 0.0f;
 #pragma unroll
@@ -406,10 +473,10 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
                 const float mul = (CAP ? a.scale / a.softcap : a.scale * kLog2e) * back * 0x1p24f;
                 int rl = 0, rh = 0;
                 if (real) {
-                    rh = min(use.s.n, max(0, use.s.shift + i + 1));
+                    rh = min(n, max(0, shift + i + 1));
                     if (a.window) {
-                        const int64_t pos = use.b == a.B ? a.prefix_len + query_shift(a, use.s.q0 + i)
-                                                         : int64_t(use.s.shift) + i;
+                        const int64_t pos =
+                            desc->prefix ? a.prefix_len + query_shift(a, q0 + i) : int64_t(shift) + i;
                         rl = int(min(int64_t(rh), max(int64_t(0), pos - a.window + 1)));
                     }
                 }
@@ -421,8 +488,9 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
                     start[nt][k] = __shfl_sync(0xffffffffu, tot, src) * (-8.0f * 0x1p-24f);
                     lo[nt][k] = __shfl_sync(0xffffffffu, rl, src);
                     hi[nt][k] = __shfl_sync(0xffffffffu, rh, src);
-                    ref[nt][k] = kNone;
+                    ref[nt][k] = 0.0f;
                     sum[nt][k] = 0.0f;
+                    if (lo[nt][k] >= hi[nt][k]) seen |= 1u << (2 * nt + k);  // nothing to see
                 }
                 // rows past the last one see nothing, and are not looked at
                 lo_all = max(lo_all, __reduce_max_sync(0xffffffffu, real ? rl : 0));
@@ -433,136 +501,181 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
                     for (int k = 0; k < 4; ++k) o[nt][mt][k] = 0.0f;
             }
         }
-        cp_async_wait<STAGES - 2>();
-        __syncwarp();
-        const int t0 = use.c * CH + 16 * warp;
-        if (loaded & (1u << stage)) {
-            const unsigned char *st = ring_p + stage * C::STAGE;
+        constexpr uint32_t kMine = (1u << MT) - 1;
+        const uint32_t mine_ok = flags >> (MT * warp) & kMine;
+        if (mine_ok) {
+            const int t0 = desc->t0 + 16 * MT * warp;
+            const unsigned char *st = smem + rg.idx * C::STAGE + 16 * MT * warp * (D / 2);
+            const float *sc = reinterpret_cast<const float *>(smem + rg.idx * C::STAGE + 2 * C::CODES) + 16 * MT * warp;
             // ---- scores: S^T[key][row] ----
-            float x[NT][4];
+            float x[MT][NT][4], ks[MT][2], lv[MT][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                x[nt][0] = x[nt][2] = start[nt][0];
-                x[nt][1] = x[nt][3] = start[nt][1];
-            }
-            uint32_t k0[W], k1[W];  // this lane's parts of the key rows g and g + 8
-            if constexpr (D == 128) {
-                const uint4 u = *reinterpret_cast<const uint4 *>(st + 64 * g + 16 * c);
-                const uint4 v = *reinterpret_cast<const uint4 *>(st + 64 * (g + 8) + 16 * c);
-                k0[0] = u.x, k0[1] = u.y, k0[2] = u.z, k0[3] = u.w;
-                k1[0] = v.x, k1[1] = v.y, k1[2] = v.z, k1[3] = v.w;
-            } else {
-                const uint2 u = *reinterpret_cast<const uint2 *>(st + 32 * g + 8 * c);
-                const uint2 v = *reinterpret_cast<const uint2 *>(st + 32 * (g + 8) + 8 * c);
-                k0[0] = u.x, k0[1] = u.y;
-                k1[0] = v.x, k1[1] = v.y;
-            }
+            for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-            for (int w = 0; w < W; ++w) {
-                const uint32_t u = k0[w], v = k1[w], u8 = u >> 8, v8 = v >> 8;
+                for (int nt = 0; nt < NT; ++nt) {
+                    x[mt][nt][0] = x[mt][nt][2] = start[nt][0];
+                    x[mt][nt][1] = x[mt][nt][3] = start[nt][1];
+                }
+                uint32_t k0[W], k1[W];  // this lane's parts of the key rows g and g + 8
+                const unsigned char *kt = st + 16 * mt * (D / 2);
+                if constexpr (D == 128) {
+                    const uint4 u = *reinterpret_cast<const uint4 *>(kt + 64 * og + 16 * c);
+                    const uint4 v = *reinterpret_cast<const uint4 *>(kt + 64 * (og + 8) + 16 * c);
+                    k0[0] = u.x, k0[1] = u.y, k0[2] = u.z, k0[3] = u.w;
+                    k1[0] = v.x, k1[1] = v.y, k1[2] = v.z, k1[3] = v.w;
+                } else {
+                    const uint2 u = *reinterpret_cast<const uint2 *>(kt + 32 * og + 8 * c);
+                    const uint2 v = *reinterpret_cast<const uint2 *>(kt + 32 * (og + 8) + 8 * c);
+                    k0[0] = u.x, k0[1] = u.y;
+                    k1[0] = v.x, k1[1] = v.y;
+                }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    mma_f16(x[nt], nib_lo(u), nib_lo(v), nib_hi(u), nib_hi(v), qf[nt][2 * w][0], qf[nt][2 * w][1]);
+                for (int k = 0; k < 2; ++k) {
+                    ks[mt][k] = sc[16 * mt + og + 8 * k];
+                    // a scale of 0 (a row of zeros) counts as 2^-100 here: its codes are 0 anyway
+                    lv[mt][k] = fmaxf(lg2(sc[CH + 16 * mt + og + 8 * k]), -100.0f);
+                }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    mma_f16(x[nt], nib_lo(u8), nib_lo(v8), nib_hi(u8), nib_hi(v8), qf[nt][2 * w + 1][0],
-                            qf[nt][2 * w + 1][1]);
-            }
-            // ---- weights ----
-            const float *sc = reinterpret_cast<const float *>(st + 2 * C::KB);
-            const bool in0 = t0 + g < use.s.n, in1 = t0 + g + 8 < use.s.n;  // past the end a page may hold anything
-            const float ks0 = in0 ? sc[g] : 0.0f, ks1 = in1 ? sc[g + 8] : 0.0f;
-            // a scale of 0 (a row of zeros) counts as 2^-100 here: its codes are 0 anyway
-            const float lv0 = in0 ? fmaxf(lg2(sc[16 + g]), -100.0f) : 0.0f;
-            const float lv1 = in1 ? fmaxf(lg2(sc[16 + g + 8]), -100.0f) : 0.0f;
-            const bool inner = t0 >= lo_all && t0 + 16 <= hi_all;
-            bool grow = false;
+                for (int w = 0; w < W; ++w) {
+                    const uint32_t u = k0[w], v = k1[w], u8 = u >> 8, v8 = v >> 8;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma_f16(x[mt][nt], nib_lo(u), nib_lo(v), nib_hi(u), nib_hi(v), qf[nt][2 * w][0], qf[nt][2 * w][1]);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float v = x[nt][k] * (k < 2 ? ks0 : ks1) * mult[nt][k & 1];
-                    if (CAP) v = a.softcap * kLog2e * tanh_exp(v);
-                    if (!inner) {
-                        const int t = t0 + g + (k < 2 ? 0 : 8);
-                        v = t >= lo[nt][k & 1] && t < hi[nt][k & 1] ? v : -INFINITY;
-                    }
-                    x[nt][k] = v;
-                    grow |= v + (k < 2 ? lv0 : lv1) > ref[nt][k & 1] + 14.0f;
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma_f16(x[mt][nt], nib_lo(u8), nib_lo(v8), nib_hi(u8), nib_hi(v8), qf[nt][2 * w + 1][0],
+                                qf[nt][2 * w + 1][1]);
                 }
             }
-            if (__any_sync(0xffffffffu, grow)) {
+            // ---- weights ----
+            const bool inner = mine_ok == kMine && t0 >= lo_all && t0 + 16 * MT <= hi_all;
+            if (!inner) {  // past the last key a page may hold anything
+                const int n = desc->n;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    const int left = mine_ok >> mt & 1u ? n - t0 - 16 * mt : 0;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        if (og + 8 * k >= left) ks[mt][k] = lv[mt][k] = 0.0f;
+                }
+            }
+            float top = -INFINITY;  // of a weight's exponent
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float f = ks[mt][k >> 1] * mult[nt][k & 1];
+                        float v;
+                        if (CAP) v = fmaf(tanh_exp(x[mt][nt][k] * f), a.softcap * kLog2e, -ref[nt][k & 1]);
+                        else v = fmaf(x[mt][nt][k], f, -ref[nt][k & 1]);
+                        x[mt][nt][k] = v;
+                    }
+            if (!inner) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int t = mine_ok >> mt & 1u ? t0 + 16 * mt + og + 8 * k : INT_MAX;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+                                if (t < lo[nt][j] || t >= hi[nt][j]) x[mt][nt][2 * k + j] = -INFINITY;
+                    }
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    top = fmax3(top, fmaxf(x[mt][nt][0], x[mt][nt][1]) + lv[mt][0],
+                                fmaxf(x[mt][nt][2], x[mt][nt][3]) + lv[mt][1]);
+            if (__any_sync(0xffffffffu, top > 14.0f || seen != kAllSeen)) {
                 // move the references to 6 under the maxima so far
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        float top = fmaxf(x[nt][k] + lv0, x[nt][k + 2] + lv1);
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                        const float r = fmaxf(ref[nt][k], top - 6.0f), f = ex2(ref[nt][k] - r);
-                        ref[nt][k] = r;
+                        float up = -INFINITY;
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt)
+                            up = fmax3(up, x[mt][nt][k] + lv[mt][0], x[mt][nt][k + 2] + lv[mt][1]);
+                        up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 4));
+                        up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 8));
+                        up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 16));
+                        const bool was = seen >> (2 * nt + k) & 1u;
+                        // a row's first keys set its reference, later ones may only raise it
+                        if (up > -INFINITY) seen |= 1u << (2 * nt + k);
+                        up = was ? fmaxf(up - 6.0f, 0.0f) : up > -INFINITY ? up - 6.0f : 0.0f;
+                        const float f = was ? ex2(-up) : 1.0f;
+                        ref[nt][k] += up;
                         sum[nt][k] *= f;
 #pragma unroll
-                        for (int mt = 0; mt < D / 16; ++mt) {
-                            o[nt][mt][k] *= f;
-                            o[nt][mt][k + 2] *= f;
+                        for (int mt = 0; mt < MT; ++mt) {
+                            x[mt][nt][k] -= up;
+                            x[mt][nt][k + 2] -= up;
+                        }
+#pragma unroll
+                        for (int e = 0; e < D / 16; ++e) {
+                            o[nt][e][k] *= f;
+                            o[nt][e][k + 2] *= f;
                         }
                     }
             }
-            uint32_t pf[NT][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float w[4];
+            for (int mt = 0; mt < MT; ++mt) {
+                uint32_t pf[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float w[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        sum[nt][k & 1] += ex2(x[mt][nt][k]);
+                        w[k] = ex2(x[mt][nt][k] + lv[mt][k >> 1]);
+                    }
+                    pf[nt][0] = transpose8x8(pack_f16x2(w[0], w[1]));
+                    pf[nt][1] = transpose8x8(pack_f16x2(w[2], w[3]));
+                }
+                // ---- values: O^T[element][row] += codes^T weights ----
+                // this lane's elements: D / 8 from g D / 8 on, of the tile's rows 2c, 2c + 1 and 2c + 8, 2c + 9
+                const unsigned char *vt = st + C::CODES + 16 * mt * (D / 2);
+                uint32_t v[4][D / 64];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const float d = x[nt][k] - ref[nt][k & 1];
-                    sum[nt][k & 1] += ex2(d);
-                    w[k] = ex2(d + (k < 2 ? lv0 : lv1));
-                }
-                pf[nt][0] = transpose8x8(pack_f16x2(w[0], w[1]));
-                pf[nt][1] = transpose8x8(pack_f16x2(w[2], w[3]));
-            }
-            // ---- values: O^T[element][row] += codes^T weights ----
-            // this lane's elements: D / 8 from g D / 8 on, of the keys 2c, 2c + 1 (first) and 2c + 8, 2c + 9
-            const unsigned char *vt = st + C::KB;
-            uint32_t v[4][D / 64];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int r = 2 * c + (k & 1) + 8 * (k >> 1);
-                if constexpr (D == 128) {
-                    const uint2 u = *reinterpret_cast<const uint2 *>(vt + value_place<D>(r, g >> 1) + 8 * (g & 1));
-                    v[k][0] = u.x, v[k][1] = u.y;
-                } else {
-                    v[k][0] = *reinterpret_cast<const uint32_t *>(vt + value_place<D>(r, g >> 2) + 4 * (g & 3));
-                }
-            }
-#pragma unroll
-            for (int w = 0; w < D / 64; ++w)
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    // nibbles 4 half .. 4 half + 3 of the word, of a pair of keys
-                    const uint32_t sel = half ? 0x7632u : 0x5410u;
-                    const uint32_t u = __byte_perm(v[0][w], v[1][w], sel), y = __byte_perm(v[2][w], v[3][w], sel);
-                    constexpr uint32_t kEight = 0x80088008u, kOne = 0x3c003c00u, kSixteenth = 0x2c002c00u;
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const uint32_t us = q ? u >> 8 : u, ys = q ? y >> 8 : y;
-                        const uint32_t a0 = hfma2(nib_lo(us), kOne, kEight), a1 = hfma2(nib_hi(us), kSixteenth, kEight);
-                        const uint32_t a2 = hfma2(nib_lo(ys), kOne, kEight), a3 = hfma2(nib_hi(ys), kSixteenth, kEight);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma_f16(o[nt][4 * w + 2 * half + q], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+                    const int r = order(2 * c + (k & 1)) + 8 * (k >> 1);
+                    if constexpr (D == 128) {
+                        const uint2 u = *reinterpret_cast<const uint2 *>(vt + 64 * r + 8 * g);
+                        v[k][0] = u.x, v[k][1] = u.y;
+                    } else {
+                        v[k][0] = *reinterpret_cast<const uint32_t *>(vt + 32 * r + 4 * g);
                     }
                 }
+#pragma unroll
+                for (int w = 0; w < D / 64; ++w)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        // nibbles 4 half .. 4 half + 3 of the word, of a pair of keys
+                        const uint32_t sel = half ? 0x7632u : 0x5410u;
+                        const uint32_t u = __byte_perm(v[0][w], v[1][w], sel), y = __byte_perm(v[2][w], v[3][w], sel);
+                        constexpr uint32_t kEight = 0x80088008u, kOne = 0x3c003c00u, kSixteenth = 0x2c002c00u;
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const uint32_t us = q ? u >> 8 : u, ys = q ? y >> 8 : y;
+                            const uint32_t a0 = hfma2(nib_lo(us), kOne, kEight);
+                            const uint32_t a1 = hfma2(nib_hi(us), kSixteenth, kEight);
+                            const uint32_t a2 = hfma2(nib_lo(ys), kOne, kEight);
+                            const uint32_t a3 = hfma2(nib_hi(ys), kSixteenth, kEight);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma_f16(o[nt][4 * w + 2 * half + q], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+                        }
+                    }
+            }
         }
-        __syncwarp();
-        issue((stage + STAGES - 1) % STAGES);
 
         // ---- the unit's end, or the share's: join the warps ----
-        const bool unit_end = use.c + 1 == use.s.c0 + use.s.N;
-        if (unit_end || step + 1 == w1) {
+        if (flags & kUnitEnds) {
             float *part = reinterpret_cast<float *>(smem + C::OFF_PART + warp * C::PART);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -574,7 +687,7 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
                     l += __shfl_xor_sync(0xffffffffu, l, 8);
                     l += __shfl_xor_sync(0xffffffffu, l, 16);
                     if (g == 0) {
-                        part[R * D + row] = ref[nt][k];
+                        part[R * D + row] = l == 0.0f ? kNone : ref[nt][k];
                         part[R * D + R + row] = l;
                     }
 #pragma unroll
@@ -585,12 +698,16 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
                     }
                 }
             }
-            __syncthreads();
-            const bool whole = unit_end && (seg > 0 || scan[1] % use.s.N == 0);
-            const int slot = seg == 0 && !(whole) && !(scan[1] % use.s.N == 0) ? 0 : 1;
-            const int rows = min(R, use.s.m * p.G - use.tile * R);
+            const int q0 = desc->q0, h = desc->h, tile = desc->tile, place = desc->place;
+            const int rows = min(R, desc->m * p.G - tile * R);
+            const int64_t whole_at = desc->prefix ? a.T * H : 0;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::JOIN));
+            if (!__all_sync(0xffffffffu, wait_bounded_err(bar(C::JOIN), joins & 1u, s_abort, kSiteKvWait, kWaitLimitNs,
+                                                          false, a.err)))
+                break;
             const float *all = reinterpret_cast<const float *>(smem + C::OFF_PART);
-            for (int u = tid; u < rows * (D / 4); u += R_THREADS) {
+            for (int u = tid; u < rows * (D / 4); u += 32 * WARPS) {
                 const int row = u / (D / 4), d = 4 * (u % (D / 4));
                 float top = kNone;
 #pragma unroll
@@ -607,23 +724,28 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
                 }
                 const float inv = l > 0.0f ? 0x1p24f / l : l == 0.0f ? 0.0f : l;
                 const float lse = l == 0.0f ? -INFINITY : top + lg2(l);  // in powers of two
-                const int j = use.tile * R + row, i = j / p.G;
-                const int64_t at = int64_t(use.s.q0 + i) * H + use.h * p.G + (j - i * p.G);
+                const int j = tile * R + row, i = j / p.G;
+                const int64_t at = int64_t(q0 + i) * H + h * p.G + (j - i * p.G);
                 v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
-                if (whole && !p.shared) {
+                if (place == kWhole && !p.shared) {
                     *reinterpret_cast<uint2 *>(a.out + at * D + d) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
                     if (a.lse && d == 0) a.lse[at] = lse * 0.6931471805599453f;
                 } else {
-                    const int64_t k = whole ? (use.b == a.B ? a.T * H : 0) + at : (int64_t(blockIdx.x) * 2 + slot) * R + row;
-                    *reinterpret_cast<float4 *>((whole ? p.whole_o : p.slot_o) + k * D + d) = v;
-                    if (d == 0) (whole ? p.whole_l : p.slot_l)[k] = lse;
+                    const int64_t k = place == kWhole ? whole_at + at : int64_t(place) * R + row;
+                    *reinterpret_cast<float4 *>((place == kWhole ? p.whole_o : p.slot_o) + k * D + d) = v;
+                    if (d == 0) (place == kWhole ? p.whole_l : p.slot_l)[k] = lse;
                 }
             }
-            __syncthreads();
-            ++seg;
-            fresh = true;
+            // the parts are free again once all have read them
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::JOIN + 1));
+            if (!__all_sync(0xffffffffu, wait_bounded_err(bar(C::JOIN + 1), joins & 1u, s_abort, kSiteKvWait,
+                                                          kWaitLimitNs, false, a.err)))
+                break;
+            ++joins;
         }
-        use.next(p, seqs);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::EMPTY + rg.idx));
     }
 }
 
