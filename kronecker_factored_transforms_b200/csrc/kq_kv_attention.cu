@@ -108,7 +108,7 @@ struct Plan {
     int G;             // query heads per key head
     int shared;        // a prefix is there
     int ctas;          // blocks of the row kernel
-    int64_t *cum;      // [B + 1 (+ 1)] chunks before a sequence, in the workspace
+    int2 *parts;       // [2][T * H] for every row: the first block that has keys of it, and how many have
     float *slot_o;     // [ctas][2][R][D] partial rows: a block's first unit, its last unit
     float *slot_l;     // [ctas][2][R]
     float *whole_o;    // [2][T * H][D] rows whose keys lay in one block (own keys; the prefix's)
@@ -157,7 +157,11 @@ __device__ __forceinline__ Seq load_seq(const Plan &p, int64_t b, bool report) {
         const int most = int(a.max_pages) << a.c.page_shift;
         s.n = min(given, most);
         s.m = min(m, a.max_q);
-        if (report && (given > most || m > a.max_q)) atomicOr(a.err, kSiteKvAttention);
+        if (report && (given > most || m > a.max_q)) {
+            atomicOr(a.err, kSiteKvAttention);
+            for (int64_t r = int64_t(s.q0 + s.m) * a.q_heads; r < int64_t(s.q0 + m) * a.q_heads; ++r)
+                p.parts[r] = make_int2(0, 0);  // rows past the bound
+        }
         s.shift = given - m;
         s.pages = a.page_table + b * a.max_pages;
         if (a.window) lo = max(0, s.shift - a.window + 1);
@@ -168,6 +172,21 @@ __device__ __forceinline__ Seq load_seq(const Plan &p, int64_t b, bool report) {
     s.tiles = (s.m * p.G + R - 1) / R;
     return s;
 }
+
+// The chunks of all units, dealt to the blocks: n each, and one more to the first `more`.  With
+// fewer chunks than blocks the last ones have none, so the blocks of a unit are consecutive.
+struct Shares {
+    int64_t n, more;
+    __device__ __forceinline__ Shares(int64_t total, int ctas) {
+        n = total < (int64_t(1) << 31) ? int64_t(uint32_t(total) / uint32_t(ctas)) : total / ctas;
+        more = total - n * ctas;
+    }
+    __device__ __forceinline__ int64_t begin(int64_t block) const { return n * block + min(block, more); }
+    __device__ __forceinline__ int block_of(int64_t chunk) const {
+        const int64_t big = (n + 1) * more;
+        return int(chunk < big ? chunk / (n + 1) : more + (chunk - big) / n);
+    }
+};
 
 // A walk over the chunks of a block: sequence, head, row tile, chunk.
 template <int R>
@@ -209,9 +228,10 @@ __device__ __forceinline__ int query_shift(const KvAttnArgs &a, int t) {
 template <int D, int NT>
 struct RCfg {
     static constexpr int R = 8 * NT;               // query rows per tile
-    static constexpr int STAGES = NT == 1 ? 3 : 4;
+    static constexpr int STAGES = 3;
     static constexpr int CODES = CH * D / 2;       // a chunk's codes, of keys or of values
-    static constexpr int STAGE = 2 * CODES + 2 * CH * 4;
+    static constexpr int Q = 2 * CODES + 2 * CH * 4;  // the unit's query rows, where one begins
+    static constexpr int STAGE = Q + R * D * 2;
     static constexpr int PART = R * (D + 2) * 4;   // a warp's rows when a unit ends: values, reference, sum
     static constexpr int OFF_PART = STAGES * STAGE;
     static constexpr int OFF_DESC = OFF_PART + WARPS * PART;      // a Desc per stage
@@ -233,12 +253,31 @@ struct Desc {
     int q0, m, h, tile;
     int place;        // of partial rows: kWhole, or the slot's number
     int prefix;       // whether this is the shared prefix
-    int pad[6];
+    int parts;        // blocks that have keys of the unit (0: this is not the first of them)
+    int pad[5];
 };
 static_assert(sizeof(Desc) == 64, "a stage's description");
 enum : uint32_t { kUnitBegins = 1u << 16, kUnitEnds = 1u << 17 };  // ends: or the block's share does
 constexpr int kWhole = -1;
 enum : unsigned { kSiteKvWait = 262144u };
+
+// Wait for a phase without taking issue slots: try_wait suspends the thread until the phase
+// completes or the hint (in ns) has passed.  Gives up as wait_bounded_err does.
+__device__ __forceinline__ bool wait_suspended(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(20000u)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile int *abort, unsigned int *err) {
+    if (__all_sync(0xffffffffu, wait_suspended(bar, parity))) return true;
+    return __all_sync(0xffffffffu,
+                      tc::wait_bounded_err(bar, parity, abort, kSiteKvWait, tc::kWaitLimitNs, false, err));
+}
 
 template <int D, int NT, bool CAP>
 __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel(const __grid_constant__ Plan p) {
@@ -288,19 +327,9 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
         if (w < warp) before += scan[w];
         total += scan[w];
     }
-    // no more shares than chunks: every share has one, so a unit's blocks are consecutive
-    const int64_t shares = min(int64_t(p.ctas), total);
-    if (blockIdx.x == 0) {  // for the combining kernel
-        int64_t at = before;
-        for (int64_t b = s0; b < s1; ++b) {
-            const Seq s = load_seq<R>(p, b, false);
-            p.cum[b] = at;
-            at += int64_t(s.tiles) * s.N * Hk;
-        }
-        if (tid == 0) p.cum[seqs] = total;
-    }
-    if (blockIdx.x >= shares) return;
-    const int64_t w0 = blockIdx.x * total / shares, w1 = (blockIdx.x + 1) * total / shares;
+    if (blockIdx.x >= total) return;
+    const Shares sh(total, p.ctas);
+    const int64_t w0 = sh.begin(blockIdx.x), w1 = sh.begin(blockIdx.x + 1);
     const int steps = int(w1 - w0);
     __syncthreads();
     if (before <= w0 && w0 < before + mine) {
@@ -338,15 +367,14 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
         Ring rg;
         int issued = 0;
         for (int i = 0; i < steps; ++i, rg.next(C::STAGES)) {
-            if (!__all_sync(0xffffffffu, wait_bounded_err(bar(C::EMPTY + rg.idx), rg.phase ^ 1u, s_abort, kSiteKvWait,
-                                                          kWaitLimitNs, false, a.err)))
-                break;
+            if (!wait_all(bar(C::EMPTY + rg.idx), rg.phase ^ 1u, s_abort, a.err)) break;
             const int t = w.c * CH + (piece << gsh);
             const bool there = t < w.s.n && uint32_t(page) < uint32_t(a.c.pages);
             if (t < w.s.n && !there && what == 0) atomicOr(a.err, kSiteKvAttention);
             const uint32_t ok = __ballot_sync(0xffffffffu, there && lane < pieces);
             const int last = w.s.c0 + w.s.N - 1;
             const bool ends = w.c == last || i + 1 == steps;
+            const int rows = begins ? min(R, w.s.m * p.G - w.tile * R) : 0;
             if (lane == 0) {
                 uint32_t flags = (begins ? uint32_t(kUnitBegins) : 0u) | (ends ? uint32_t(kUnitEnds) : 0u);
                 for (int s = 0; s < CH / 16; ++s)  // 16 keys s lie in piece (16 s) >> gsh
@@ -362,9 +390,10 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
                 d.tile = w.tile;
                 d.place = entire && w.c == last ? kWhole : int(blockIdx.x) * 2 + (first && !entire ? 0 : 1);
                 d.prefix = w.b == a.B;
+                d.parts = !entire ? 0 : w.c == last ? 1 : ends ? sh.block_of(w0 + i + last - w.c) - int(blockIdx.x) + 1 : 0;
                 *reinterpret_cast<Desc *>(smem + C::OFF_DESC + 64 * rg.idx) = d;
                 const int n = __popc(ok) << gsh;
-                mbar_arrive_expect_tx(bar(C::FULL + rg.idx), uint32_t(n * (D + 8)));
+                mbar_arrive_expect_tx(bar(C::FULL + rg.idx), uint32_t(n * (D + 8) + rows * D * 2));
             }
             __syncwarp();
             if (there && what < 4) {
@@ -377,6 +406,11 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
                 const uint32_t dst = sbase + uint32_t(rg.idx * C::STAGE) + (codes ? 0 : 2 * C::CODES) +
                                      (val ? (codes ? C::CODES : 4 * CH) : 0) + uint32_t(piece << gsh) * per_key;
                 bulk_load(dst, src, per_key << gsh, bar(C::FULL + rg.idx));
+            }
+            if (lane < rows) {
+                const int j = w.tile * R + lane, t = j / p.G;
+                bulk_load(sbase + uint32_t(rg.idx * C::STAGE + C::Q + lane * D * 2),
+                          a.q + (int64_t(w.s.q0 + t) * H + w.h * p.G + (j - t * p.G)) * D, D * 2, bar(C::FULL + rg.idx));
             }
             ++issued;
             if (i + 1 < steps) {
@@ -412,14 +446,12 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
     uint32_t joins = 0;
     const int og = order(g);
     for (int step = 0; step < steps; ++step, rg.next(C::STAGES)) {
-        if (!__all_sync(0xffffffffu, wait_bounded_err(bar(C::FULL + rg.idx), rg.phase, s_abort, kSiteKvWait,
-                                                      kWaitLimitNs, false, a.err)))
-            break;
+        if (!wait_all(bar(C::FULL + rg.idx), rg.phase, s_abort, a.err)) break;
         const Desc *desc = reinterpret_cast<const Desc *>(smem + C::OFF_DESC + 64 * rg.idx);
         const uint32_t flags = desc->flags;
         if (flags & kUnitBegins) {
             // ---- a unit begins: its queries ----
-            const int q0 = desc->q0, m = desc->m, h = desc->h, tile = desc->tile, shift = desc->shift, n = desc->n;
+            const int q0 = desc->q0, m = desc->m, tile = desc->tile, shift = desc->shift, n = desc->n;
             lo_all = 0;
             hi_all = INT_MAX;
             seen = 0;
@@ -428,12 +460,12 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
                 const int j = tile * R + 8 * nt + g;
                 const bool real = j < m * p.G;
                 const int i = real ? j / p.G : 0;
-                const uint16_t *qr = a.q + (int64_t(q0 + i) * H + h * p.G + (real ? j - i * p.G : 0)) * D;
+                const unsigned char *qr = smem + rg.idx * C::STAGE + C::Q + (8 * nt + g) * D * 2 + c * (D / 2);
                 uint4 v[W];
                 float big = 0.0f;
 #pragma unroll
                 for (int w = 0; w < W; ++w) {  // eight consecutive elements per word of codes
-                    v[w] = real ? *reinterpret_cast<const uint4 *>(qr + c * (D / 4) + 8 * w) : make_uint4(0, 0, 0, 0);
+                    v[w] = real ? *reinterpret_cast<const uint4 *>(qr + 16 * w) : make_uint4(0, 0, 0, 0);
                     const uint32_t u[4] = {v[w].x, v[w].y, v[w].z, v[w].w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
@@ -658,10 +690,10 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
                         // nibbles 4 half .. 4 half + 3 of the word, of a pair of keys
                         const uint32_t sel = half ? 0x7632u : 0x5410u;
                         const uint32_t u = __byte_perm(v[0][w], v[1][w], sel), y = __byte_perm(v[2][w], v[3][w], sel);
-                        constexpr uint32_t kEight = 0x80088008u, kOne = 0x3c003c00u, kSixteenth = 0x2c002c00u;
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
                             const uint32_t us = q ? u >> 8 : u, ys = q ? y >> 8 : y;
+                            constexpr uint32_t kEight = 0x80088008u, kOne = 0x3c003c00u, kSixteenth = 0x2c002c00u;
                             const uint32_t a0 = hfma2(nib_lo(us), kOne, kEight);
                             const uint32_t a1 = hfma2(nib_hi(us), kSixteenth, kEight);
                             const uint32_t a2 = hfma2(nib_lo(ys), kOne, kEight);
@@ -676,6 +708,8 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
 
         // ---- the unit's end, or the share's: join the warps ----
         if (flags & kUnitEnds) {
+            // the parts are free once all warps have read the last unit's
+            if (joins && !wait_all(bar(C::JOIN + 1), (joins - 1) & 1u, s_abort, a.err)) break;
             float *part = reinterpret_cast<float *>(smem + C::OFF_PART + warp * C::PART);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -703,9 +737,9 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
             const int64_t whole_at = desc->prefix ? a.T * H : 0;
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::JOIN));
-            if (!__all_sync(0xffffffffu, wait_bounded_err(bar(C::JOIN), joins & 1u, s_abort, kSiteKvWait, kWaitLimitNs,
-                                                          false, a.err)))
-                break;
+            const int parts = desc->parts;
+            int2 *rec = p.parts + whole_at;
+            if (!wait_all(bar(C::JOIN), joins & 1u, s_abort, a.err)) break;
             const float *all = reinterpret_cast<const float *>(smem + C::OFF_PART);
             for (int u = tid; u < rows * (D / 4); u += 32 * WARPS) {
                 const int row = u / (D / 4), d = 4 * (u % (D / 4));
@@ -727,6 +761,7 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
                 const int j = tile * R + row, i = j / p.G;
                 const int64_t at = int64_t(q0 + i) * H + h * p.G + (j - i * p.G);
                 v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
+                if (d == 0 && parts) rec[at] = make_int2(blockIdx.x, parts);
                 if (place == kWhole && !p.shared) {
                     *reinterpret_cast<uint2 *>(a.out + at * D + d) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
                     if (a.lse && d == 0) a.lse[at] = lse * 0.6931471805599453f;
@@ -736,12 +771,8 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
                     if (d == 0) (place == kWhole ? p.whole_l : p.slot_l)[k] = lse;
                 }
             }
-            // the parts are free again once all have read them
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::JOIN + 1));
-            if (!__all_sync(0xffffffffu, wait_bounded_err(bar(C::JOIN + 1), joins & 1u, s_abort, kSiteKvWait,
-                                                          kWaitLimitNs, false, a.err)))
-                break;
             ++joins;
         }
         __syncwarp();
@@ -750,84 +781,119 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
 }
 
 // ---- joining partial rows ---------------------------------------------------------
-// A block per output row: its parts are the slots of the blocks that its unit was cut
-// over, in order; behind a prefix, those of both units.  Four warps take every fourth
-// part, then join.
-template <int D, int R>
+// A row's parts are the slots of the blocks that its unit was cut over, in order; behind a
+// prefix, those of both units.  WARPS_PER_ROW = 1: four rows per block, or 4: one, its warps
+// taking every fourth part (few rows, each cut over many blocks).  A warp's lanes first read
+// the parts' sums, 32 at a time, then add up the parts' values with the weights that result.
+template <int D, int R, int WARPS_PER_ROW>
 __global__ void __launch_bounds__(128) kq_kv_combine_kernel(const __grid_constant__ Plan p) {
     __shared__ float so[4][D], sl[4], sw[4];
     const KvAttnArgs &a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, H = a.q_heads;
     griddep_wait();
     griddep_launch_dependents();
-    const int64_t at = blockIdx.x;
-    const int t = int(at / H), head = int(at % H), h = head / p.G;
-    int64_t b = t;
-    int i = 0;
-    if (a.q_start) {
-        int lo = 0, hi = int(a.B);
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (a.q_start[mid + 1] <= t) lo = mid + 1;
-            else hi = mid;
+    const int64_t rows = a.T * H;
+    const int64_t at = WARPS_PER_ROW == 4 ? blockIdx.x : int64_t(blockIdx.x) * 4 + warp;
+    const bool real = at < rows && at < int64_t(all_queries(a)) * H;  // not padding behind the last sequence
+    int2 rec[2] = {make_int2(0, 0), make_int2(0, 0)};
+    int row[2] = {0, 0};
+    if (real) {
+        rec[0] = p.parts[at];
+        if (p.shared) rec[1] = p.parts[rows + at];
+    }
+    if (rec[0].y < 1 || rec[0].x < 0 || rec[0].x + rec[0].y > p.ctas || (!p.shared && rec[0].y == 1)) return;
+    if (p.shared && (rec[1].y < 1 || rec[1].x < 0 || rec[1].x + rec[1].y > p.ctas)) return;
+    const int n = rec[0].y + rec[1].y;
+    if (rec[0].y > 1 || rec[1].y > 1) {  // the row's place in its unit's tile
+        const int t = int(at / H), head = int(at - int64_t(t) * H), g = head % p.G;
+        int q0 = t;
+        if (a.q_start) {
+            int lo = 0, hi = int(a.B);
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (a.q_start[mid + 1] <= t) lo = mid + 1;
+                else hi = mid;
+            }
+            q0 = a.q_start[lo];
         }
-        if (lo == int(a.B)) return;  // padding behind the last sequence
-        b = lo;
-        i = t - a.q_start[lo];
+        row[0] = ((t - q0) * p.G + g) % R;
+        row[1] = (t * p.G + g) % R;
     }
-    if (i >= a.max_q) return;
-    const int64_t total = p.cum[a.B + p.shared], shares = min(int64_t(p.ctas), total);
-    // of each unit: its first slot (or the row's whole place) and the number of parts
-    int64_t first[2];
-    int parts[2] = {0, 0}, row[2];
-    for (int u = 0; u < 1 + p.shared; ++u) {
-        const int64_t sb = u ? a.B : b, c0 = p.cum[sb], c1 = p.cum[sb + 1];
-        int q0, m;
-        queries_of(a, b, q0, m);
-        m = u ? all_queries(a) : min(m, a.max_q);
-        const int tiles = (m * p.G + R - 1) / R, j = (u ? t : i) * p.G + head - h * p.G;
-        const int64_t N = (c1 - c0) / (int64_t(tiles) * a.c.heads);
-        const int64_t g0 = c0 + (int64_t(h) * tiles + j / R) * N;
-        first[u] = ((g0 + 1) * shares - 1) / total;
-        parts[u] = int(((g0 + N) * shares - 1) / total - first[u]) + 1;
-        row[u] = j % R;
-        if (parts[u] < 1 || first[u] < 0 || first[u] + parts[u] > p.ctas) return;  // q_start is not ascending
-    }
-    if (!p.shared && parts[0] == 1) return;  // written by its block
+    // where part k lies: its index among the partial (or whole) rows
+    auto place = [&](int k, bool &whole) -> int64_t {
+        const int u = k >= rec[0].y;
+        const int i = u ? k - rec[0].y : k;
+        whole = rec[u].y == 1;
+        // a unit's first block holds it as its last unit, the others as their first
+        return whole ? u * rows + at : (int64_t(rec[u].x + i) * 2 + (i == 0 ? 1 : 0)) * R + row[u];
+    };
     float top = -INFINITY, wsum = 0.0f;
     float v[D / 32];
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) v[e] = 0.0f;
-    for (int k = warp; k < parts[0] + parts[1]; k += 4) {
-        const int u = k >= parts[0];
-        const int n = u ? k - parts[0] : k;
-        const bool whole = parts[u] == 1;
-        // a unit's first block holds it as its last unit, the others as their first
-        const int64_t place = whole ? u * a.T * H + at : ((first[u] + n) * 2 + (n == 0 ? 1 : 0)) * R + row[u];
-        const float l = (whole ? p.whole_l : p.slot_l)[place];
-        const float *src = (whole ? p.whole_o : p.slot_o) + place * D + lane * (D / 32);
-        if (l == -INFINITY) continue;
-        const float nt = fmaxf(top, l);
-        const float f = ex2(top - nt), w = ex2(l - nt);
+    const int first = WARPS_PER_ROW == 4 ? warp : 0;
+    for (int k0 = first; k0 < n; k0 += 32 * WARPS_PER_ROW) {
+        const int mine = k0 + lane * WARPS_PER_ROW;
+        float l = -INFINITY;
+        int64_t from = 0;
+        bool whole = false;
+        if (mine < n) {
+            from = place(mine, whole);
+            l = (whole ? p.whole_l : p.slot_l)[from];
+        }
+        const float *src = (whole ? p.whole_o : p.slot_o) + from * D;
+        float m = l;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float nt = fmaxf(top, m);
+        float w = l == -INFINITY ? 0.0f : ex2(l - nt);
+        const float f = top == -INFINITY ? 0.0f : ex2(top - nt);
         top = nt;
-        wsum = wsum * f + w;
+        float s = w;
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) v[e] = v[e] * f + src[e] * w;
-    }
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        wsum = wsum * f + s;
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) so[warp][lane * (D / 32) + e] = v[e];
-    if (lane == 0) sl[warp] = top, sw[warp] = wsum;
-    __syncthreads();
-    top = fmaxf(fmaxf(sl[0], sl[1]), fmaxf(sl[2], sl[3]));
-    float w = 0.0f, r = 0.0f;
-    for (int k = 0; k < 4; ++k) {
-        if (sw[k] == 0.0f) continue;  // no part with a key
-        const float f = ex2(sl[k] - top);
-        w += sw[k] * f;
-        if (tid < D) r += so[k][tid] * f;
+        for (int e = 0; e < D / 32; ++e) v[e] *= f;
+        const int cnt = min(32, (n - k0 + WARPS_PER_ROW - 1) / WARPS_PER_ROW);
+#pragma unroll 4
+        for (int k = 0; k < cnt; ++k) {
+            const float wk = __shfl_sync(0xffffffffu, w, k);
+            const float *sk = reinterpret_cast<const float *>(
+                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), k));
+            if constexpr (D == 128) {
+                const float4 z = reinterpret_cast<const float4 *>(sk)[lane];
+                v[0] = fmaf(z.x, wk, v[0]), v[1] = fmaf(z.y, wk, v[1]);
+                v[2] = fmaf(z.z, wk, v[2]), v[3] = fmaf(z.w, wk, v[3]);
+            } else {
+                const float2 z = reinterpret_cast<const float2 *>(sk)[lane];
+                v[0] = fmaf(z.x, wk, v[0]), v[1] = fmaf(z.y, wk, v[1]);
+            }
+        }
     }
-    if (tid < D) a.out[at * D + tid] = float_to_bf16_bits(w == 0.0f ? 0.0f : r / w);
-    if (tid == 0 && a.lse) a.lse[at] = w == 0.0f ? -INFINITY : (top + lg2(w)) * 0.6931471805599453f;
+    if constexpr (WARPS_PER_ROW == 4) {
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) so[warp][lane * (D / 32) + e] = v[e];
+        if (lane == 0) sl[warp] = top, sw[warp] = wsum;
+        __syncthreads();
+        if (warp) return;
+        top = fmaxf(fmaxf(sl[0], sl[1]), fmaxf(sl[2], sl[3]));
+        wsum = 0.0f;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) v[e] = 0.0f;
+        for (int k = 0; k < 4; ++k) {
+            if (sw[k] == 0.0f) continue;  // no part with a key
+            const float f = ex2(sl[k] - top);
+            wsum += sw[k] * f;
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e) v[e] += so[k][lane * (D / 32) + e] * f;
+        }
+    }
+    const float inv = wsum == 0.0f ? 0.0f : 1.0f / wsum;
+    uint32_t *out = reinterpret_cast<uint32_t *>(a.out + at * D) + lane * (D / 64);
+#pragma unroll
+    for (int e = 0; e < D / 64; ++e) out[e] = pack_bf16x2(v[2 * e] * inv, v[2 * e + 1] * inv);
+    if (lane == 0 && a.lse) a.lse[at] = wsum == 0.0f ? -INFINITY : (top + lg2(wsum)) * 0.6931471805599453f;
 }
 
 // ---- host side ------------------------------------------------------------------------
@@ -838,18 +904,18 @@ int row_tile(int G, int max_q) { return int64_t(G) * max_q <= 8 ? 8 : 16; }
 uint64_t align256(uint64_t x) { return (x + 255) & ~uint64_t(255); }
 
 // The workspace's parts, from `base`; returns the bytes.
-uint64_t lay_out(Plan *p, unsigned char *base, int64_t T, int64_t B, int H, int D, int R) {
+uint64_t lay_out(Plan *p, unsigned char *base, int64_t T, int H, int D, int R) {
     uint64_t at = 0;
     auto take = [&](uint64_t bytes) {
         unsigned char *r = base + at;
         at += align256(bytes);
         return r;
     };
-    unsigned char *cum = take(uint64_t(B + 2) * 8);
+    unsigned char *parts = take(uint64_t(T) * H * 2 * 8);
     unsigned char *so = take(uint64_t(kMaxCtas) * 2 * R * D * 4), *sl = take(uint64_t(kMaxCtas) * 2 * R * 4);
     unsigned char *wo = take(uint64_t(T) * H * 2 * D * 4), *wl = take(uint64_t(T) * H * 2 * 4);
     if (p) {
-        p->cum = reinterpret_cast<int64_t *>(cum);
+        p->parts = reinterpret_cast<int2 *>(parts);
         p->slot_o = reinterpret_cast<float *>(so);
         p->slot_l = reinterpret_cast<float *>(sl);
         p->whole_o = reinterpret_cast<float *>(wo);
@@ -872,7 +938,9 @@ cudaError_t launch_rows(Plan &p, int num_sms, int device, cudaStream_t stream) {
     p.ctas = num_sms * C::OCC < kMaxCtas ? num_sms * C::OCC : kMaxCtas;
     cudaError_t e = launch_overlapped(kern, unsigned(p.ctas), R_THREADS, C::SMEM, stream, p);
     if (e != cudaSuccess) return e;
-    return launch_overlapped(kq_kv_combine_kernel<D, C::R>, unsigned(p.a.T * p.a.q_heads), 128, 0, stream, p);
+    const int64_t rows = p.a.T * p.a.q_heads;
+    return rows <= 2048 ? launch_overlapped(kq_kv_combine_kernel<D, C::R, 4>, unsigned(rows), 128, 0, stream, p)
+                        : launch_overlapped(kq_kv_combine_kernel<D, C::R, 1>, unsigned((rows + 3) / 4), 128, 0, stream, p);
 }
 
 template <int D, int NT>
@@ -883,8 +951,8 @@ cudaError_t launch_cap(Plan &p, int num_sms, int device, cudaStream_t stream) {
 
 }  // namespace
 
-uint64_t kv_attention_workspace_bytes(int64_t T, int64_t B, int q_heads, int kv_heads, int head_dim, int max_q) {
-    return lay_out(nullptr, nullptr, T, B, q_heads, head_dim, row_tile(q_heads / kv_heads, max_q));
+uint64_t kv_attention_workspace_bytes(int64_t T, int64_t, int q_heads, int kv_heads, int head_dim, int max_q) {
+    return lay_out(nullptr, nullptr, T, q_heads, head_dim, row_tile(q_heads / kv_heads, max_q));
 }
 
 cudaError_t launch_kv_attention(const KvAttnArgs &a, int num_sms, int device, cudaStream_t stream) {
@@ -893,7 +961,7 @@ cudaError_t launch_kv_attention(const KvAttnArgs &a, int num_sms, int device, cu
     p.G = a.q_heads / a.c.heads;
     p.shared = a.prefix_pages != nullptr;
     const int R = row_tile(p.G, a.max_q);
-    lay_out(&p, a.workspace, a.T, a.B, a.q_heads, a.c.D, R);
+    lay_out(&p, a.workspace, a.T, a.q_heads, a.c.D, R);
     if (a.c.D == 128)
         return R == 8 ? launch_cap<128, 1>(p, num_sms, device, stream) : launch_cap<128, 2>(p, num_sms, device, stream);
     return R == 8 ? launch_cap<64, 1>(p, num_sms, device, stream) : launch_cap<64, 2>(p, num_sms, device, stream);
