@@ -3,81 +3,440 @@
 //
 //     q_out = R(pos) q Pq,   y = R(pos) k Pk  or  v Pv,
 //     s = alpha max|y| / 7,  code = clamp(round_half_even(y / s), -8, 7)
+//
+// All rows of one kind (queries, keys, values) are one [rows x D] [D x D] product:
+// tiles of 128 rows, a thread and a TMEM lane per row, D its head_dim.  The bytes of
+// the rows bound it (2 D in, and 2 D or D / 2 + 4 out), so a row moves once each way:
+//   - a thread's row comes by one bulk copy into a padded row of shared memory (reads
+//     16 bytes a lane without conflicts) and a query row leaves from the same place;
+//     the row for the tile after next is fetched as soon as the place is free.
+//   - the thread rotates its row in fp32 and splits each value into bf16 terms by
+//     truncation, which go to TMEM as the A operand: two terms for queries (16 bits;
+//     the result is rounded to bf16), three for keys (all 24 bits of the fp32 value),
+//     one for values (they are bf16).  The factor is the B operand in shared memory,
+//     as it lies in memory (N contiguous).
+//   - 256 TMEM columns a warpgroup: terms in 128, the fp32 row in 128.  The keys'
+//     largest term waits for the products of the other two and takes their columns
+//     (smallest first: the tensor core truncates the sum at every addition).
+//   - two warpgroups a block and one block an SM, on tiles of one kind at a time.
+//
+// Codes of exact arithmetic: fp32 leaves y / s uncertain by up to kBorder of its
+// largest value; a row with a value nearer than that to a rounding border (a row in a
+// few hundred) is computed again by its warp in fp64, scale and all.
+#include <mutex>
+
 #include "kq_common.cuh"
 #include "kq_internal.h"
+#include "kq_tc05_ptx.cuh"
+#include "kq_wait.cuh"
 
 namespace kq {
 namespace {
 
-constexpr int A_THREADS = 128;
+using namespace tc;
 
-// Element i of a row rotated by its token's angles; exact products in fp64.
-__device__ __forceinline__ double rotated(const uint16_t *x, int i, const float *cs, int rope_dim, bool inter) {
-    const double xi = double(bf16_bits_to_float(x[i]));
-    if (i >= rope_dim) return xi;
+constexpr int A_THREADS = 256;     // two warpgroups
+constexpr float kBorder = 0x1p-19f;  // of max|y|: bound of fp32's error in a row
+enum : unsigned { kSiteKvAppendWait = 524288u };
+
+template <int D>
+struct ACfg {
+    static constexpr int ROW = D * 2 + 16;            // a row's place in shared memory, padded
+    static constexpr int STAGE = 128 * ROW;
+    static constexpr int OFF_X = D * D * 2;           // after the factor
+    static constexpr int OFF_Y = OFF_X + 4 * STAGE;   // fp64 rows of the exact path, one per warp
+    static constexpr int OFF_BAR = OFF_Y + 8 * D * 8;
+    static constexpr int OFF_MISC = OFF_BAR + 8 * 6;  // full[2][2], mma[2]
+    static constexpr int SMEM = OFF_MISC + 16 + 1024;
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+// One row's exact codes and scale, by a whole warp: lane l has the columns l, l + 32, ...
+template <int D>
+__device__ __noinline__ void exact_row(const unsigned char *xrow, const unsigned char *factor, double *xs,
+                                       const float *cs, int rope_dim, bool inter, float alpha, uint8_t *codes,
+                                       float *scale) {
+    const int lane = threadIdx.x & 31, half = rope_dim >> 1;
+    const uint16_t *x = reinterpret_cast<const uint16_t *>(xrow);
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) {
+        const int i = lane + 32 * e;
+        double v = double(bf16_bits_to_float(x[i]));
+        if (i < rope_dim) {
+            const int k = inter ? i >> 1 : (i < half ? i : i - half);  // the pair's angle
+            const bool first = inter ? (i & 1) == 0 : i < half;
+            const int j = inter ? i ^ 1 : (first ? i + half : i - half);
+            const double w = double(bf16_bits_to_float(x[j])), c = double(cs[k]), s = double(cs[half + k]);
+            v = first ? v * c - w * s : w * s + v * c;
+        }
+        xs[i] = v;
+    }
+    __syncwarp();
+    double y[D / 32];
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) y[e] = 0.0;
+    for (int k = 0; k < D; ++k) {
+        const double xk = xs[k];
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) {
+            const int n = lane + 32 * e;
+            const uint16_t w = *reinterpret_cast<const uint16_t *>(factor + (n >> 6) * D * 128 + k * 128 +
+                                                                   ((((n & 63) >> 3) ^ (k & 7)) << 4) + 2 * (n & 7));
+            y[e] = fma(xk, double(bf16_bits_to_float(w)), y[e]);
+        }
+    }
+    double m = 0.0;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) m = fmax(m, fabs(y[e]));
+    for (int o = 16; o; o >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const double s = double(alpha) * m / 7.0;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) {
+        const int c = s > 0.0 ? int(rint(fmin(fmax(y[e] / s, -8.0), 7.0))) & 15 : 0;
+        const int up = __shfl_down_sync(0xffffffffu, c, 1);
+        if ((lane & 1) == 0) codes[(lane >> 1) + 16 * e] = uint8_t(c | (up << 4));
+    }
+    if (lane == 0) *scale = float(s);
+    __syncwarp();
+}
+
+// Four consecutive pairs of fp32 values -> words of their leading bf16 terms (truncated), the
+// values less those terms left behind; exact.
+__device__ __forceinline__ void take_term(float (&v)[8], uint32_t (&w)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t a = __float_as_uint(v[2 * i]), b = __float_as_uint(v[2 * i + 1]);
+        w[i] = __byte_perm(a, b, 0x7632);
+        v[2 * i] -= __uint_as_float(a & 0xffff0000u);
+        v[2 * i + 1] -= __uint_as_float(b & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void unpack8(const uint4 &u, float (&v)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+
+// The row's values, rotated, eight at a time: calls put(first element, values).
+template <int D, typename F>
+__device__ __forceinline__ void rotated_row(const unsigned char *xrow, const float *cs, int rope_dim, bool inter,
+                                            F put) {
+    const uint4 *x = reinterpret_cast<const uint4 *>(xrow);
     const int half = rope_dim >> 1;
-    const int a = inter ? i >> 1 : (i < half ? i : i - half);  // the pair's angle
-    const bool first = inter ? (i & 1) == 0 : i < half;
-    const int j = inter ? i ^ 1 : (first ? i + half : i - half);
-    const double xj = double(bf16_bits_to_float(x[j]));
-    const double c = double(cs[a]), s = double(cs[half + a]);
-    return first ? xi * c - xj * s : xj * s + xi * c;
+    if (inter) {
+        for (int i = 0; i < rope_dim; i += 8) {
+            float v[8];
+            unpack8(x[i >> 3], v);
+            const float4 c = __ldg(reinterpret_cast<const float4 *>(cs + (i >> 1)));
+            const float4 s = __ldg(reinterpret_cast<const float4 *>(cs + half + (i >> 1)));
+            const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float a = v[2 * e], b = v[2 * e + 1];
+                v[2 * e] = fmaf(a, cc[e], -(b * ss[e]));
+                v[2 * e + 1] = fmaf(b, cc[e], a * ss[e]);
+            }
+            put(i, v);
+        }
+    } else {
+        for (int i = 0; i < half; i += 8) {
+            float a[8], b[8];
+            unpack8(x[i >> 3], a);
+            unpack8(x[(i + half) >> 3], b);
+            float c[8], s[8];
+#pragma unroll
+            for (int e = 0; e < 8; e += 4) {
+                const float4 u = __ldg(reinterpret_cast<const float4 *>(cs + i + e));
+                const float4 w = __ldg(reinterpret_cast<const float4 *>(cs + half + i + e));
+                c[e] = u.x, c[e + 1] = u.y, c[e + 2] = u.z, c[e + 3] = u.w;
+                s[e] = w.x, s[e + 1] = w.y, s[e + 2] = w.z, s[e + 3] = w.w;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float p = a[e], q = b[e];
+                a[e] = fmaf(p, c[e], -(q * s[e]));
+                b[e] = fmaf(q, c[e], p * s[e]);
+            }
+            put(i, a);
+            put(i + half, b);
+        }
+    }
+    for (int i = rope_dim; i < D; i += 8) {
+        float v[8];
+        unpack8(x[i >> 3], v);
+        put(i, v);
+    }
+}
+
+// round_half_even(y * inv) as an int for |y * inv| < 2^22 (alpha >= 2^-19): the low mantissa bits
+// after adding 1.5 * 2^23; `off` keeps the largest distance to the rounded value.
+__device__ __forceinline__ int round_off(uint32_t ybits, float inv, float &off) {
+    const float y = __uint_as_float(ybits), b = fmaf(y, inv, 12582912.0f);
+    off = fmaxf(off, fabsf(fmaf(y, inv, -(b - 12582912.0f))));
+    return int(__float_as_uint(b)) - 0x4B400000;
 }
 
 template <int D>
-__global__ void __launch_bounds__(A_THREADS) kq_kv_append_kernel(const __grid_constant__ KvAppendArgs a) {
-    __shared__ double xs[D];
-    __shared__ double red[4];
-    __shared__ uint8_t cs[D];
-    const int H = a.q_heads, Hk = a.c.heads, tid = threadIdx.x;
-    const int rows = H + 2 * Hk;
+__global__ void __launch_bounds__(A_THREADS, 1) kq_kv_append_kernel(const __grid_constant__ KvAppendArgs a) {
+    using C = ACfg<D>;
+    extern __shared__ __align__(1024) unsigned char a_raw[];
+    const uint32_t raw_addr = smem_u32(a_raw), sbase = (raw_addr + 1023u) & ~1023u;
+    unsigned char *smem = a_raw + (sbase - raw_addr);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2, r = tid & 127;
+    auto bar = [&](int i) -> uint32_t { return sbase + uint32_t(C::OFF_BAR + 8 * i); };
+    const uint32_t mma_bar = bar(4 + wg);
+    volatile int *s_abort = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
+    if (tid == 0) {
+        for (int i = 0; i < 4; ++i) mbar_init(bar(i), 128);
+        mbar_init(bar(4), 1);
+        mbar_init(bar(5), 1);
+        *s_abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(sbase + C::OFF_MISC, 512);
+        tmem_relinquish();
+    }
+    const int H = a.q_heads, Hk = a.c.heads, psh = a.c.page_shift;
+    const int64_t rows_q = a.T * H, rows_k = a.T * Hk;
+    const int64_t tq = (rows_q + 127) / 128, tk = (rows_k + 127) / 128, tiles = tq + 2 * tk;
+    // the block's tiles, in order: queries, then keys, then values; its warpgroups take turns
+    const int64_t t0 = blockIdx.x * tiles / gridDim.x, t1 = (blockIdx.x + 1) * tiles / gridDim.x;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + C::OFF_MISC) + uint32_t(256 * wg);
     griddep_wait();
     griddep_launch_dependents();
-    for (int64_t u = blockIdx.x; u < a.T * rows; u += gridDim.x) {
-        const int64_t t = u / rows;
-        const int r = int(u % rows);
-        const int kind = r < H ? 0 : r < H + Hk ? 1 : 2;
-        const int h = kind == 0 ? r : kind == 1 ? r - H : r - H - Hk;
-        const uint16_t *x = kind == 0 ? a.q + t * a.q_stride : kind == 1 ? a.k + t * a.k_stride : a.v + t * a.v_stride;
-        const uint16_t *P = kind == 0 ? a.Pq : kind == 1 ? a.Pk : a.Pv;
-        x += int64_t(h) * D;
-        bool pos_ok = true;
-        const float *table = nullptr;
-        if (a.rope) {
-            const int64_t pos = a.positions[t];
-            pos_ok = pos >= 0 && pos < a.rope_positions;
-            table = a.rope + (pos_ok ? pos : 0) * a.rope_dim;
+
+    auto kind_of = [&](int64_t tile) { return tile < tq ? 0 : tile < tq + tk ? 1 : 2; };
+    // This thread's row of a tile: token and head; false past the last row.
+    auto row_of = [&](int64_t tile, int kind, int &t, int &h) -> bool {
+        const int64_t row = (tile - (kind == 0 ? 0 : kind == 1 ? tq : tq + tk)) * 128 + r;
+        const int heads = kind == 0 ? H : Hk;
+        t = int(row / heads);
+        h = int(row - int64_t(t) * heads);
+        return row < (kind == 0 ? rows_q : rows_k);
+    };
+    unsigned char *place[2] = {smem + C::OFF_X + (2 * wg) * C::STAGE + r * C::ROW,
+                               smem + C::OFF_X + (2 * wg + 1) * C::STAGE + r * C::ROW};
+    auto fetch = [&](int64_t tile, int stage) {
+        if (tile >= t1) return;
+        const int kind = kind_of(tile);
+        int t, h;
+        const uint32_t b = bar(2 * wg + stage);
+        if (row_of(tile, kind, t, h)) {
+            const uint16_t *x = kind == 0   ? a.q + int64_t(t) * a.q_stride
+                                : kind == 1 ? a.k + int64_t(t) * a.k_stride
+                                            : a.v + int64_t(t) * a.v_stride;
+            mbar_arrive_expect_tx(b, D * 2);
+            bulk_load(smem_u32(place[stage]), x + int64_t(h) * D, D * 2, b);
+        } else {
+            mbar_arrive(b);
         }
-        __syncthreads();
-        if (tid < D)
-            xs[tid] = rotated(x, tid, table, kind < 2 && a.rope ? a.rope_dim : 0, a.rope_interleaved != 0);
-        __syncthreads();
-        double y = 0.0;
-        if (tid < D)
-            for (int i = 0; i < D; ++i) y += xs[i] * double(bf16_bits_to_float(P[i * D + tid]));
-        if (kind == 0) {
-            if (tid < D) a.q_out[(t * H + h) * D + tid] = pos_ok ? float_to_bf16_bits(float(y)) : 0;
-            if (!pos_ok && tid == 0) atomicOr(a.err, kSiteKvAppend);
-            continue;
+    };
+    fetch(t0 + wg, 0);
+    fetch(t0 + wg + 2, 1);
+
+    const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16, ta = tmem + lanes, td = ta + 128;
+    constexpr uint32_t idesc = idesc_bf16_f32_bn(128, D);
+    // D (+)= terms from column `col` of A times the factor, by one thread of the warpgroup.
+    auto multiply = [&](int terms, bool accumulate) {
+        tmem_wait_st();
+        tc_fence_before();
+        named_barrier_sync(1 + wg, 128);
+        if ((warp & 3) == 0) {
+            tc_fence_after();
+            if (elect_one()) {
+                // the smallest term first: the sum is truncated at every addition
+                for (int term = terms - 1; term >= 0; --term)
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        mma_ts(tmem + 128, tmem + uint32_t(64 * term + 8 * k),
+                               sdesc_nmajor_sw128(sbase + uint32_t(2048 * k), D * 128), idesc,
+                               accumulate || term + 1 < terms || k);
+                tc_commit(mma_bar);
+            }
+            __syncwarp();
         }
-        double m = fabs(y);
-        for (int o = 16; o; o >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if ((tid & 31) == 0) red[tid >> 5] = m;
-        __syncthreads();
-        m = fmax(fmax(red[0], red[1]), fmax(red[2], red[3]));
-        const double s = double(kind == 1 ? a.alpha_k : a.alpha_v) * m / 7.0;
-        if (tid < D) cs[tid] = uint8_t(int(s > 0.0 ? rint(fmin(fmax(y / s, -8.0), 7.0)) : 0.0) & 15);
-        __syncthreads();
-        const int64_t slot = a.slots[t], psize = int64_t(1) << a.c.page_shift;
-        if (slot < 0) continue;
-        if (slot >= a.c.pages * psize || !pos_ok) {
-            if (tid == 0) atomicOr(a.err, kSiteKvAppend);
-            continue;
+    };
+    uint32_t products = 0, turns = 0;
+    auto multiplied = [&] {
+        wait_bounded_err(mma_bar, products++ & 1u, s_abort, kSiteKvAppendWait, kWaitLimitNs, false, a.err);
+        __syncwarp();
+        tc_fence_after();
+    };
+
+    int have = -1;  // the factor in shared memory
+    // Both warpgroups go through the same kinds; `base` is the first of a pair of tiles.
+    for (int64_t first = t0; first < t1;) {
+        const int kind = kind_of(first);
+        const int64_t end = min(t1, kind == 0 ? tq : kind == 1 ? tq + tk : tiles);
+        if (kind != have) {
+            __syncthreads();  // no product reads the last factor any more
+            const uint16_t *P = kind == 0 ? a.Pq : kind == 1 ? a.Pk : a.Pv;
+#pragma unroll
+            for (int u = tid; u < D * D / 8; u += A_THREADS) {
+                const int k = u / (D / 8), n = 8 * (u % (D / 8));
+                *reinterpret_cast<uint4 *>(smem + (n >> 6) * D * 128 + k * 128 + ((((n & 63) >> 3) ^ (k & 7)) << 4)) =
+                    __ldg(reinterpret_cast<const uint4 *>(P + k * D + n));
+            }
+            fence_proxy_async_smem();
+            __syncthreads();
+            have = kind;
         }
-        const int64_t row = ((slot >> a.c.page_shift) * Hk + h) * psize + (slot & (psize - 1));
-        uint8_t *codes = kind == 1 ? a.c.k_codes : a.c.v_codes;
-        if (tid < D / 2) codes[row * (D / 2) + tid] = uint8_t(cs[2 * tid] | (cs[2 * tid + 1] << 4));
-        if (tid == 0) (kind == 1 ? a.c.k_scale : a.c.v_scale)[row] = float(s);
+        // this warpgroup's tiles of the kind: those of its parity from t0
+        int64_t tile = first + ((first - t0 + wg) & 1);
+        for (; tile < end; tile += 2, ++turns) {
+            const int stage = int(turns & 1u);
+            int t, h;
+            const bool real = row_of(tile, kind, t, h);
+            int64_t slot = -1;
+            bool pos_ok = true;
+            const float *cs = nullptr;
+            if (real) {
+                if (kind != 0) slot = a.slots[t];
+                if (a.rope_dim) {
+                    const int64_t pos = a.positions[t];
+                    pos_ok = pos >= 0 && pos < a.rope_positions;
+                    if (!pos_ok) atomicOr(a.err, kSiteKvAppend);
+                    cs = a.rope + (pos_ok ? pos : 0) * a.rope_dim;
+                }
+                if (kind != 0 && slot >= a.c.pages << psh) {
+                    atomicOr(a.err, kSiteKvAppend);
+                    slot = -1;
+                }
+            }
+            wait_bounded_err(bar(2 * wg + stage), (turns >> 1) & 1u, s_abort, kSiteKvAppendWait, kWaitLimitNs, false,
+                             a.err);
+            __syncwarp();
+            const unsigned char *x = place[stage];
+            const int rope = kind == 2 || !real ? 0 : a.rope_dim;
+            const int rope_w = __reduce_max_sync(0xffffffffu, rope);  // rows past the last follow their warp
+            if (cs == nullptr) cs = a.rope;
+            const bool inter = a.rope_interleaved != 0;
+            if (kind == 2) {
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    const uint4 u = reinterpret_cast<const uint4 *>(x)[i];
+                    tmem_st_32x32b_x4(ta + uint32_t(4 * i), u.x, u.y, u.z, u.w);
+                }
+                multiply(1, false);
+            } else {
+                // queries: both terms; keys: the second and third, and then the first
+                rotated_row<D>(x, cs, rope_w, inter, [&](int i, float (&v)[8]) {
+                    uint32_t w[4];
+                    take_term(v, w);
+                    if (kind == 1) take_term(v, w);
+                    tmem_st_32x32b_x4(ta + uint32_t(i >> 1), w[0], w[1], w[2], w[3]);
+                    tmem_st_32x32b_x4(ta + 64 + uint32_t(i >> 1), pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                      pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+                });
+                multiply(2, false);
+                if (kind == 1) {
+                    multiplied();
+                    rotated_row<D>(x, cs, rope_w, inter, [&](int i, float (&v)[8]) {
+                        uint32_t w[4];
+                        take_term(v, w);
+                        tmem_st_32x32b_x4(ta + uint32_t(i >> 1), w[0], w[1], w[2], w[3]);
+                    });
+                    multiply(1, true);
+                }
+            }
+            multiplied();
+            if (kind == 0) {
+                // ---- queries out: bf16, through the row's place ----
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(td + uint32_t(32 * c), v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            w[k] = pos_ok ? pack_bf16x2(__uint_as_float(v[8 * e + 2 * k]),
+                                                        __uint_as_float(v[8 * e + 2 * k + 1]))
+                                          : 0u;
+                        reinterpret_cast<uint4 *>(place[stage])[4 * c + e] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+                fence_proxy_async_smem();
+                if (real) {
+                    bulk_store(a.q_out + (int64_t(t) * H + h) * D, smem_u32(place[stage]), D * 2);
+                    bulk_commit();
+                    bulk_wait_read<0>();
+                }
+            } else {
+                // ---- a row of the cache ----
+                float m = 0.0f;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(td + uint32_t(32 * c), v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2)
+                        m = fmax3(m, fabsf(__uint_as_float(v[e])), fabsf(__uint_as_float(v[e + 1])));
+                }
+                const float alpha = kind == 1 ? a.alpha_k : a.alpha_v;
+                const float sc = __fdiv_rn(alpha * m, 7.0f);
+                const float inv = sc > 0.0f ? fminf(__frcp_rn(sc), 3.0e38f) : 0.0f;
+                const bool store = real && slot >= 0 && pos_ok;
+                const int64_t row = store ? (((slot >> psh) * Hk + h) << psh) + (slot & ((int64_t(1) << psh) - 1)) : 0;
+                uint8_t *codes = (kind == 1 ? a.c.k_codes : a.c.v_codes) + row * (D / 2);
+                float *scale = (kind == 1 ? a.c.k_scale : a.c.v_scale) + row;
+                float off = 0.0f;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t v[32], w[4];
+                    tmem_ld_32x32b_x32(td + uint32_t(32 * c), v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t *y = v + 8 * k;
+                        uint32_t p = 0;
+#pragma unroll
+                        for (int e = 6; e >= 0; e -= 2)
+                            p = pack_s4x2(round_off(y[e + 1], inv, off), round_off(y[e], inv, off), p);
+                        w[k] = p;
+                    }
+                    if (store) reinterpret_cast<uint4 *>(codes)[c] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                if (store) *scale = sc;
+                // ---- rows with a value too near a border for fp32, again in fp64 ----
+                // (scales that leave fp32's normal range are among them; a NaN or an infinity is not)
+                const bool near = store && m < 3.0e38f &&
+                                  (off > 0.5f - 7.0f * kBorder / alpha || (m > 0.0f && sc < 1e-30f));
+                uint32_t again = __ballot_sync(0xffffffffu, near);
+                while (again) {
+                    const int src = __ffs(again) - 1;
+                    again &= again - 1;
+                    const uint64_t pc = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(codes), src);
+                    const uint64_t ps = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(scale), src);
+                    const uint64_t pt = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(cs), src);
+                    __syncwarp();
+                    exact_row<D>(x + (src - lane) * C::ROW, smem,
+                                 reinterpret_cast<double *>(smem + C::OFF_Y) + warp * D,
+                                 reinterpret_cast<const float *>(pt), rope_w, inter, alpha,
+                                 reinterpret_cast<uint8_t *>(pc), reinterpret_cast<float *>(ps));
+                }
+            }
+            tc_fence_before();
+            __syncwarp();  // the warp's rows have been read (the exact path reads across lanes)
+            fetch(tile + 4, stage);
+        }
+        first = end;
+    }
+    bulk_wait_read<0>();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
     }
 }
 
@@ -124,11 +483,24 @@ __global__ void __launch_bounds__(256)
 
 }  // namespace
 
+template <int D>
+static cudaError_t launch_append_inst(const KvAppendArgs &a, int num_sms, int device, cudaStream_t stream) {
+    using C = ACfg<D>;
+    auto kern = kq_kv_append_kernel<D>;
+    static std::once_flag once[64];
+    static cudaError_t attr_err[64];
+    if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
+    std::call_once(once[device], [&] {
+        attr_err[device] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    });
+    if (attr_err[device] != cudaSuccess) return attr_err[device];
+    const int64_t tiles = (a.T * a.q_heads + 127) / 128 + 2 * ((a.T * a.c.heads + 127) / 128);
+    return launch_overlapped(kern, unsigned(tiles < num_sms ? tiles : num_sms), A_THREADS, C::SMEM, stream, a);
+}
+
 cudaError_t launch_kv_append(const KvAppendArgs &a, int num_sms, int device, cudaStream_t stream) {
-    const int64_t units = a.T * (a.q_heads + 2 * a.c.heads);
-    const unsigned grid = unsigned(units < 16 * num_sms ? units : 16 * num_sms);
-    return a.c.D == 128 ? launch_overlapped(kq_kv_append_kernel<128>, grid, A_THREADS, 0, stream, a)
-                        : launch_overlapped(kq_kv_append_kernel<64>, grid, A_THREADS, 0, stream, a);
+    return a.c.D == 128 ? launch_append_inst<128>(a, num_sms, device, stream)
+                        : launch_append_inst<64>(a, num_sms, device, stream);
 }
 
 cudaError_t launch_kv_gather(const KvCache &c, const int64_t *slots, uint16_t *k_out, uint16_t *v_out, int64_t T,

@@ -162,6 +162,12 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
+// 32 lanes x 32 bits, 4 columns: thread t -> lane t.
+__device__ __forceinline__ void tmem_st_32x32b_x4(uint32_t taddr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r0), "r"(r1), "r"(r2),
+                 "r"(r3)
+                 : "memory");
+}
 // 32 lanes x 32 bits, 32 columns: thread t <- lane t, registers = columns.
 __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
@@ -335,6 +341,17 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
            | (1u << 10)                       // B format: bf16
            | (uint32_t(N >> 3) << 17)         // N / 8
            | (uint32_t(M >> 4) << 24);        // M / 16
+}
+
+// The same with B laid out along N (MN-major): see sdesc_nmajor_sw128.
+__host__ __device__ constexpr uint32_t idesc_bf16_f32_bn(int M, int N) { return idesc_bf16_f32(M, N) | (1u << 16); }
+
+// Shared-memory matrix descriptor for a B operand whose N index is contiguous, 128-byte
+// swizzle: a row of one k holds 64 values of N (128 B), eight k's make a 1024-byte group,
+// groups follow each other (stride byte offset 1024), and the next 64 values of N lie
+// `next_n` bytes on (leading byte offset).  Advancing K by 16 adds 2048 B.
+__device__ __forceinline__ uint64_t sdesc_nmajor_sw128(uint32_t saddr, uint32_t next_n) {
+    return (uint64_t(kSdescSw128Hi) << 32) | (uint64_t((next_n >> 4) & 0x3FFFu) << 16) | ((saddr >> 4) & 0x3FFFu);
 }
 
 }  // namespace tc
