@@ -7,18 +7,21 @@
 // All rows of one kind (queries, keys, values) are one [rows x D] [D x D] product:
 // tiles of 128 rows, a thread and a TMEM lane per row, D its head_dim.  The bytes of
 // the rows bound it (2 D in, and 2 D or D / 2 + 4 out), so a row moves once each way:
-//   - a thread's row comes by one bulk copy into a padded row of shared memory (reads
-//     16 bytes a lane without conflicts) and a query row leaves from the same place;
-//     the row for the tile after next is fetched as soon as the place is free.
+//   - a warp fetches its 32 rows by cp.async, two rows a step, into padded rows of
+//     shared memory (a thread then reads its row 16 bytes at a time without conflicts),
+//     the rows of the tile after next as soon as their place is free; query rows leave
+//     through the same place, again two whole rows a store.
 //   - the thread rotates its row in fp32 and splits each value into bf16 terms by
 //     truncation, which go to TMEM as the A operand: two terms for queries (16 bits;
 //     the result is rounded to bf16), three for keys (all 24 bits of the fp32 value),
 //     one for values (they are bf16).  The factor is the B operand in shared memory,
 //     as it lies in memory (N contiguous).
-//   - 256 TMEM columns a warpgroup: terms in 128, the fp32 row in 128.  The keys'
-//     largest term waits for the products of the other two and takes their columns
-//     (smallest first: the tensor core truncates the sum at every addition).
-//   - two warpgroups a block and one block an SM, on tiles of one kind at a time.
+//   - two pairs of warpgroups, each with 256 TMEM columns: one warpgroup turns rows
+//     into terms (128 columns), the other takes the fp32 rows (128 columns) while the
+//     first is at its next tile.  The keys' largest term waits for the products of the
+//     other two and takes their columns (smallest first: the tensor core truncates the
+//     sum at every addition).
+//   - one block an SM, on tiles of one kind at a time.
 //
 // Codes of exact arithmetic: fp32 leaves y / s uncertain by up to kBorder of its
 // largest value; a row with a value nearer than that to a rounding border (a row in a
@@ -35,7 +38,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int A_THREADS = 256;     // two warpgroups
+constexpr int A_THREADS = 512;     // two warpgroups that make terms, two that take rows
 constexpr float kBorder = 0x1p-19f;  // of max|y|: bound of fp32's error in a row
 enum : unsigned { kSiteKvAppendWait = 524288u };
 
@@ -44,20 +47,29 @@ struct ACfg {
     static constexpr int ROW = D * 2 + 16;            // a row's place in shared memory, padded
     static constexpr int STAGE = 128 * ROW;
     static constexpr int OFF_X = D * D * 2;           // after the factor
-    static constexpr int OFF_Y = OFF_X + 4 * STAGE;   // fp64 rows of the exact path, one per warp
-    static constexpr int OFF_BAR = OFF_Y + 8 * D * 8;
-    static constexpr int OFF_MISC = OFF_BAR + 8 * 6;  // full[2][2], mma[2]
+    static constexpr int OFF_Y = OFF_X + 4 * STAGE;   // 4 KB for each warp that takes rows
+    static constexpr int OFF_BAR = OFF_Y + 8 * 4096;
+    static constexpr int OFF_MISC = OFF_BAR + 8 * 6;  // of each pair: products done, rows ready, rows taken
     static constexpr int SMEM = OFF_MISC + 16 + 1024;
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
+// 16 bytes to shared memory, of which the first `size` come from `src` and the rest are zeros.
+__device__ __forceinline__ void cp_async16(uint32_t dst, uint64_t src, uint32_t size) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // One row's exact codes and scale, by a whole warp: lane l has the columns l, l + 32, ...
 template <int D>
-__device__ __noinline__ void exact_row(const unsigned char *xrow, const unsigned char *factor, double *xs,
+__device__ __noinline__ void exact_row(const uint16_t *x, const unsigned char *factor, double *xs,
                                        const float *cs, int rope_dim, bool inter, float alpha, uint8_t *codes,
                                        float *scale) {
     const int lane = threadIdx.x & 31, half = rope_dim >> 1;
-    const uint16_t *x = reinterpret_cast<const uint16_t *>(xrow);
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) {
         const int i = lane + 32 * e;
@@ -142,7 +154,7 @@ __device__ __forceinline__ void rotated_row(const unsigned char *xrow, const flo
             put(i, v);
         }
     } else {
-        for (int i = 0; i < half; i += 8) {
+        auto eight = [&](int i) {
             float a[8], b[8];
             unpack8(x[i >> 3], a);
             unpack8(x[(i + half) >> 3], b);
@@ -162,7 +174,13 @@ __device__ __forceinline__ void rotated_row(const unsigned char *xrow, const flo
             }
             put(i, a);
             put(i + half, b);
+        };
+        if (rope_dim == D) {  // the usual case, unrolled so that the table's loads run ahead
+#pragma unroll 4
+            for (int i = 0; i < D / 2; i += 8) eight(i);
+            return;
         }
+        for (int i = 0; i < half; i += 8) eight(i);
     }
     for (int i = rope_dim; i < D; i += 8) {
         float v[8];
@@ -185,14 +203,14 @@ __global__ void __launch_bounds__(A_THREADS, 1) kq_kv_append_kernel(const __grid
     extern __shared__ __align__(1024) unsigned char a_raw[];
     const uint32_t raw_addr = smem_u32(a_raw), sbase = (raw_addr + 1023u) & ~1023u;
     unsigned char *smem = a_raw + (sbase - raw_addr);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2, r = tid & 127;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, pair = (warp >> 2) & 1, r = tid & 127;
     auto bar = [&](int i) -> uint32_t { return sbase + uint32_t(C::OFF_BAR + 8 * i); };
-    const uint32_t mma_bar = bar(4 + wg);
+    const uint32_t done = bar(pair), ready = bar(2 + pair), taken = bar(4 + pair);
     volatile int *s_abort = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
     if (tid == 0) {
-        for (int i = 0; i < 4; ++i) mbar_init(bar(i), 128);
-        mbar_init(bar(4), 1);
-        mbar_init(bar(5), 1);
+        for (int i = 0; i < 4; ++i) mbar_init(bar(i), 1);
+        mbar_init(bar(4), 4);
+        mbar_init(bar(5), 4);
         *s_abort = 0;
         fence_mbar_init();
     }
@@ -203,240 +221,292 @@ __global__ void __launch_bounds__(A_THREADS, 1) kq_kv_append_kernel(const __grid
     const int H = a.q_heads, Hk = a.c.heads, psh = a.c.page_shift;
     const int64_t rows_q = a.T * H, rows_k = a.T * Hk;
     const int64_t tq = (rows_q + 127) / 128, tk = (rows_k + 127) / 128, tiles = tq + 2 * tk;
-    // the block's tiles, in order: queries, then keys, then values; its warpgroups take turns
-    const int64_t t0 = blockIdx.x * tiles / gridDim.x, t1 = (blockIdx.x + 1) * tiles / gridDim.x;
+    // all tiles in order: queries, then keys, then values.  The block has every gridDim.x-th, so that
+    // each block gets its part of each kind; its pairs of warpgroups take turns.
+    const int64_t step = gridDim.x;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + C::OFF_MISC) + uint32_t(256 * wg);
+    const uint32_t tmem0 = *reinterpret_cast<volatile uint32_t *>(smem + C::OFF_MISC);
+    const uint32_t tmem = tmem0 + uint32_t(256 * pair), lanes = uint32_t(32 * (warp & 3)) << 16;
     griddep_wait();
     griddep_launch_dependents();
 
+    auto wait = [&](uint32_t b, uint32_t parity) {
+        if (!mbar_try_wait_for(b, parity, 20000u))
+            wait_bounded_err(b, parity, s_abort, kSiteKvAppendWait, kWaitLimitNs, false, a.err);
+        __syncwarp();
+    };
     auto kind_of = [&](int64_t tile) { return tile < tq ? 0 : tile < tq + tk ? 1 : 2; };
     // This thread's row of a tile: token and head; false past the last row.
     auto row_of = [&](int64_t tile, int kind, int &t, int &h) -> bool {
         const int64_t row = (tile - (kind == 0 ? 0 : kind == 1 ? tq : tq + tk)) * 128 + r;
-        const int heads = kind == 0 ? H : Hk;
-        t = int(row / heads);
-        h = int(row - int64_t(t) * heads);
+        const uint32_t heads = kind == 0 ? H : Hk;
+        t = int(uint32_t(row) / heads);
+        h = int(uint32_t(row) - uint32_t(t) * heads);
         return row < (kind == 0 ? rows_q : rows_k);
     };
-    unsigned char *place[2] = {smem + C::OFF_X + (2 * wg) * C::STAGE + r * C::ROW,
-                               smem + C::OFF_X + (2 * wg + 1) * C::STAGE + r * C::ROW};
-    auto fetch = [&](int64_t tile, int stage) {
-        if (tile >= t1) return;
-        const int kind = kind_of(tile);
-        int t, h;
-        const uint32_t b = bar(2 * wg + stage);
-        if (row_of(tile, kind, t, h)) {
-            const uint16_t *x = kind == 0   ? a.q + int64_t(t) * a.q_stride
-                                : kind == 1 ? a.k + int64_t(t) * a.k_stride
-                                            : a.v + int64_t(t) * a.v_stride;
-            mbar_arrive_expect_tx(b, D * 2);
-            bulk_load(smem_u32(place[stage]), x + int64_t(h) * D, D * 2, b);
-        } else {
-            mbar_arrive(b);
-        }
+    auto source = [&](int kind, int t, int h) -> const uint16_t * {
+        return (kind == 0   ? a.q + int64_t(t) * a.q_stride
+                : kind == 1 ? a.k + int64_t(t) * a.k_stride
+                            : a.v + int64_t(t) * a.v_stride) + int64_t(h) * D;
     };
-    fetch(t0 + wg, 0);
-    fetch(t0 + wg + 2, 1);
+    // The kind's first and last tile, its factor brought to shared memory; false if the block has none of it.
+    auto begin_kind = [&](int kind, int64_t &end) -> bool {
+        const int64_t from = kind == 0 ? 0 : kind == 1 ? tq : tq + tk;
+        end = from + (kind == 0 ? tq : tk);
+        if (from + ((blockIdx.x - from % step) + step) % step >= end) return false;
+        __syncthreads();  // nothing reads the last factor any more
+        const uint16_t *P = kind == 0 ? a.Pq : kind == 1 ? a.Pk : a.Pv;
+#pragma unroll
+        for (int u = tid; u < D * D / 8; u += A_THREADS) {
+            const int k = u / (D / 8), n = 8 * (u % (D / 8));
+            *reinterpret_cast<uint4 *>(smem + (n >> 6) * D * 128 + k * 128 + ((((n & 63) >> 3) ^ (k & 7)) << 4)) =
+                __ldg(reinterpret_cast<const uint4 *>(P + k * D + n));
+        }
+        fence_proxy_async_smem();
+        __syncthreads();
+        return true;
+    };
 
-    const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16, ta = tmem + lanes, td = ta + 128;
-    constexpr uint32_t idesc = idesc_bf16_f32_bn(128, D);
-    // D (+)= terms from column `col` of A times the factor, by one thread of the warpgroup.
-    auto multiply = [&](int terms, bool accumulate) {
-        tmem_wait_st();
-        tc_fence_before();
-        named_barrier_sync(1 + wg, 128);
-        if ((warp & 3) == 0) {
+    int64_t tile = blockIdx.x + pair * step, end;
+    uint32_t turns = 0;
+    if (warp < 8) {
+        // ---------------- rows into terms, terms times the factor ----------------
+        unsigned char *const place0 = smem + C::OFF_X + 2 * pair * C::STAGE + r * C::ROW;
+        // The warp's rows of a tile: a step takes 32 / PIECES rows, a lane 16 bytes.
+        constexpr int PIECES = D / 8, PER = 32 / PIECES;
+        const int sub = lane / PIECES, piece = lane % PIECES;
+        int pos_of[2] = {0, 0};  // positions of this thread's row of the tiles in the two places
+        auto fetch = [&](int64_t tile, int stage) {
+            if (tile < tiles) {
+                const int kind = kind_of(tile);
+                int t, h;
+                const uint16_t *x = nullptr;
+                if (row_of(tile, kind, t, h)) {
+                    x = source(kind, t, h);
+                    if (kind < 2 && a.rope_dim) pos_of[stage] = a.positions[t];
+                }
+                const uint32_t dst =
+                    smem_u32(place0 + stage * C::STAGE - lane * C::ROW) + uint32_t(sub * C::ROW + 16 * piece);
+#pragma unroll
+                for (int i = 0; i < 32 / PER; ++i) {
+                    const uint64_t src = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(x), i * PER + sub);
+                    cp_async16(dst + uint32_t(i * PER * C::ROW), src ? src + 16 * piece : reinterpret_cast<uint64_t>(a.Pk),
+                               src ? 16u : 0u);  // rows past the last are zeros
+                }
+            }
+            cp_async_commit();
+        };
+        fetch(tile, 0);
+        fetch(tile + 2 * step, 1);
+        const uint32_t ta = tmem + lanes;
+        constexpr uint32_t idesc = idesc_bf16_f32_bn(128, D);
+        uint32_t products = 0;
+        // Rows (+)= the terms times the factor, by one thread of the warpgroup.
+        auto multiply = [&](int terms, bool accumulate, bool last) {
+            tmem_wait_st();
+            tc_fence_before();
+            named_barrier_sync(1 + pair, 128);
+            if ((warp & 3) == 0) {
+                if (!accumulate) wait(taken, (turns & 1u) ^ 1u);  // the last tile's rows
+                tc_fence_after();
+                if (elect_one()) {
+                    // the smallest term first: the sum is truncated at every addition
+                    for (int term = terms - 1; term >= 0; --term)
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k)
+                            mma_ts(tmem + 128, tmem + uint32_t(64 * term + 8 * k),
+                                   sdesc_nmajor_sw128(sbase + uint32_t(2048 * k), D * 128), idesc,
+                                   accumulate || term + 1 < terms || k);
+                    tc_commit(done);
+                    if (last) tc_commit(ready);
+                }
+                __syncwarp();
+            }
+            ++products;
+        };
+        // the terms' columns are free once the last product is done
+        auto multiplied = [&] {
+            if (products) wait(done, (products - 1) & 1u);
             tc_fence_after();
-            if (elect_one()) {
-                // the smallest term first: the sum is truncated at every addition
-                for (int term = terms - 1; term >= 0; --term)
+        };
+        const bool inter = a.rope_interleaved != 0;
+        for (int kind = 0; kind < 3; ++kind) {
+            if (!begin_kind(kind, end)) continue;
+            for (; tile < end; tile += 2 * step, ++turns) {
+                const int stage = int(turns & 1u);
+                const unsigned char *x = place0 + stage * C::STAGE;
+                const int64_t pos = stage ? pos_of[1] : pos_of[0];
+                const float *cs = a.rope + (pos >= 0 && pos < a.rope_positions ? pos : 0) * a.rope_dim;
+                cp_async_wait<1>();
+                __syncwarp();
+                multiplied();
+                if (kind == 2) {
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-                        mma_ts(tmem + 128, tmem + uint32_t(64 * term + 8 * k),
-                               sdesc_nmajor_sw128(sbase + uint32_t(2048 * k), D * 128), idesc,
-                               accumulate || term + 1 < terms || k);
-                tc_commit(mma_bar);
-            }
-            __syncwarp();
-        }
-    };
-    uint32_t products = 0, turns = 0;
-    auto multiplied = [&] {
-        wait_bounded_err(mma_bar, products++ & 1u, s_abort, kSiteKvAppendWait, kWaitLimitNs, false, a.err);
-        __syncwarp();
-        tc_fence_after();
-    };
-
-    int have = -1;  // the factor in shared memory
-    // Both warpgroups go through the same kinds; `base` is the first of a pair of tiles.
-    for (int64_t first = t0; first < t1;) {
-        const int kind = kind_of(first);
-        const int64_t end = min(t1, kind == 0 ? tq : kind == 1 ? tq + tk : tiles);
-        if (kind != have) {
-            __syncthreads();  // no product reads the last factor any more
-            const uint16_t *P = kind == 0 ? a.Pq : kind == 1 ? a.Pk : a.Pv;
-#pragma unroll
-            for (int u = tid; u < D * D / 8; u += A_THREADS) {
-                const int k = u / (D / 8), n = 8 * (u % (D / 8));
-                *reinterpret_cast<uint4 *>(smem + (n >> 6) * D * 128 + k * 128 + ((((n & 63) >> 3) ^ (k & 7)) << 4)) =
-                    __ldg(reinterpret_cast<const uint4 *>(P + k * D + n));
-            }
-            fence_proxy_async_smem();
-            __syncthreads();
-            have = kind;
-        }
-        // this warpgroup's tiles of the kind: those of its parity from t0
-        int64_t tile = first + ((first - t0 + wg) & 1);
-        for (; tile < end; tile += 2, ++turns) {
-            const int stage = int(turns & 1u);
-            int t, h;
-            const bool real = row_of(tile, kind, t, h);
-            int64_t slot = -1;
-            bool pos_ok = true;
-            const float *cs = nullptr;
-            if (real) {
-                if (kind != 0) slot = a.slots[t];
-                if (a.rope_dim) {
-                    const int64_t pos = a.positions[t];
-                    pos_ok = pos >= 0 && pos < a.rope_positions;
-                    if (!pos_ok) atomicOr(a.err, kSiteKvAppend);
-                    cs = a.rope + (pos_ok ? pos : 0) * a.rope_dim;
-                }
-                if (kind != 0 && slot >= a.c.pages << psh) {
-                    atomicOr(a.err, kSiteKvAppend);
-                    slot = -1;
-                }
-            }
-            wait_bounded_err(bar(2 * wg + stage), (turns >> 1) & 1u, s_abort, kSiteKvAppendWait, kWaitLimitNs, false,
-                             a.err);
-            __syncwarp();
-            const unsigned char *x = place[stage];
-            const int rope = kind == 2 || !real ? 0 : a.rope_dim;
-            const int rope_w = __reduce_max_sync(0xffffffffu, rope);  // rows past the last follow their warp
-            if (cs == nullptr) cs = a.rope;
-            const bool inter = a.rope_interleaved != 0;
-            if (kind == 2) {
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    const uint4 u = reinterpret_cast<const uint4 *>(x)[i];
-                    tmem_st_32x32b_x4(ta + uint32_t(4 * i), u.x, u.y, u.z, u.w);
-                }
-                multiply(1, false);
-            } else {
-                // queries: both terms; keys: the second and third, and then the first
-                rotated_row<D>(x, cs, rope_w, inter, [&](int i, float (&v)[8]) {
-                    uint32_t w[4];
-                    take_term(v, w);
-                    if (kind == 1) take_term(v, w);
-                    tmem_st_32x32b_x4(ta + uint32_t(i >> 1), w[0], w[1], w[2], w[3]);
-                    tmem_st_32x32b_x4(ta + 64 + uint32_t(i >> 1), pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                      pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-                });
-                multiply(2, false);
-                if (kind == 1) {
-                    multiplied();
-                    rotated_row<D>(x, cs, rope_w, inter, [&](int i, float (&v)[8]) {
+                    for (int i = 0; i < D / 8; ++i) {
+                        const uint4 u = reinterpret_cast<const uint4 *>(x)[i];
+                        tmem_st_32x32b_x4(ta + uint32_t(4 * i), u.x, u.y, u.z, u.w);
+                    }
+                    multiply(1, false, true);
+                } else {
+                    // queries: both terms; keys: the second and third, and then the first
+                    rotated_row<D>(x, cs, a.rope_dim, inter, [&](int i, float (&v)[8]) {
                         uint32_t w[4];
                         take_term(v, w);
+                        if (kind == 1) take_term(v, w);
                         tmem_st_32x32b_x4(ta + uint32_t(i >> 1), w[0], w[1], w[2], w[3]);
+                        tmem_st_32x32b_x4(ta + 64 + uint32_t(i >> 1), pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                          pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
                     });
-                    multiply(1, true);
-                }
-            }
-            multiplied();
-            if (kind == 0) {
-                // ---- queries out: bf16, through the row's place ----
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t v[32];
-                    tmem_ld_32x32b_x32(td + uint32_t(32 * c), v);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            w[k] = pos_ok ? pack_bf16x2(__uint_as_float(v[8 * e + 2 * k]),
-                                                        __uint_as_float(v[8 * e + 2 * k + 1]))
-                                          : 0u;
-                        reinterpret_cast<uint4 *>(place[stage])[4 * c + e] = make_uint4(w[0], w[1], w[2], w[3]);
+                    multiply(2, false, kind == 0);
+                    if (kind == 1) {
+                        multiplied();
+                        rotated_row<D>(x, cs, a.rope_dim, inter, [&](int i, float (&v)[8]) {
+                            uint32_t w[4];
+                            take_term(v, w);
+                            tmem_st_32x32b_x4(ta + uint32_t(i >> 1), w[0], w[1], w[2], w[3]);
+                        });
+                        multiply(1, true, true);
                     }
                 }
-                fence_proxy_async_smem();
-                if (real) {
-                    bulk_store(a.q_out + (int64_t(t) * H + h) * D, smem_u32(place[stage]), D * 2);
-                    bulk_commit();
-                    bulk_wait_read<0>();
-                }
-            } else {
-                // ---- a row of the cache ----
-                float m = 0.0f;
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t v[32];
-                    tmem_ld_32x32b_x32(td + uint32_t(32 * c), v);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2)
-                        m = fmax3(m, fabsf(__uint_as_float(v[e])), fabsf(__uint_as_float(v[e + 1])));
-                }
-                const float alpha = kind == 1 ? a.alpha_k : a.alpha_v;
-                const float sc = __fdiv_rn(alpha * m, 7.0f);
-                const float inv = sc > 0.0f ? fminf(__frcp_rn(sc), 3.0e38f) : 0.0f;
-                const bool store = real && slot >= 0 && pos_ok;
-                const int64_t row = store ? (((slot >> psh) * Hk + h) << psh) + (slot & ((int64_t(1) << psh) - 1)) : 0;
-                uint8_t *codes = (kind == 1 ? a.c.k_codes : a.c.v_codes) + row * (D / 2);
-                float *scale = (kind == 1 ? a.c.k_scale : a.c.v_scale) + row;
-                float off = 0.0f;
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t v[32], w[4];
-                    tmem_ld_32x32b_x32(td + uint32_t(32 * c), v);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t *y = v + 8 * k;
-                        uint32_t p = 0;
-#pragma unroll
-                        for (int e = 6; e >= 0; e -= 2)
-                            p = pack_s4x2(round_off(y[e + 1], inv, off), round_off(y[e], inv, off), p);
-                        w[k] = p;
-                    }
-                    if (store) reinterpret_cast<uint4 *>(codes)[c] = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-                if (store) *scale = sc;
-                // ---- rows with a value too near a border for fp32, again in fp64 ----
-                // (scales that leave fp32's normal range are among them; a NaN or an infinity is not)
-                const bool near = store && m < 3.0e38f &&
-                                  (off > 0.5f - 7.0f * kBorder / alpha || (m > 0.0f && sc < 1e-30f));
-                uint32_t again = __ballot_sync(0xffffffffu, near);
-                while (again) {
-                    const int src = __ffs(again) - 1;
-                    again &= again - 1;
-                    const uint64_t pc = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(codes), src);
-                    const uint64_t ps = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(scale), src);
-                    const uint64_t pt = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(cs), src);
-                    __syncwarp();
-                    exact_row<D>(x + (src - lane) * C::ROW, smem,
-                                 reinterpret_cast<double *>(smem + C::OFF_Y) + warp * D,
-                                 reinterpret_cast<const float *>(pt), rope_w, inter, alpha,
-                                 reinterpret_cast<uint8_t *>(pc), reinterpret_cast<float *>(ps));
-                }
+                __syncwarp();  // all lanes have read the warp's rows
+                fetch(tile + 4 * step, stage);
             }
-            tc_fence_before();
-            __syncwarp();  // the warp's rows have been read (the exact path reads across lanes)
-            fetch(tile + 4, stage);
         }
-        first = end;
+        cp_async_wait<0>();
+        multiplied();
+    } else {
+        // ---------------- rows out ----------------
+        const uint32_t td = tmem + lanes + 128;
+        unsigned char *const own = smem + C::OFF_Y + (warp - 8) * 4096;
+        for (int kind = 0; kind < 3; ++kind) {
+            if (!begin_kind(kind, end)) continue;
+            for (; tile < end; tile += 2 * step, ++turns) {
+                int t, h;
+                const bool real = row_of(tile, kind, t, h);
+                int64_t slot = -1;
+                bool pos_ok = true;
+                const float *cs = a.rope;
+                if (real) {
+                    if (kind != 0) slot = a.slots[t];
+                    if (a.rope_dim) {
+                        const int64_t pos = a.positions[t];
+                        pos_ok = pos >= 0 && pos < a.rope_positions;
+                        if (!pos_ok) atomicOr(a.err, kSiteKvAppend);
+                        cs += (pos_ok ? pos : 0) * a.rope_dim;
+                    }
+                    if (kind != 0 && slot >= a.c.pages << psh) {
+                        atomicOr(a.err, kSiteKvAppend);
+                        slot = -1;
+                    }
+                }
+                wait(ready, turns & 1u);
+                tc_fence_after();
+                if (kind == 0) {
+                    // ---- queries: bf16, 64 columns at a time through the warp's 4 KB (32 rows of 128 bytes,
+                    // their pieces exchanged by row), so that whole rows are stored; q_out is dense ----
+                    const int64_t row0 = tile * 128 + 32 * (warp & 3);
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c) {
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+                            uint32_t v[32];
+                            tmem_ld_32x32b_x32(td + uint32_t(64 * c + 32 * b), v);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    w[k] = pos_ok ? pack_bf16x2(__uint_as_float(v[8 * e + 2 * k]),
+                                                                __uint_as_float(v[8 * e + 2 * k + 1]))
+                                                  : 0u;
+                                *reinterpret_cast<uint4 *>(own + 128 * lane + (((4 * b + e) ^ (lane & 7)) << 4)) =
+                                    make_uint4(w[0], w[1], w[2], w[3]);
+                            }
+                        }
+                        if (c == D / 64 - 1) tc_fence_before();
+                        __syncwarp();
+                        if (c == D / 64 - 1 && lane == 0) mbar_arrive(taken);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int row = 4 * i + (lane >> 3);
+                            if (row0 + row < rows_q)
+                                *reinterpret_cast<uint4 *>(a.q_out + (row0 + row) * D + 64 * c + 8 * (lane & 7)) =
+                                    *reinterpret_cast<const uint4 *>(own + 128 * row + (((lane ^ row) & 7) << 4));
+                        }
+                        __syncwarp();
+                    }
+                } else {
+                    // ---- a row of the cache ----
+                    float m = 0.0f;
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t v[32];
+                        tmem_ld_32x32b_x32(td + uint32_t(32 * c), v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2)
+                            m = fmax3(m, fabsf(__uint_as_float(v[e])), fabsf(__uint_as_float(v[e + 1])));
+                    }
+                    const float alpha = kind == 1 ? a.alpha_k : a.alpha_v;
+                    const float sc = __fdiv_rn(alpha * m, 7.0f);
+                    const float inv = sc > 0.0f ? fminf(__frcp_rn(sc), 3.0e38f) : 0.0f;
+                    const bool store = real && slot >= 0 && pos_ok;
+                    const int64_t row =
+                        store ? (((slot >> psh) * Hk + h) << psh) + (slot & ((int64_t(1) << psh) - 1)) : 0;
+                    uint8_t *codes = (kind == 1 ? a.c.k_codes : a.c.v_codes) + row * (D / 2);
+                    float *scale = (kind == 1 ? a.c.k_scale : a.c.v_scale) + row;
+                    float off = 0.0f;
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t v[32], w[4];
+                        tmem_ld_32x32b_x32(td + uint32_t(32 * c), v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t *y = v + 8 * k;
+                            uint32_t p = 0;
+#pragma unroll
+                            for (int e = 6; e >= 0; e -= 2)
+                                p = pack_s4x2(round_off(y[e + 1], inv, off), round_off(y[e], inv, off), p);
+                            w[k] = p;
+                        }
+                        if (store) reinterpret_cast<uint4 *>(codes)[c] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(taken);
+                    if (store) *scale = sc;
+                    // ---- rows with a value too near a border for fp32, again in fp64 ----
+                    // (scales that leave fp32's normal range are among them; a NaN or an infinity is not)
+                    const bool near = store && m < 3.0e38f &&
+                                      (off > 0.5f - 7.0f * kBorder / alpha || (m > 0.0f && sc < 1e-30f));
+                    uint32_t again = __ballot_sync(0xffffffffu, near);
+                    const uint16_t *x = source(kind, t, h);
+                    while (again) {
+                        const int src = __ffs(again) - 1;
+                        again &= again - 1;
+                        const uint64_t pc = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(codes), src);
+                        const uint64_t ps = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(scale), src);
+                        const uint64_t pt = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(cs), src);
+                        const uint64_t px = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(x), src);
+                        __syncwarp();
+                        exact_row<D>(reinterpret_cast<const uint16_t *>(px), smem, reinterpret_cast<double *>(own),
+                                     reinterpret_cast<const float *>(pt), kind == 1 ? a.rope_dim : 0,
+                                     a.rope_interleaved != 0, alpha, reinterpret_cast<uint8_t *>(pc),
+                                     reinterpret_cast<float *>(ps));
+                    }
+                }
+            }
+        }
     }
-    bulk_wait_read<0>();
+    tc_fence_before();
     __syncthreads();
     if (warp == 0) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(tmem0, 512);
     }
 }
 

@@ -261,20 +261,9 @@ enum : uint32_t { kUnitBegins = 1u << 16, kUnitEnds = 1u << 17 };  // ends: or t
 constexpr int kWhole = -1;
 enum : unsigned { kSiteKvWait = 262144u };
 
-// Wait for a phase without taking issue slots: try_wait suspends the thread until the phase
-// completes or the hint (in ns) has passed.  Gives up as wait_bounded_err does.
-__device__ __forceinline__ bool wait_suspended(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(20000u)
-        : "memory");
-    return ok != 0;
-}
+// Wait for a phase, suspended at first; gives up as wait_bounded_err does.
 __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile int *abort, unsigned int *err) {
-    if (__all_sync(0xffffffffu, wait_suspended(bar, parity))) return true;
+    if (__all_sync(0xffffffffu, tc::mbar_try_wait_for(bar, parity, 20000u))) return true;
     return __all_sync(0xffffffffu,
                       tc::wait_bounded_err(bar, parity, abort, kSiteKvWait, tc::kWaitLimitNs, false, err));
 }
