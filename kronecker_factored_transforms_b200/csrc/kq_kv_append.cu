@@ -64,15 +64,20 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// One row's exact codes and scale, by a whole warp: lane l has the columns l, l + 32, ...
+// One row's exact codes and scale, by a whole warp, from the row in fp32: `y32` in shared memory,
+// off by at most kBorder of its largest value `m`.  A lane has the columns D / 32 lane and on, and as
+// many elements of the rotated row; a column is computed again, in fp64, where its code or the
+// scale depends on it.
 template <int D>
-__device__ __noinline__ void exact_row(const uint16_t *x, const unsigned char *factor, double *xs,
+__device__ __noinline__ void exact_row(const uint16_t *x, const unsigned char *factor, const float *y32, float m,
                                        const float *cs, int rope_dim, bool inter, float alpha, uint8_t *codes,
                                        float *scale) {
+    constexpr int N = D / 32;
     const int lane = threadIdx.x & 31, half = rope_dim >> 1;
+    double xs[N];
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) {
-        const int i = lane + 32 * e;
+    for (int e = 0; e < N; ++e) {
+        const int i = N * lane + e;
         double v = double(bf16_bits_to_float(x[i]));
         if (i < rope_dim) {
             const int k = inter ? i >> 1 : (i < half ? i : i - half);  // the pair's angle
@@ -81,35 +86,67 @@ __device__ __noinline__ void exact_row(const uint16_t *x, const unsigned char *f
             const double w = double(bf16_bits_to_float(x[j])), c = double(cs[k]), s = double(cs[half + k]);
             v = first ? v * c - w * s : w * s + v * c;
         }
-        xs[i] = v;
+        xs[e] = v;
     }
-    __syncwarp();
-    double y[D / 32];
+    auto column = [&](int n) -> double {
+        double y = 0.0;
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) y[e] = 0.0;
-    for (int k = 0; k < D; ++k) {
-        const double xk = xs[k];
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) {
-            const int n = lane + 32 * e;
+        for (int e = 0; e < N; ++e) {
+            const int k = N * lane + e;
             const uint16_t w = *reinterpret_cast<const uint16_t *>(factor + (n >> 6) * D * 128 + k * 128 +
                                                                    ((((n & 63) >> 3) ^ (k & 7)) << 4) + 2 * (n & 7));
-            y[e] = fma(xk, double(bf16_bits_to_float(w)), y[e]);
+            y = fma(xs[e], double(bf16_bits_to_float(w)), y);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+        return y;
+    };
+    float y[N];
+    double top = 0.0;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        y[e] = y32[N * lane + e];
+        uint32_t may = __ballot_sync(0xffffffffu, fabsf(y[e]) >= m * (1.0f - 2.5f * kBorder));  // the largest, maybe
+        while (may) {
+            const int l = __ffs(may) - 1;
+            may &= may - 1;
+            top = fmax(top, fabs(column(N * l + e)));
         }
     }
-    double m = 0.0;
+    const double s = double(alpha) * top / 7.0;
+    uint32_t byte = 0;
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) m = fmax(m, fabs(y[e]));
-    for (int o = 16; o; o >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const double s = double(alpha) * m / 7.0;
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) {
-        const int c = s > 0.0 ? int(rint(fmin(fmax(y[e] / s, -8.0), 7.0))) & 15 : 0;
-        const int up = __shfl_down_sync(0xffffffffu, c, 1);
-        if ((lane & 1) == 0) codes[(lane >> 1) + 16 * e] = uint8_t(c | (up << 4));
+    for (int e = 0; e < N; ++e) {
+        const double r = s > 0.0 ? double(y[e]) / s : 0.0;
+        int c = int(rint(fmin(fmax(r, -8.0), 7.0)));
+        const float off = float(fabs(r - rint(r)));
+        uint32_t near = __ballot_sync(0xffffffffu, fabs(r) < 9.0 && off > 0.5f - 14.0f * kBorder / alpha);
+        while (near) {
+            const int l = __ffs(near) - 1;
+            near &= near - 1;
+            const double q = column(N * l + e);
+            if (lane == l) c = s > 0.0 ? int(rint(fmin(fmax(q / s, -8.0), 7.0))) : 0;
+        }
+        byte |= uint32_t(c & 15) << (4 * e);
     }
+    if constexpr (N == 4) reinterpret_cast<uint16_t *>(codes)[lane] = uint16_t(byte);
+    else codes[lane] = uint8_t(byte);
     if (lane == 0) *scale = float(s);
     __syncwarp();
+}
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t d, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(d));
+}
+__device__ __forceinline__ uint64_t f32x2_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
 }
 
 // Four consecutive pairs of fp32 values -> words of their leading bf16 terms (truncated), the
@@ -119,8 +156,9 @@ __device__ __forceinline__ void take_term(float (&v)[8], uint32_t (&w)[4]) {
     for (int i = 0; i < 4; ++i) {
         const uint32_t a = __float_as_uint(v[2 * i]), b = __float_as_uint(v[2 * i + 1]);
         w[i] = __byte_perm(a, b, 0x7632);
-        v[2 * i] -= __uint_as_float(a & 0xffff0000u);
-        v[2 * i + 1] -= __uint_as_float(b & 0xffff0000u);
+        unpack2(f32x2_sub(pack2(v[2 * i], v[2 * i + 1]),
+                          pack2(__uint_as_float(a & 0xffff0000u), __uint_as_float(b & 0xffff0000u))),
+                v[2 * i], v[2 * i + 1]);
     }
 }
 __device__ __forceinline__ void unpack8(const uint4 &u, float (&v)[8]) {
@@ -167,10 +205,12 @@ __device__ __forceinline__ void rotated_row(const unsigned char *xrow, const flo
                 s[e] = w.x, s[e + 1] = w.y, s[e + 2] = w.z, s[e + 3] = w.w;
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float p = a[e], q = b[e];
-                a[e] = fmaf(p, c[e], -(q * s[e]));
-                b[e] = fmaf(q, c[e], p * s[e]);
+            for (int e = 0; e < 8; e += 2) {
+                const uint64_t p = pack2(a[e], a[e + 1]), q = pack2(b[e], b[e + 1]);
+                const uint64_t cc = pack2(c[e], c[e + 1]), ss = pack2(s[e], s[e + 1]);
+                const uint64_t minus = pack2(-b[e], -b[e + 1]);
+                unpack2(f32x2_fma(p, cc, f32x2_mul(minus, ss)), a[e], a[e + 1]);
+                unpack2(f32x2_fma(q, cc, f32x2_mul(p, ss)), b[e], b[e + 1]);
             }
             put(i, a);
             put(i + half, b);
@@ -233,8 +273,13 @@ __global__ void __launch_bounds__(A_THREADS, 1) kq_kv_append_kernel(const __grid
     griddep_launch_dependents();
 
     auto wait = [&](uint32_t b, uint32_t parity) {
-        if (!mbar_try_wait_for(b, parity, 20000u))
-            wait_bounded_err(b, parity, s_abort, kSiteKvAppendWait, kWaitLimitNs, false, a.err);
+        // looks 60 ns apart at first, which leave the issue slots to the other warps
+        bool ok = mbar_try_wait(b, parity);
+        for (int i = 0; i < 200 && !ok; ++i) {
+            __nanosleep(60);
+            ok = mbar_try_wait(b, parity);
+        }
+        if (!ok) wait_bounded_err(b, parity, s_abort, kSiteKvAppendWait, kWaitLimitNs, false, a.err);
         __syncwarp();
     };
     auto kind_of = [&](int64_t tile) { return tile < tq ? 0 : tile < tq + tk ? 1 : 2; };
@@ -475,9 +520,6 @@ __global__ void __launch_bounds__(A_THREADS, 1) kq_kv_append_kernel(const __grid
                         }
                         if (store) reinterpret_cast<uint4 *>(codes)[c] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(taken);
                     if (store) *scale = sc;
                     // ---- rows with a value too near a border for fp32, again in fp64 ----
                     // (scales that leave fp32's normal range are among them; a NaN or an infinity is not)
@@ -488,16 +530,31 @@ __global__ void __launch_bounds__(A_THREADS, 1) kq_kv_append_kernel(const __grid
                     while (again) {
                         const int src = __ffs(again) - 1;
                         again &= again - 1;
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t v[32];
+                            tmem_ld_32x32b_x32(td + uint32_t(32 * c), v);
+                            tmem_wait_ld();
+                            if (lane == src)
+#pragma unroll
+                                for (int e = 0; e < 8; ++e)
+                                    *reinterpret_cast<uint4 *>(own + 128 * c + 16 * e) =
+                                        make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                        }
                         const uint64_t pc = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(codes), src);
                         const uint64_t ps = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(scale), src);
                         const uint64_t pt = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(cs), src);
                         const uint64_t px = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(x), src);
+                        const float mm = __shfl_sync(0xffffffffu, m, src);
                         __syncwarp();
-                        exact_row<D>(reinterpret_cast<const uint16_t *>(px), smem, reinterpret_cast<double *>(own),
-                                     reinterpret_cast<const float *>(pt), kind == 1 ? a.rope_dim : 0,
+                        exact_row<D>(reinterpret_cast<const uint16_t *>(px), smem, reinterpret_cast<const float *>(own),
+                                     mm, reinterpret_cast<const float *>(pt), kind == 1 ? a.rope_dim : 0,
                                      a.rope_interleaved != 0, alpha, reinterpret_cast<uint8_t *>(pc),
                                      reinterpret_cast<float *>(ps));
                     }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(taken);
                 }
             }
         }
