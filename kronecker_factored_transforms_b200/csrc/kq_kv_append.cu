@@ -16,12 +16,12 @@
 //     the result is rounded to bf16), three for keys (all 24 bits of the fp32 value),
 //     one for values (they are bf16).  The factor is the B operand in shared memory,
 //     as it lies in memory (N contiguous).
-//   - two pairs of warpgroups, each with 256 TMEM columns: one warpgroup turns rows
-//     into terms (128 columns), the other takes the fp32 rows (128 columns) while the
-//     first is at its next tile.  The keys' largest term waits for the products of the
-//     other two and takes their columns (smallest first: the tensor core truncates the
-//     sum at every addition).
-//   - one block an SM, on tiles of one kind at a time.
+//   - two teams, each with 256 TMEM columns: eight warps turn rows into terms (128
+//     columns; two warps share the rows of a TMEM quarter, every second 16 bytes each),
+//     four take the fp32 rows (128 columns) while the eight are at their next tile.
+//     The keys' largest term waits for the products of the other two and takes their
+//     columns (smallest first: the tensor core truncates the sum at every addition).
+//   - one block an SM, all its tiles of one kind, so that it needs one factor.
 //
 // Codes of exact arithmetic: fp32 leaves y / s uncertain by up to kBorder of its
 // largest value; a row with a value nearer than that to a rounding border (a row in a
@@ -38,7 +38,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int A_THREADS = 512;     // two warpgroups that make terms, two that take rows
+constexpr int A_THREADS = 768;     // per team eight warps that make terms and four that take rows
 constexpr float kBorder = 0x1p-19f;  // of max|y|: bound of fp32's error in a row
 enum : unsigned { kSiteKvAppendWait = 524288u };
 
@@ -170,14 +170,15 @@ __device__ __forceinline__ void unpack8(const uint4 &u, float (&v)[8]) {
     }
 }
 
-// The row's values, rotated, eight at a time: calls put(first element, values).
+// Every second eight (`which`: the even or the odd ones) of the row's values, rotated, or pair
+// of eights that turn together: calls put(first element, values).
 template <int D, typename F>
 __device__ __forceinline__ void rotated_row(const unsigned char *xrow, const float *cs, int rope_dim, bool inter,
-                                            F put) {
+                                            int which, F put) {
     const uint4 *x = reinterpret_cast<const uint4 *>(xrow);
     const int half = rope_dim >> 1;
     if (inter) {
-        for (int i = 0; i < rope_dim; i += 8) {
+        for (int i = 8 * which; i < rope_dim; i += 16) {
             float v[8];
             unpack8(x[i >> 3], v);
             const float4 c = __ldg(reinterpret_cast<const float4 *>(cs + (i >> 1)));
@@ -216,13 +217,13 @@ __device__ __forceinline__ void rotated_row(const unsigned char *xrow, const flo
             put(i + half, b);
         };
         if (rope_dim == D) {  // the usual case, unrolled so that the table's loads run ahead
-#pragma unroll 4
-            for (int i = 0; i < D / 2; i += 8) eight(i);
+#pragma unroll
+            for (int i = 0; i < D / 2; i += 16) eight(i + 8 * which);
             return;
         }
-        for (int i = 0; i < half; i += 8) eight(i);
+        for (int i = 8 * which; i < half; i += 16) eight(i);
     }
-    for (int i = rope_dim; i < D; i += 8) {
+    for (int i = rope_dim + 8 * which; i < D; i += 16) {
         float v[8];
         unpack8(x[i >> 3], v);
         put(i, v);
@@ -238,12 +239,14 @@ __device__ __forceinline__ int round_off(uint32_t ybits, float inv, float &off) 
 }
 
 template <int D>
-__global__ void __launch_bounds__(A_THREADS, 1) kq_kv_append_kernel(const __grid_constant__ KvAppendArgs a) {
+__global__ void __launch_bounds__(A_THREADS, 1)
+    kq_kv_append_kernel(const __grid_constant__ KvAppendArgs a, int blocks_q, int blocks_k, int blocks_v) {
     using C = ACfg<D>;
     extern __shared__ __align__(1024) unsigned char a_raw[];
     const uint32_t raw_addr = smem_u32(a_raw), sbase = (raw_addr + 1023u) & ~1023u;
     unsigned char *smem = a_raw + (sbase - raw_addr);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, pair = (warp >> 2) & 1, r = tid & 127;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int pair = warp < 16 ? warp >> 3 : (warp - 16) >> 2, r = tid & 127;  // the team; this thread's row of a tile
     auto bar = [&](int i) -> uint32_t { return sbase + uint32_t(C::OFF_BAR + 8 * i); };
     const uint32_t done = bar(pair), ready = bar(2 + pair), taken = bar(4 + pair);
     volatile int *s_abort = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
@@ -259,11 +262,11 @@ __global__ void __launch_bounds__(A_THREADS, 1) kq_kv_append_kernel(const __grid
         tmem_relinquish();
     }
     const int H = a.q_heads, Hk = a.c.heads, psh = a.c.page_shift;
-    const int64_t rows_q = a.T * H, rows_k = a.T * Hk;
-    const int64_t tq = (rows_q + 127) / 128, tk = (rows_k + 127) / 128, tiles = tq + 2 * tk;
-    // all tiles in order: queries, then keys, then values.  The block has every gridDim.x-th, so that
-    // each block gets its part of each kind; its pairs of warpgroups take turns.
-    const int64_t step = gridDim.x;
+    // the block's kind, and its tiles: every blocks_*-th of the kind; the teams take turns
+    const int bid = blockIdx.x, kind = bid < blocks_q ? 0 : bid < blocks_q + blocks_k ? 1 : 2;
+    const int64_t rows = a.T * (kind == 0 ? H : Hk), tiles = (rows + 127) / 128;
+    const int64_t step = kind == 0 ? blocks_q : kind == 1 ? blocks_k : blocks_v;
+    const uint32_t heads = kind == 0 ? H : Hk;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -282,26 +285,17 @@ __global__ void __launch_bounds__(A_THREADS, 1) kq_kv_append_kernel(const __grid
         if (!ok) wait_bounded_err(b, parity, s_abort, kSiteKvAppendWait, kWaitLimitNs, false, a.err);
         __syncwarp();
     };
-    auto kind_of = [&](int64_t tile) { return tile < tq ? 0 : tile < tq + tk ? 1 : 2; };
     // This thread's row of a tile: token and head; false past the last row.
-    auto row_of = [&](int64_t tile, int kind, int &t, int &h) -> bool {
-        const int64_t row = (tile - (kind == 0 ? 0 : kind == 1 ? tq : tq + tk)) * 128 + r;
-        const uint32_t heads = kind == 0 ? H : Hk;
+    auto row_of = [&](int64_t tile, int &t, int &h) -> bool {
+        const int64_t row = tile * 128 + r;
         t = int(uint32_t(row) / heads);
         h = int(uint32_t(row) - uint32_t(t) * heads);
-        return row < (kind == 0 ? rows_q : rows_k);
+        return row < rows;
     };
-    auto source = [&](int kind, int t, int h) -> const uint16_t * {
-        return (kind == 0   ? a.q + int64_t(t) * a.q_stride
-                : kind == 1 ? a.k + int64_t(t) * a.k_stride
-                            : a.v + int64_t(t) * a.v_stride) + int64_t(h) * D;
-    };
-    // The kind's first and last tile, its factor brought to shared memory; false if the block has none of it.
-    auto begin_kind = [&](int kind, int64_t &end) -> bool {
-        const int64_t from = kind == 0 ? 0 : kind == 1 ? tq : tq + tk;
-        end = from + (kind == 0 ? tq : tk);
-        if (from + ((blockIdx.x - from % step) + step) % step >= end) return false;
-        __syncthreads();  // nothing reads the last factor any more
+    const uint16_t *const rows_from = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
+    const int64_t stride = kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride;
+    auto source = [&](int t, int h) { return rows_from + int64_t(t) * stride + int64_t(h) * D; };
+    {  // the factor
         const uint16_t *P = kind == 0 ? a.Pq : kind == 1 ? a.Pk : a.Pv;
 #pragma unroll
         for (int u = tid; u < D * D / 8; u += A_THREADS) {
@@ -310,26 +304,24 @@ __global__ void __launch_bounds__(A_THREADS, 1) kq_kv_append_kernel(const __grid
                 __ldg(reinterpret_cast<const uint4 *>(P + k * D + n));
         }
         fence_proxy_async_smem();
-        __syncthreads();
-        return true;
-    };
+    }
 
-    int64_t tile = blockIdx.x + pair * step, end;
+    int64_t tile = (bid - (kind == 0 ? 0 : kind == 1 ? blocks_q : blocks_q + blocks_k)) + pair * step;
     uint32_t turns = 0;
-    if (warp < 8) {
+    if (warp < 16) {
         // ---------------- rows into terms, terms times the factor ----------------
+        const int which = (warp >> 2) & 1;  // of the two warps of a TMEM quarter
         unsigned char *const place0 = smem + C::OFF_X + 2 * pair * C::STAGE + r * C::ROW;
-        // The warp's rows of a tile: a step takes 32 / PIECES rows, a lane 16 bytes.
-        constexpr int PIECES = D / 8, PER = 32 / PIECES;
-        const int sub = lane / PIECES, piece = lane % PIECES;
+        // The quarter's 32 rows of a tile, half of their pieces: a step takes PER rows, a lane 16 bytes.
+        constexpr int PIECES = D / 16, PER = 32 / PIECES;
+        const int sub = lane / PIECES, piece = lane % PIECES + which * PIECES;
         int pos_of[2] = {0, 0};  // positions of this thread's row of the tiles in the two places
         auto fetch = [&](int64_t tile, int stage) {
             if (tile < tiles) {
-                const int kind = kind_of(tile);
                 int t, h;
                 const uint16_t *x = nullptr;
-                if (row_of(tile, kind, t, h)) {
-                    x = source(kind, t, h);
+                if (row_of(tile, t, h)) {
+                    x = source(t, h);
                     if (kind < 2 && a.rope_dim) pos_of[stage] = a.positions[t];
                 }
                 const uint32_t dst =
@@ -345,6 +337,7 @@ __global__ void __launch_bounds__(A_THREADS, 1) kq_kv_append_kernel(const __grid
         };
         fetch(tile, 0);
         fetch(tile + 2 * step, 1);
+        __syncthreads();  // the factor
         const uint32_t ta = tmem + lanes;
         constexpr uint32_t idesc = idesc_bf16_f32_bn(128, D);
         uint32_t products = 0;
@@ -352,8 +345,8 @@ __global__ void __launch_bounds__(A_THREADS, 1) kq_kv_append_kernel(const __grid
         auto multiply = [&](int terms, bool accumulate, bool last) {
             tmem_wait_st();
             tc_fence_before();
-            named_barrier_sync(1 + pair, 128);
-            if ((warp & 3) == 0) {
+            named_barrier_sync(1 + pair, 256);
+            if ((warp & 7) == 0) {
                 if (!accumulate) wait(taken, (turns & 1u) ^ 1u);  // the last tile's rows
                 tc_fence_after();
                 if (elect_one()) {
@@ -377,59 +370,55 @@ __global__ void __launch_bounds__(A_THREADS, 1) kq_kv_append_kernel(const __grid
             tc_fence_after();
         };
         const bool inter = a.rope_interleaved != 0;
-        for (int kind = 0; kind < 3; ++kind) {
-            if (!begin_kind(kind, end)) continue;
-            for (; tile < end; tile += 2 * step, ++turns) {
-                const int stage = int(turns & 1u);
-                const unsigned char *x = place0 + stage * C::STAGE;
-                const int64_t pos = stage ? pos_of[1] : pos_of[0];
-                const float *cs = a.rope + (pos >= 0 && pos < a.rope_positions ? pos : 0) * a.rope_dim;
-                cp_async_wait<1>();
-                __syncwarp();
-                multiplied();
-                if (kind == 2) {
+        for (; tile < tiles; tile += 2 * step, ++turns) {
+            const int stage = int(turns & 1u);
+            const unsigned char *x = place0 + stage * C::STAGE;
+            const int64_t pos = stage ? pos_of[1] : pos_of[0];
+            const float *cs = a.rope + (pos >= 0 && pos < a.rope_positions ? pos : 0) * a.rope_dim;
+            cp_async_wait<1>();
+            named_barrier_sync(3 + pair, 256);  // the other warp's pieces
+            multiplied();
+            if (kind == 2) {
 #pragma unroll
-                    for (int i = 0; i < D / 8; ++i) {
-                        const uint4 u = reinterpret_cast<const uint4 *>(x)[i];
-                        tmem_st_32x32b_x4(ta + uint32_t(4 * i), u.x, u.y, u.z, u.w);
-                    }
-                    multiply(1, false, true);
-                } else {
-                    // queries: both terms; keys: the second and third, and then the first
-                    rotated_row<D>(x, cs, a.rope_dim, inter, [&](int i, float (&v)[8]) {
+                for (int i = 0; i < D / 16; ++i) {
+                    const uint4 u = reinterpret_cast<const uint4 *>(x)[2 * i + which];
+                    tmem_st_32x32b_x4(ta + uint32_t(4 * (2 * i + which)), u.x, u.y, u.z, u.w);
+                }
+                multiply(1, false, true);
+            } else {
+                // queries: both terms; keys: the second and third, and then the first
+                rotated_row<D>(x, cs, a.rope_dim, inter, which, [&](int i, float (&v)[8]) {
+                    uint32_t w[4];
+                    take_term(v, w);
+                    if (kind == 1) take_term(v, w);
+                    tmem_st_32x32b_x4(ta + uint32_t(i >> 1), w[0], w[1], w[2], w[3]);
+                    tmem_st_32x32b_x4(ta + 64 + uint32_t(i >> 1), pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                      pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+                });
+                multiply(2, false, kind == 0);
+                if (kind == 1) {
+                    multiplied();
+                    rotated_row<D>(x, cs, a.rope_dim, inter, which, [&](int i, float (&v)[8]) {
                         uint32_t w[4];
                         take_term(v, w);
-                        if (kind == 1) take_term(v, w);
                         tmem_st_32x32b_x4(ta + uint32_t(i >> 1), w[0], w[1], w[2], w[3]);
-                        tmem_st_32x32b_x4(ta + 64 + uint32_t(i >> 1), pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                          pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
                     });
-                    multiply(2, false, kind == 0);
-                    if (kind == 1) {
-                        multiplied();
-                        rotated_row<D>(x, cs, a.rope_dim, inter, [&](int i, float (&v)[8]) {
-                            uint32_t w[4];
-                            take_term(v, w);
-                            tmem_st_32x32b_x4(ta + uint32_t(i >> 1), w[0], w[1], w[2], w[3]);
-                        });
-                        multiply(1, true, true);
-                    }
+                    multiply(1, true, true);
                 }
-                __syncwarp();  // all lanes have read the warp's rows
-                fetch(tile + 4 * step, stage);
             }
+            fetch(tile + 4 * step, stage);  // all warps have read the tile's rows: they were at multiply's barrier
         }
         cp_async_wait<0>();
         multiplied();
     } else {
         // ---------------- rows out ----------------
         const uint32_t td = tmem + lanes + 128;
-        unsigned char *const own = smem + C::OFF_Y + (warp - 8) * 4096;
-        for (int kind = 0; kind < 3; ++kind) {
-            if (!begin_kind(kind, end)) continue;
-            for (; tile < end; tile += 2 * step, ++turns) {
+        unsigned char *const own = smem + C::OFF_Y + (warp - 16) * 4096;
+        __syncthreads();  // the factor
+        {
+            for (; tile < tiles; tile += 2 * step, ++turns) {
                 int t, h;
-                const bool real = row_of(tile, kind, t, h);
+                const bool real = row_of(tile, t, h);
                 int64_t slot = -1;
                 bool pos_ok = true;
                 const float *cs = a.rope;
@@ -477,7 +466,7 @@ __global__ void __launch_bounds__(A_THREADS, 1) kq_kv_append_kernel(const __grid
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const int row = 4 * i + (lane >> 3);
-                            if (row0 + row < rows_q)
+                            if (row0 + row < rows)
                                 *reinterpret_cast<uint4 *>(a.q_out + (row0 + row) * D + 64 * c + 8 * (lane & 7)) =
                                     *reinterpret_cast<const uint4 *>(own + 128 * row + (((lane ^ row) & 7) << 4));
                         }
@@ -526,7 +515,7 @@ __global__ void __launch_bounds__(A_THREADS, 1) kq_kv_append_kernel(const __grid
                     const bool near = store && m < 3.0e38f &&
                                       (off > 0.5f - 7.0f * kBorder / alpha || (m > 0.0f && sc < 1e-30f));
                     uint32_t again = __ballot_sync(0xffffffffu, near);
-                    const uint16_t *x = source(kind, t, h);
+                    const uint16_t *x = source(t, h);
                     while (again) {
                         const int src = __ffs(again) - 1;
                         again &= again - 1;
@@ -621,8 +610,25 @@ static cudaError_t launch_append_inst(const KvAppendArgs &a, int num_sms, int de
         attr_err[device] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     });
     if (attr_err[device] != cudaSuccess) return attr_err[device];
-    const int64_t tiles = (a.T * a.q_heads + 127) / 128 + 2 * ((a.T * a.c.heads + 127) / 128);
-    return launch_overlapped(kern, unsigned(tiles < num_sms ? tiles : num_sms), A_THREADS, C::SMEM, stream, a);
+    // Blocks for each kind: one more at a time to the kind whose blocks have the most to do.  A tile of keys
+    // takes about 1.6 times, one of values 1.0 times what one of queries does.
+    const int64_t tiles[3] = {(a.T * a.q_heads + 127) / 128, (a.T * a.c.heads + 127) / 128,
+                              (a.T * a.c.heads + 127) / 128};
+    const double cost[3] = {1.0, 1.6, 1.0};
+    int blocks[3] = {tiles[0] > 0, 1, 1};
+    for (int n = blocks[0] + 2; n < num_sms; ++n) {
+        int most = -1;
+        double load = 0.0;
+        for (int k = 0; k < 3; ++k) {
+            if (blocks[k] >= tiles[k]) continue;
+            const double l = cost[k] * double((tiles[k] + blocks[k] - 1) / blocks[k]);
+            if (l > load) most = k, load = l;
+        }
+        if (most < 0) break;
+        ++blocks[most];
+    }
+    return launch_overlapped(kern, unsigned(blocks[0] + blocks[1] + blocks[2]), A_THREADS, C::SMEM, stream, a, blocks[0],
+                             blocks[1], blocks[2]);
 }
 
 cudaError_t launch_kv_append(const KvAppendArgs &a, int num_sms, int device, cudaStream_t stream) {
