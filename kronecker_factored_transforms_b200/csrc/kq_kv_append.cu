@@ -315,28 +315,33 @@ __global__ void __launch_bounds__(A_THREADS, 1)
         // The quarter's 32 rows of a tile, half of their pieces: a step takes PER rows, a lane 16 bytes.
         constexpr int PIECES = D / 16, PER = 32 / PIECES;
         const int sub = lane / PIECES, piece = lane % PIECES + which * PIECES;
-        int pos_of[2] = {0, 0};  // positions of this thread's row of the tiles in the two places
-        auto fetch = [&](int64_t tile, int stage) {
-            if (tile < tiles) {
-                int t, h;
-                const uint16_t *x = nullptr;
-                if (row_of(tile, t, h)) {
-                    x = source(t, h);
-                    if (kind < 2 && a.rope_dim) pos_of[stage] = a.positions[t];
-                }
-                const uint32_t dst =
-                    smem_u32(place0 + stage * C::STAGE - lane * C::ROW) + uint32_t(sub * C::ROW + 16 * piece);
+        // This thread's row of a tile (null past the last), and its position: both an iteration ahead of their use.
+        auto look = [&](int64_t tile, const uint16_t *&x, int &pos) {
+            x = nullptr;
+            pos = 0;
+            int t, h;
+            if (tile < tiles && row_of(tile, t, h)) {
+                x = source(t, h);
+                if (kind < 2 && a.rope_dim) pos = a.positions[t];
+            }
+        };
+        auto fetch = [&](const uint16_t *x, int stage) {
+            const uint32_t dst =
+                smem_u32(place0 + stage * C::STAGE - lane * C::ROW) + uint32_t(sub * C::ROW + 16 * piece);
 #pragma unroll
-                for (int i = 0; i < 32 / PER; ++i) {
-                    const uint64_t src = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(x), i * PER + sub);
-                    cp_async16(dst + uint32_t(i * PER * C::ROW), src ? src + 16 * piece : reinterpret_cast<uint64_t>(a.Pk),
-                               src ? 16u : 0u);  // rows past the last are zeros
-                }
+            for (int i = 0; i < 32 / PER; ++i) {
+                const uint64_t src = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(x), i * PER + sub);
+                cp_async16(dst + uint32_t(i * PER * C::ROW), src ? src + 16 * piece : reinterpret_cast<uint64_t>(a.Pk),
+                           src ? 16u : 0u);  // rows past the last are zeros
             }
             cp_async_commit();
         };
-        fetch(tile, 0);
-        fetch(tile + 2 * step, 1);
+        const uint16_t *x2;
+        int pos0, pos1, pos2;
+        look(tile, x2, pos0);
+        fetch(x2, 0);
+        look(tile + 2 * step, x2, pos1);
+        fetch(x2, 1);
         __syncthreads();  // the factor
         const uint32_t ta = tmem + lanes;
         constexpr uint32_t idesc = idesc_bf16_f32_bn(128, D);
@@ -373,8 +378,8 @@ __global__ void __launch_bounds__(A_THREADS, 1)
         for (; tile < tiles; tile += 2 * step, ++turns) {
             const int stage = int(turns & 1u);
             const unsigned char *x = place0 + stage * C::STAGE;
-            const int64_t pos = stage ? pos_of[1] : pos_of[0];
-            const float *cs = a.rope + (pos >= 0 && pos < a.rope_positions ? pos : 0) * a.rope_dim;
+            const float *cs = a.rope + int64_t(uint32_t(pos0) < uint32_t(a.rope_positions) ? pos0 : 0) * a.rope_dim;
+            look(tile + 4 * step, x2, pos2);
             cp_async_wait<1>();
             named_barrier_sync(3 + pair, 256);  // the other warp's pieces
             multiplied();
@@ -406,7 +411,9 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                     multiply(1, true, true);
                 }
             }
-            fetch(tile + 4 * step, stage);  // all warps have read the tile's rows: they were at multiply's barrier
+            fetch(x2, stage);  // all warps have read the tile's rows: they were at multiply's barrier
+            pos0 = pos1;
+            pos1 = pos2;
         }
         cp_async_wait<0>();
         multiplied();
@@ -415,25 +422,36 @@ __global__ void __launch_bounds__(A_THREADS, 1)
         const uint32_t td = tmem + lanes + 128;
         unsigned char *const own = smem + C::OFF_Y + (warp - 16) * 4096;
         __syncthreads();  // the factor
+        // This thread's row of a tile, its slot and position, loaded a tile ahead of their use.
+        struct Row {
+            int t, h, pos;
+            bool real;
+            int64_t slot;
+        };
+        auto look = [&](int64_t tile) {
+            Row w;
+            w.pos = 0;
+            w.slot = -1;
+            w.real = row_of(tile, w.t, w.h) && tile < tiles;
+            if (w.real) {
+                if (kind != 0) w.slot = a.slots[w.t];
+                if (a.rope_dim) w.pos = a.positions[w.t];
+            }
+            return w;
+        };
+        Row next = look(tile);
         {
             for (; tile < tiles; tile += 2 * step, ++turns) {
-                int t, h;
-                const bool real = row_of(tile, t, h);
-                int64_t slot = -1;
-                bool pos_ok = true;
-                const float *cs = a.rope;
-                if (real) {
-                    if (kind != 0) slot = a.slots[t];
-                    if (a.rope_dim) {
-                        const int64_t pos = a.positions[t];
-                        pos_ok = pos >= 0 && pos < a.rope_positions;
-                        if (!pos_ok) atomicOr(a.err, kSiteKvAppend);
-                        cs += (pos_ok ? pos : 0) * a.rope_dim;
-                    }
-                    if (kind != 0 && slot >= a.c.pages << psh) {
-                        atomicOr(a.err, kSiteKvAppend);
-                        slot = -1;
-                    }
+                const Row now = next;
+                next = look(tile + 2 * step);
+                const int t = now.t, h = now.h;
+                const bool real = now.real;
+                const bool pos_ok = !a.rope_dim || uint32_t(now.pos) < uint32_t(a.rope_positions);
+                int64_t slot = now.slot;
+                const float *cs = a.rope + int64_t(pos_ok ? now.pos : 0) * a.rope_dim;
+                if (!pos_ok || (slot >= a.c.pages << psh)) {
+                    atomicOr(a.err, kSiteKvAppend);
+                    slot = -1;
                 }
                 wait(ready, turns & 1u);
                 tc_fence_after();
