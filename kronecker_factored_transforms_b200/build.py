@@ -10,8 +10,9 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libkq.so")
 SOURCES = ["kq_api.cu", "kq_warp_mma.cu", "kq_tc05.cu", "kq_fused.cu", "kq_inverse.cu", "kq_gemm.cu",
-           "kq_rowwise.cu", "kq_two_stage.cu", "kq_scratch.cu", "kq_kv_append.cu", "kq_kv_attention.cu"]
-HEADERS = ["kq_common.cuh", "kq_internal.h", "kq_tc05_ptx.cuh", "kq_tile.cuh", "kq_wait.cuh"]
+           "kq_rowwise.cu", "kq_two_stage.cu", "kq_scratch.cu", "kq_kv_append.cu", "kq_kv_attention.cu",
+           "kq_kv_tile.cu"]
+HEADERS = ["kq_common.cuh", "kq_internal.h", "kq_kv_plan.cuh", "kq_tc05_ptx.cuh", "kq_tile.cuh", "kq_wait.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -41,34 +41,18 @@
 
 #include <mutex>
 
-#include "kq_common.cuh"
-#include "kq_internal.h"
-#include "kq_wait.cuh"
+#include "kq_kv_plan.cuh"
 
 namespace kq {
 namespace {
 
+using namespace kv;
+
+constexpr float kNone = -1e30f;  // reference of a row that has seen no key
 constexpr int WARPS = 4;        // multiplying warps per block
 constexpr int MT = 2;           // tiles of 16 keys that each takes of a chunk
-constexpr int CH = 16 * MT * WARPS;  // keys per chunk
+static_assert(CH == 16 * MT * WARPS, "keys per chunk");
 constexpr int R_THREADS = 32 * (WARPS + 1);
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kNone = -1e30f;  // reference of a row that has seen no key
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float lg2(float x) {
-    float y;
-    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-// tanh as 1 - 2 / (e^2z + 1): off by about 2^-22, absolutely.
-__device__ __forceinline__ float tanh_exp(float z) {
-    return 1.0f - __fdividef(2.0f, ex2(z * (2.0f * kLog2e)) + 1.0f);
-}
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -98,80 +82,6 @@ __device__ __forceinline__ uint32_t and_xor(uint32_t w, uint32_t mask, uint32_t 
 }
 __device__ __forceinline__ uint32_t nib_lo(uint32_t w) { return and_xor(w, 0x000f000fu, 0x00080008u); }
 __device__ __forceinline__ uint32_t nib_hi(uint32_t w) { return and_xor(w, 0x00f000f0u, 0x00800080u); }
-
-// ---- which keys and rows a unit has ---------------------------------------------
-
-// The launch as both kernels see it.  "Sequence" B, where there is a shared prefix,
-// is the prefix with the queries of all sequences.
-struct Plan {
-    KvAttnArgs a;
-    int G;             // query heads per key head
-    int shared;        // a prefix is there
-    int ctas;          // blocks of the row kernel
-    int2 *parts;       // [2][T * H] for every row: the first block that has keys of it, and how many have
-    float *slot_o;     // [ctas][2][R][D] partial rows: a block's first unit, its last unit
-    float *slot_l;     // [ctas][2][R]
-    float *whole_o;    // [2][T * H][D] rows whose keys lay in one block (own keys; the prefix's)
-    float *whole_l;    // [2][T * H]
-};
-
-struct Seq {
-    int n;         // keys
-    int m;         // queries that are computed
-    int q0;        // first query token
-    int shift;     // query i sees the keys t <= shift + i
-    int c0, N;     // first chunk, chunks
-    int tiles;     // row tiles
-    const int32_t *pages;
-};
-
-// First query token and number of queries of sequence b, within the T tokens whatever q_start holds.
-__device__ __forceinline__ void queries_of(const KvAttnArgs &a, int64_t b, int &q0, int &m) {
-    q0 = int(b);
-    m = 1;
-    if (a.q_start) {
-        const int T = int(a.T);
-        q0 = min(max(a.q_start[b], 0), T);
-        m = max(min(a.q_start[b + 1], T) - q0, 0);
-    }
-}
-__device__ __forceinline__ int all_queries(const KvAttnArgs &a) {
-    return a.q_start ? min(max(a.q_start[a.B], 0), int(a.T)) : int(a.T);
-}
-
-template <int R>
-__device__ __forceinline__ Seq load_seq(const Plan &p, int64_t b, bool report) {
-    const KvAttnArgs &a = p.a;
-    Seq s;
-    int lo = 0;
-    if (b == a.B) {  // the shared prefix: every row sees all of it, but for a window
-        s.n = int(a.prefix_len);
-        s.q0 = 0;
-        s.m = all_queries(a);
-        s.shift = s.n;
-        s.pages = a.prefix_pages;
-    } else {
-        int m;
-        queries_of(a, b, s.q0, m);
-        const int given = max(a.kv_len[b], 0);
-        const int most = int(a.max_pages) << a.c.page_shift;
-        s.n = min(given, most);
-        s.m = min(m, a.max_q);
-        if (report && (given > most || m > a.max_q)) {
-            atomicOr(a.err, kSiteKvAttention);
-            for (int64_t r = int64_t(s.q0 + s.m) * a.q_heads; r < int64_t(s.q0 + m) * a.q_heads; ++r)
-                p.parts[r] = make_int2(0, 0);  // rows past the bound
-        }
-        s.shift = given - m;
-        s.pages = a.page_table + b * a.max_pages;
-        if (a.window) lo = max(0, s.shift - a.window + 1);
-    }
-    const int hi = min(s.n, max(0, s.shift + s.m));
-    s.c0 = min(lo, max(hi - 1, 0)) / CH;
-    s.N = max(1, (hi + CH - 1) / CH - s.c0);  // a unit without keys still has its rows to write
-    s.tiles = (s.m * p.G + R - 1) / R;
-    return s;
-}
 
 // The chunks of all units, dealt to the blocks: n each, and one more to the first `more`.  With
 // fewer chunks than blocks the last ones have none, so the blocks of a unit are consecutive.
@@ -210,19 +120,6 @@ struct Walk {
     }
 };
 
-// Position of token t's queries among the keys of its sequence (for windows over a prefix).
-__device__ __forceinline__ int query_shift(const KvAttnArgs &a, int t) {
-    if (!a.q_start) return a.kv_len[t] > 0 ? a.kv_len[t] - 1 : -1;
-    int lo = 0, hi = int(a.B);
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (a.q_start[mid + 1] <= t) lo = mid + 1;
-        else hi = mid;
-    }
-    if (lo == int(a.B)) return -1;
-    return max(a.kv_len[lo], 0) - (a.q_start[lo + 1] - a.q_start[lo]) + t - a.q_start[lo];
-}
-
 // ---- the row kernel ----------------------------------------------------------------
 
 template <int D, int NT>
@@ -259,14 +156,6 @@ struct Desc {
 static_assert(sizeof(Desc) == 64, "a stage's description");
 enum : uint32_t { kUnitBegins = 1u << 16, kUnitEnds = 1u << 17 };  // ends: or the block's share does
 constexpr int kWhole = -1;
-enum : unsigned { kSiteKvWait = 262144u };
-
-// Wait for a phase, suspended at first; gives up as wait_bounded_err does.
-__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile int *abort, unsigned int *err) {
-    if (__all_sync(0xffffffffu, tc::mbar_try_wait_for(bar, parity, 20000u))) return true;
-    return __all_sync(0xffffffffu,
-                      tc::wait_bounded_err(bar, parity, abort, kSiteKvWait, tc::kWaitLimitNs, false, err));
-}
 
 template <int D, int NT, bool CAP>
 __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel(const __grid_constant__ Plan p) {
@@ -277,7 +166,8 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
     const KvAttnArgs &a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int Hk = a.c.heads, H = a.q_heads, psh = a.c.page_shift;
-    const int64_t seqs = a.B + p.shared;
+    // sequences of the walk: the own keys', and the prefix last
+    const int64_t seqs = a.B + p.rows_prefix;
     const uint32_t sbase = smem_u32(smem);
     auto bar = [&](int i) -> uint32_t { return sbase + uint32_t(C::OFF_BAR + 8 * i); };
     volatile int *s_abort = reinterpret_cast<volatile int *>(smem + C::OFF_MISC);
@@ -350,7 +240,7 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
         const int piece = lane & (pieces - 1), what = lane / pieces;  // what: codes and scales of keys, of values
         auto page_of = [&]() -> int {
             const int t = w.c * CH + (piece << gsh);
-            return t < w.s.n ? w.s.pages[t >> psh] : -1;
+            return t < w.s.n && t + (1 << gsh) > w.s.lo ? w.s.pages[t >> psh] : -1;
         };
         int page = page_of();
         Ring rg;
@@ -358,8 +248,9 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
         for (int i = 0; i < steps; ++i, rg.next(C::STAGES)) {
             if (!wait_all(bar(C::EMPTY + rg.idx), rg.phase ^ 1u, s_abort, a.err)) break;
             const int t = w.c * CH + (piece << gsh);
-            const bool there = t < w.s.n && uint32_t(page) < uint32_t(a.c.pages);
-            if (t < w.s.n && !there && what == 0) atomicOr(a.err, kSiteKvAttention);
+            const bool wanted = t < w.s.n && t + (1 << gsh) > w.s.lo;
+            const bool there = wanted && uint32_t(page) < uint32_t(a.c.pages);
+            if (wanted && !there && what == 0) atomicOr(a.err, kSiteKvAttention);
             const uint32_t ok = __ballot_sync(0xffffffffu, there && lane < pieces);
             const int last = w.s.c0 + w.s.N - 1;
             const bool ends = w.c == last || i + 1 == steps;
@@ -751,7 +642,7 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
                 const int64_t at = int64_t(q0 + i) * H + h * p.G + (j - i * p.G);
                 v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
                 if (d == 0 && parts) rec[at] = make_int2(blockIdx.x, parts);
-                if (place == kWhole && !p.shared) {
+                if (place == kWhole && !p.partial) {
                     *reinterpret_cast<uint2 *>(a.out + at * D + d) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
                     if (a.lse && d == 0) a.lse[at] = lse * 0.6931471805599453f;
                 } else {
@@ -784,37 +675,50 @@ __global__ void __launch_bounds__(128) kq_kv_combine_kernel(const __grid_constan
     const int64_t rows = a.T * H;
     const int64_t at = WARPS_PER_ROW == 4 ? blockIdx.x : int64_t(blockIdx.x) * 4 + warp;
     const bool real = at < rows && at < int64_t(all_queries(a)) * H;  // not padding behind the last sequence
-    int2 rec[2] = {make_int2(0, 0), make_int2(0, 0)};
+    if (!real) return;
+    // own keys: parts of the row kernel (as its records say) or of the tile kernel, and so for the prefix's
+    int2 rec[2] = {make_int2(0, p.own_splits), make_int2(0, p.pre_splits)};
     int row[2] = {0, 0};
-    if (real) {
-        rec[0] = p.parts[at];
-        if (p.shared) rec[1] = p.parts[rows + at];
-    }
-    if (rec[0].y < 1 || rec[0].x < 0 || rec[0].x + rec[0].y > p.ctas || (!p.shared && rec[0].y == 1)) return;
-    if (p.shared && (rec[1].y < 1 || rec[1].x < 0 || rec[1].x + rec[1].y > p.ctas)) return;
+    if (p.rows_own) rec[0] = p.parts[at];
+    if (p.rows_prefix) rec[1] = p.parts[rows + at];
+    if ((p.rows_own && (rec[0].y < 1 || rec[0].x < 0 || rec[0].x + rec[0].y > p.ctas)) ||
+        (p.rows_prefix && (rec[1].y < 1 || rec[1].x < 0 || rec[1].x + rec[1].y > p.ctas)))
+        return;  // a row past the bound on queries
+    if (!p.partial && p.rows_own && rec[0].y == 1) return;  // written by its block
     const int n = rec[0].y + rec[1].y;
-    if (rec[0].y > 1 || rec[1].y > 1) {  // the row's place in its unit's tile
-        const int t = int(at / H), head = int(at - int64_t(t) * H), g = head % p.G;
-        int q0 = t;
-        if (a.q_start) {
-            int lo = 0, hi = int(a.B);
-            while (lo < hi) {
-                const int mid = (lo + hi) >> 1;
-                if (a.q_start[mid + 1] <= t) lo = mid + 1;
-                else hi = mid;
-            }
-            q0 = a.q_start[lo];
+    const bool cut0 = p.rows_own && rec[0].y > 1, cut1 = p.rows_prefix && rec[1].y > 1;
+    if (a.q_start && (cut0 || cut1 || !p.rows_own)) {  // the row's place in its unit's tile; whether it is bounded away
+        const int t = int(at / H), g = int(at - int64_t(t) * H) % p.G;
+        int lo = 0, hi = int(a.B);
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (a.q_start[mid + 1] <= t) lo = mid + 1;
+            else hi = mid;
         }
-        row[0] = ((t - q0) * p.G + g) % R;
+        const int i = t - a.q_start[lo];
+        if (i >= a.max_q) return;
+        row[0] = (i * p.G + g) % R;
+        row[1] = (t * p.G + g) % R;
+    } else if (cut0 || cut1) {
+        const int t = int(at / H), g = int(at - int64_t(t) * H) % p.G;
+        row[0] = g % R;
         row[1] = (t * p.G + g) % R;
     }
-    // where part k lies: its index among the partial (or whole) rows
-    auto place = [&](int k, bool &whole) -> int64_t {
+    // Where part k lies: the rows and sums that it is among, and its index there.
+    auto place = [&](int k, const float *&o, const float *&l) -> int64_t {
         const int u = k >= rec[0].y;
         const int i = u ? k - rec[0].y : k;
-        whole = rec[u].y == 1;
+        if (u ? !p.rows_prefix : !p.rows_own) {
+            o = p.tile_o, l = p.tile_l;
+            return int64_t((u ? p.own_splits : 0) + i) * rows + at;
+        }
+        if (rec[u].y == 1) {
+            o = p.whole_o, l = p.whole_l;
+            return u * rows + at;
+        }
+        o = p.slot_o, l = p.slot_l;
         // a unit's first block holds it as its last unit, the others as their first
-        return whole ? u * rows + at : (int64_t(rec[u].x + i) * 2 + (i == 0 ? 1 : 0)) * R + row[u];
+        return (int64_t(rec[u].x + i) * 2 + (i == 0 ? 1 : 0)) * R + row[u];
     };
     float top = -INFINITY, wsum = 0.0f;
     float v[D / 32];
@@ -824,13 +728,13 @@ __global__ void __launch_bounds__(128) kq_kv_combine_kernel(const __grid_constan
     for (int k0 = first; k0 < n; k0 += 32 * WARPS_PER_ROW) {
         const int mine = k0 + lane * WARPS_PER_ROW;
         float l = -INFINITY;
-        int64_t from = 0;
-        bool whole = false;
+        const float *src = p.slot_o;
         if (mine < n) {
-            from = place(mine, whole);
-            l = (whole ? p.whole_l : p.slot_l)[from];
+            const float *sums;
+            const int64_t from = place(mine, src, sums);
+            src += from * D;
+            l = sums[from];
         }
-        const float *src = (whole ? p.whole_o : p.slot_o) + from * D;
         float m = l;
 #pragma unroll
         for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -847,16 +751,18 @@ __global__ void __launch_bounds__(128) kq_kv_combine_kernel(const __grid_constan
         const int cnt = min(32, (n - k0 + WARPS_PER_ROW - 1) / WARPS_PER_ROW);
 #pragma unroll 4
         for (int k = 0; k < cnt; ++k) {
-            const float wk = __shfl_sync(0xffffffffu, w, k);
+            const float wk = __shfl_sync(0xffffffffu, w, k);  // 0 for a part without keys, whose values may be anything
             const float *sk = reinterpret_cast<const float *>(
                 __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), k));
             if constexpr (D == 128) {
                 const float4 z = reinterpret_cast<const float4 *>(sk)[lane];
-                v[0] = fmaf(z.x, wk, v[0]), v[1] = fmaf(z.y, wk, v[1]);
-                v[2] = fmaf(z.z, wk, v[2]), v[3] = fmaf(z.w, wk, v[3]);
+                if (wk != 0.0f) {
+                    v[0] = fmaf(z.x, wk, v[0]), v[1] = fmaf(z.y, wk, v[1]);
+                    v[2] = fmaf(z.z, wk, v[2]), v[3] = fmaf(z.w, wk, v[3]);
+                }
             } else {
                 const float2 z = reinterpret_cast<const float2 *>(sk)[lane];
-                v[0] = fmaf(z.x, wk, v[0]), v[1] = fmaf(z.y, wk, v[1]);
+                if (wk != 0.0f) v[0] = fmaf(z.x, wk, v[0]), v[1] = fmaf(z.y, wk, v[1]);
             }
         }
     }
@@ -888,29 +794,67 @@ __global__ void __launch_bounds__(128) kq_kv_combine_kernel(const __grid_constan
 // ---- host side ------------------------------------------------------------------------
 
 constexpr int kMaxCtas = 4 * 160;  // blocks of the row kernel, at most
-int row_tile(int G, int max_q) { return int64_t(G) * max_q <= 8 ? 8 : 16; }
+constexpr int kSms = 148;          // of a B200; the tile kernel has one block on each
+
+int row_tile(int64_t rows) { return rows <= 8 ? 8 : 16; }
+
+// Whether rows of one key head are the tile kernel's.  The row kernel takes up to two tiles of 8, for which
+// it reads every code once; beyond that it would read them again for every 16 rows, where the tile kernel's
+// tensor cores work on up to 256.
+bool many_rows(int64_t rows) { return rows > 16; }
+
+// Blocks to cut a unit's keys over, where there are too few units for all SMs: the number that leaves the
+// fewest SMs idle in the last round of blocks, with a hundredth off for each further part to join.
+int tile_splits(int64_t units, int64_t most) {
+    int best = 1;
+    double good = 0.0;
+    for (int s = 1; s <= 32 && s <= most && units * s <= 4 * kSms; ++s) {
+        const int64_t blocks = units * s, rounds = (blocks + kSms - 1) / kSms;
+        const double used = double(blocks) / double(rounds * kSms) - 0.01 * s;
+        if (used > good) best = s, good = used;
+    }
+    return best;
+}
 
 uint64_t align256(uint64_t x) { return (x + 255) & ~uint64_t(255); }
 
-// The workspace's parts, from `base`; returns the bytes.
-uint64_t lay_out(Plan *p, unsigned char *base, int64_t T, int H, int D, int R) {
+// Who does what, and the workspace's parts from `base`; returns the bytes.  `own_most`, `pre_most`: chunks
+// that a sequence, the prefix have at most (parts are no more; the sizes are laid out for any number).
+uint64_t lay_out(Plan &p, unsigned char *base, int64_t T, int64_t B, int H, int Hk, int D, int max_q, int64_t own_most,
+                 int64_t pre_most) {
+    const int G = H / Hk;
+    p.G = G;
+    const bool own_tile = many_rows(int64_t(max_q) * G), pre_tile = many_rows(T * G);
+    const int own = own_tile ? tile_splits(kv_tiles(max_q, G) * B * Hk, INT32_MAX) : 0;
+    const int pre = pre_tile ? tile_splits(kv_tiles(T, G) * Hk, INT32_MAX) : 0;
+    p.own_splits = own_tile ? tile_splits(kv_tiles(max_q, G) * B * Hk, own_most) : 0;
+    p.pre_splits = pre_most && pre_tile ? tile_splits(kv_tiles(T, G) * Hk, pre_most) : 0;
+    p.rows_own = !own_tile;
+    p.rows_prefix = pre_most && !pre_tile;
+    p.partial = pre_most > 0;
+    const int R = row_tile(pre_tile ? int64_t(max_q) * G : T * G);
+    const uint64_t rows = uint64_t(T) * H;
     uint64_t at = 0;
     auto take = [&](uint64_t bytes) {
         unsigned char *r = base + at;
         at += align256(bytes);
         return r;
     };
-    unsigned char *parts = take(uint64_t(T) * H * 2 * 8);
-    unsigned char *so = take(uint64_t(kMaxCtas) * 2 * R * D * 4), *sl = take(uint64_t(kMaxCtas) * 2 * R * 4);
-    unsigned char *wo = take(uint64_t(T) * H * 2 * D * 4), *wl = take(uint64_t(T) * H * 2 * 4);
-    if (p) {
-        p->parts = reinterpret_cast<int2 *>(parts);
-        p->slot_o = reinterpret_cast<float *>(so);
-        p->slot_l = reinterpret_cast<float *>(sl);
-        p->whole_o = reinterpret_cast<float *>(wo);
-        p->whole_l = reinterpret_cast<float *>(wl);
-    }
+    p.parts = reinterpret_cast<int2 *>(take(rows * 2 * 8));
+    p.slot_o = reinterpret_cast<float *>(take(own_tile ? 0 : uint64_t(kMaxCtas) * 2 * R * D * 4));
+    p.slot_l = reinterpret_cast<float *>(take(own_tile ? 0 : uint64_t(kMaxCtas) * 2 * R * 4));
+    p.whole_o = reinterpret_cast<float *>(take(own_tile ? 0 : rows * 2 * D * 4));
+    p.whole_l = reinterpret_cast<float *>(take(own_tile ? 0 : rows * 2 * 4));
+    p.tile_o = reinterpret_cast<float *>(take(uint64_t(own + pre) * rows * D * 4));
+    p.tile_l = reinterpret_cast<float *>(take(uint64_t(own + pre) * rows * 4));
     return at;
+}
+
+template <int D, int R>
+cudaError_t launch_combine(const Plan &p, cudaStream_t stream) {
+    const int64_t rows = p.a.T * p.a.q_heads;
+    return rows <= 2048 ? launch_overlapped(kq_kv_combine_kernel<D, R, 4>, unsigned(rows), 128, 0, stream, p)
+                        : launch_overlapped(kq_kv_combine_kernel<D, R, 1>, unsigned((rows + 3) / 4), 128, 0, stream, p);
 }
 
 template <int D, int NT, bool CAP>
@@ -925,35 +869,41 @@ cudaError_t launch_rows(Plan &p, int num_sms, int device, cudaStream_t stream) {
     });
     if (attr_err[device] != cudaSuccess) return attr_err[device];
     p.ctas = num_sms * C::OCC < kMaxCtas ? num_sms * C::OCC : kMaxCtas;
-    cudaError_t e = launch_overlapped(kern, unsigned(p.ctas), R_THREADS, C::SMEM, stream, p);
-    if (e != cudaSuccess) return e;
-    const int64_t rows = p.a.T * p.a.q_heads;
-    return rows <= 2048 ? launch_overlapped(kq_kv_combine_kernel<D, C::R, 4>, unsigned(rows), 128, 0, stream, p)
-                        : launch_overlapped(kq_kv_combine_kernel<D, C::R, 1>, unsigned((rows + 3) / 4), 128, 0, stream, p);
+    return launch_overlapped(kern, unsigned(p.ctas), R_THREADS, C::SMEM, stream, p);
 }
 
 template <int D, int NT>
-cudaError_t launch_cap(Plan &p, int num_sms, int device, cudaStream_t stream) {
-    return p.a.softcap > 0.0f ? launch_rows<D, NT, true>(p, num_sms, device, stream)
-                              : launch_rows<D, NT, false>(p, num_sms, device, stream);
+cudaError_t launch_all(Plan &p, int num_sms, int device, cudaStream_t stream) {
+    cudaError_t e = cudaSuccess;
+    p.ctas = 0;
+    if (p.rows_own)
+        e = p.a.softcap > 0.0f ? launch_rows<D, NT, true>(p, num_sms, device, stream)
+                               : launch_rows<D, NT, false>(p, num_sms, device, stream);
+    else
+        e = launch_kv_tile(p, false, p.own_splits, device, stream);
+    if (e == cudaSuccess && p.pre_splits) e = launch_kv_tile(p, true, p.pre_splits, device, stream);
+    if (e != cudaSuccess || (!p.rows_own && !p.partial && p.own_splits == 1)) return e;
+    return launch_combine<D, 8 * NT>(p, stream);
 }
 
 }  // namespace
 
-uint64_t kv_attention_workspace_bytes(int64_t T, int64_t, int q_heads, int kv_heads, int head_dim, int max_q) {
-    return lay_out(nullptr, nullptr, T, q_heads, head_dim, row_tile(q_heads / kv_heads, max_q));
+uint64_t kv_attention_workspace_bytes(int64_t T, int64_t B, int q_heads, int kv_heads, int head_dim, int max_q) {
+    Plan p;
+    return lay_out(p, nullptr, T, B, q_heads, kv_heads, head_dim, max_q, 1, 1);
 }
 
 cudaError_t launch_kv_attention(const KvAttnArgs &a, int num_sms, int device, cudaStream_t stream) {
     Plan p;
     p.a = a;
-    p.G = a.q_heads / a.c.heads;
-    p.shared = a.prefix_pages != nullptr;
-    const int R = row_tile(p.G, a.max_q);
-    lay_out(&p, a.workspace, a.T, a.q_heads, a.c.D, R);
+    const int64_t own_most = ((a.max_pages << a.c.page_shift) + CH - 1) / CH;
+    const int64_t pre_most = a.prefix_pages ? (a.prefix_len + CH - 1) / CH : 0;
+    lay_out(p, a.workspace, a.T, a.B, a.q_heads, a.c.heads, a.c.D, a.max_q, own_most, pre_most);
+    const int64_t rows = p.rows_prefix ? a.T * p.G : int64_t(a.max_q) * p.G;
+    const bool one = row_tile(rows) == 8;
     if (a.c.D == 128)
-        return R == 8 ? launch_cap<128, 1>(p, num_sms, device, stream) : launch_cap<128, 2>(p, num_sms, device, stream);
-    return R == 8 ? launch_cap<64, 1>(p, num_sms, device, stream) : launch_cap<64, 2>(p, num_sms, device, stream);
+        return one ? launch_all<128, 1>(p, num_sms, device, stream) : launch_all<128, 2>(p, num_sms, device, stream);
+    return one ? launch_all<64, 1>(p, num_sms, device, stream) : launch_all<64, 2>(p, num_sms, device, stream);
 }
 
 }  // namespace kq

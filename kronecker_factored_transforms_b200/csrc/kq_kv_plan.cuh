@@ -1,0 +1,140 @@
+// kq_kv_plan.cuh -- what the kernels of the attention over the INT4 key / value cache
+// share: which keys and rows a sequence has, the workspace's parts, small arithmetic.
+#pragma once
+
+#include <limits.h>
+
+#include "kq_common.cuh"
+#include "kq_internal.h"
+#include "kq_wait.cuh"
+
+namespace kq {
+namespace kv {
+
+constexpr int CH = 128;  // keys per chunk
+enum : unsigned { kSiteKvWait = 262144u };
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// tanh as 1 - 2 / (e^2z + 1): off by about 2^-22, absolutely.
+__device__ __forceinline__ float tanh_exp(float z) {
+    return 1.0f - __fdividef(2.0f, ex2(z * (2.0f * kLog2e)) + 1.0f);
+}
+// Wait for a phase, suspended at first; gives up as wait_bounded_err does.
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile int *abort, unsigned int *err) {
+    if (__all_sync(0xffffffffu, tc::mbar_try_wait_for(bar, parity, 20000u))) return true;
+    return __all_sync(0xffffffffu,
+                      tc::wait_bounded_err(bar, parity, abort, kSiteKvWait, tc::kWaitLimitNs, false, err));
+}
+
+// ---- which keys and rows a unit has ---------------------------------------------
+
+// The launch as its kernels see it.  "Sequence" B, where there is a shared prefix,
+// is the prefix with the queries of all sequences.  Own keys and the prefix's are each
+// the row kernel's or the tile kernel's.
+struct Plan {
+    KvAttnArgs a;
+    int G;             // query heads per key head
+    int partial;       // a prefix is there: every kernel's rows are parts, joined at the end
+    int rows_own, rows_prefix;   // the row kernel has the own keys, the prefix's
+    int own_splits, pre_splits;  // the tile kernel's parts of a row, of own keys and of the prefix's (0: not its)
+    int ctas;          // blocks of the row kernel
+    int2 *parts;       // [2][T * H] for every row: the first block that has keys of it, and how many have
+    float *slot_o;     // [ctas][2][R][D] partial rows: a block's first unit, its last unit
+    float *slot_l;     // [ctas][2][R]
+    float *whole_o;    // [2][T * H][D] rows whose keys lay in one block (own keys; the prefix's)
+    float *whole_l;    // [2][T * H]
+    float *tile_o;     // [own_splits + pre_splits][T * H][D] parts of rows
+    float *tile_l;     // [own_splits + pre_splits][T * H]
+};
+
+struct Seq {
+    int n;         // keys
+    int m;         // queries that are computed
+    int q0;        // first query token
+    int shift;     // query i sees the keys t <= shift + i
+    int lo;        // no query sees a key below
+    int c0, N;     // first chunk, chunks
+    int tiles;     // row tiles
+    const int32_t *pages;
+};
+
+// First query token and number of queries of sequence b, within the T tokens whatever q_start holds.
+__device__ __forceinline__ void queries_of(const KvAttnArgs &a, int64_t b, int &q0, int &m) {
+    q0 = int(b);
+    m = 1;
+    if (a.q_start) {
+        const int T = int(a.T);
+        q0 = min(max(a.q_start[b], 0), T);
+        m = max(min(a.q_start[b + 1], T) - q0, 0);
+    }
+}
+__device__ __forceinline__ int all_queries(const KvAttnArgs &a) {
+    return a.q_start ? min(max(a.q_start[a.B], 0), int(a.T)) : int(a.T);
+}
+
+template <int R>
+__device__ __forceinline__ Seq load_seq(const Plan &p, int64_t b, bool report) {
+    const KvAttnArgs &a = p.a;
+    Seq s;
+    int lo = 0;
+    if (b == a.B) {  // the shared prefix: every row sees all of it, but for a window
+        s.n = int(a.prefix_len);
+        s.q0 = 0;
+        s.m = all_queries(a);
+        s.shift = s.n;
+        s.pages = a.prefix_pages;
+    } else {
+        int m;
+        queries_of(a, b, s.q0, m);
+        const int given = max(a.kv_len[b], 0);
+        const int most = int(a.max_pages) << a.c.page_shift;
+        s.n = min(given, most);
+        s.m = min(m, a.max_q);
+        if (report && (given > most || m > a.max_q)) {
+            atomicOr(a.err, kSiteKvAttention);
+            for (int64_t r = int64_t(s.q0 + s.m) * a.q_heads; r < int64_t(s.q0 + m) * a.q_heads; ++r)
+                p.parts[r] = make_int2(0, 0);  // rows past the bound
+        }
+        s.shift = given - m;
+        s.pages = a.page_table + b * a.max_pages;
+        if (a.window) lo = max(0, s.shift - a.window + 1);
+    }
+    const int hi = min(s.n, max(0, s.shift + s.m));
+    s.lo = lo;
+    s.c0 = min(lo, max(hi - 1, 0)) / CH;
+    s.N = max(1, (hi + CH - 1) / CH - s.c0);  // a unit without keys still has its rows to write
+    s.tiles = (s.m * p.G + R - 1) / R;
+    return s;
+}
+
+// Position of token t's queries among the keys of its sequence (for windows over a prefix).
+__device__ __forceinline__ int query_shift(const KvAttnArgs &a, int t) {
+    if (!a.q_start) return a.kv_len[t] > 0 ? a.kv_len[t] - 1 : -1;
+    int lo = 0, hi = int(a.B);
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (a.q_start[mid + 1] <= t) lo = mid + 1;
+        else hi = mid;
+    }
+    if (lo == int(a.B)) return -1;
+    return max(a.kv_len[lo], 0) - (a.q_start[lo + 1] - a.q_start[lo]) + t - a.q_start[lo];
+}
+
+}  // namespace kv
+
+// Row tiles (256 rows of a key head) of m queries with G heads each.
+inline int64_t kv_tiles(int64_t m, int G) { return (m * G + 255) / 256; }
+// The tile kernel over the own keys of all sequences, or over the prefix.
+cudaError_t launch_kv_tile(const kv::Plan &p, bool prefix, int splits, int device, cudaStream_t stream);
+
+}  // namespace kq

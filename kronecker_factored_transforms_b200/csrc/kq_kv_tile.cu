@@ -1,0 +1,517 @@
+// kq_kv_tile.cu -- attention over the INT4 key / value cache for many query rows per
+// key head: chunks of prompts, and the queries of a whole batch against the prefix that
+// its sequences share.
+//
+// There the products bound it, 4 head_dim flops per row and key on the tensor cores,
+// and beside them the exponentials: 16 a clock and SM, so that 256 rows x 128 keys take
+// 2048 clocks in either.  A block has 256 rows of one key head, as two tiles of 128
+// (MMA's M, one row per TMEM lane), and walks 128 keys at a time:
+//   - one warpgroup brings the codes: a thread reads the 64 or 32 bytes of its key's row
+//     and of its value's row a tile ahead, turns them into bf16 integers (exact) and
+//     lays them out as operands: K with head_dim contiguous, V with the keys as MMA's K
+//     and head_dim as N.  Both row tiles multiply by them.  A word's nibbles come out in
+//     the order 0 4 1 5 2 6 3 7; queries are laid in the same order, and the output is
+//     put right where it leaves.
+//   - scores S = Q K^T into TMEM, one warpgroup per row tile for the softmax, a thread
+//     per row: x = S ks with the key's scale (times the softmax scale), its maximum, then
+//     p = 2^(x - m); p times the value's scale goes back over S as bf16, O += P V.  The
+//     scales never meet the codes, and the sum of p is fp32 with unrounded terms.  A
+//     weight's rounding to bf16 (2^-9 at most) is of the size of the output's own.
+//   - m follows the row's maximum only when it passes m + 8 (weights stay under 2^8):
+//     O has to be rescaled then, which is rare.
+//   - the two row tiles are half a step apart: while one warpgroup is at its softmax
+//     the tensor core works for the other.
+// Keys that a row does not see, past its place or out of its window, are looked at only
+// in the chunks where a warp's rows have any; those and capped scores go through TMEM
+// once more.
+//
+// One unit = 256 rows of a key head and sequence, cut over `splits` blocks along its keys
+// where there are fewer units than SMs; partial rows then go to the workspace for
+// kq_kv_combine_kernel.
+#include <mutex>
+
+#include "kq_kv_plan.cuh"
+
+namespace kq {
+namespace {
+
+using namespace kv;
+using namespace tc;
+
+constexpr int T_THREADS = 416;  // two warpgroups of softmax, one of codes, a warp of MMAs
+constexpr int T_ROWS = 256;
+
+template <int D>
+struct TCfg {
+    static constexpr int HALF = 128 * 128;           // 128 rows of 64 bf16 values
+    static constexpr int OPERAND = HALF * (D / 64);  // 128 rows of D values
+    static constexpr int OFF_Q = 0;
+    static constexpr int OFF_K = 2 * OPERAND;
+    static constexpr int OFF_V = OFF_K + 2 * OPERAND;
+    static constexpr int OFF_SC = OFF_V + 2 * OPERAND;  // per stage 128 key scales, 128 value scales
+    static constexpr int OFF_BAR = OFF_SC + 2 * 1024;
+    enum { KFULL = 0, KFREE = 2, VFULL = 4, VFREE = 6, SREADY = 8, PREADY = 10, ODONE = 12, SCFREE = 14, DONE = 16, NBAR = 17 };
+    static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
+    static constexpr int SMEM = OFF_MISC + 16 + 1024;  // TMEM base, abort flag, per stage whether keys lack a page
+    static constexpr int COL_S = 0, COL_O = 256;  // TMEM columns: S of tile q at 128 q, O at 256 + D q
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+// TMEM store, 16 columns; and the pairs arithmetic.
+__device__ __forceinline__ uint64_t pair2(float a, float b) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t pair2u(uint32_t a, uint32_t b) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ void split2(uint64_t d, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(d));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// Eight codes as bf16 integers, pairs (0, 4), (1, 5), (2, 6), (3, 7): (code + 8) | 0x4300 is 136 + code.
+__device__ __forceinline__ uint4 codes_bf16(uint32_t w) {
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t t;
+        // (x & 0xf) ^ (0x4300 | 8)
+        asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(t) : "r"(w >> (4 * i)), "r"(0x000f000fu), "r"(0x43084308u));
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(t), "r"(0x43084308u));
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+// Eight consecutive bf16 values in that order.
+__device__ __forceinline__ uint4 order_bf16(const uint4 &u) {
+    return make_uint4(__byte_perm(u.x, u.z, 0x5410), __byte_perm(u.x, u.z, 0x7632), __byte_perm(u.y, u.w, 0x5410),
+                      __byte_perm(u.y, u.w, 0x7632));
+}
+// Place of 16-byte piece u of row r in an operand of D values a row (128-byte swizzle).
+__device__ __forceinline__ uint32_t operand_place(int r, int u) {
+    return uint32_t((u >> 3) * (128 * 128) + r * 128 + (((u ^ r) & 7) << 4));
+}
+
+template <int D, bool CAP>
+__global__ void __launch_bounds__(T_THREADS, 1)
+    kq_kv_tile_kernel(const __grid_constant__ Plan p, int prefix, int splits, int tiles, int units_b) {
+    using C = TCfg<D>;
+    extern __shared__ __align__(1024) unsigned char t_raw[];
+    const uint32_t raw_addr = smem_u32(t_raw), sbase = (raw_addr + 1023u) & ~1023u;
+    unsigned char *smem = t_raw + (sbase - raw_addr);
+    const KvAttnArgs &a = p.a;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2;
+    const int Hk = a.c.heads, H = a.q_heads, psh = a.c.page_shift;
+    auto bar = [&](int i) -> uint32_t { return sbase + uint32_t(C::OFF_BAR + 8 * i); };
+    volatile int *s_abort = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(C::KFULL + i), 128);
+            mbar_init(bar(C::VFULL + i), 128);
+            mbar_init(bar(C::KFREE + i), 1);
+            mbar_init(bar(C::VFREE + i), 1);
+            mbar_init(bar(C::SREADY + i), 1);
+            mbar_init(bar(C::PREADY + i), 4);
+            mbar_init(bar(C::ODONE + i), 1);
+            mbar_init(bar(C::SCFREE + i), 8);
+        }
+        mbar_init(bar(C::DONE), 1);
+        *s_abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 12) {
+        tmem_alloc(sbase + C::OFF_MISC, 512);
+        tmem_relinquish();
+    }
+    griddep_wait();
+
+    // ---- the block's unit: rows, and its part of their keys ----
+    const int id = int(blockIdx.x), split = id % splits;
+    int u = id / splits;
+    const int h = u % Hk;
+    u /= Hk;
+    const int64_t b = prefix ? a.B : u % units_b;
+    const int tile = tiles - 1 - u / units_b;  // the last rows of a chunk have the most keys: they come first
+    const Seq s = load_seq<T_ROWS>(p, b, tile == 0 && h == 0 && split == 0 && tid == 0 && !prefix);
+    const int rows = min(T_ROWS, s.m * p.G - tile * T_ROWS);
+    const int first = tile * T_ROWS / p.G, last = (tile * T_ROWS + max(rows, 1) - 1) / p.G;  // queries
+    // keys that some row of the tile sees
+    int hi = min(s.n, max(0, s.shift + last + 1)), lo = 0;
+    if (a.window && !prefix) lo = min(max(0, s.shift + first - a.window + 1), hi);
+    const int c0 = lo / CH, chunks = (hi + CH - 1) / CH - c0;
+    const int j0 = c0 + int(int64_t(chunks) * split / splits), j1 = c0 + int(int64_t(chunks) * (split + 1) / splits);
+    const int N = j1 - j0;  // chunks of this block
+    const bool two = rows > 128;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + C::OFF_MISC);
+    griddep_launch_dependents();
+
+    // ---- queries: bf16 rows as operands; rows past the last are zeros ----
+    if (rows > 0 && N > 0 && wg < 2 && (wg == 0 || two)) {
+        const int r = tid & 127, j = tile * T_ROWS + 128 * wg + r;
+        const bool real = 128 * wg + r < rows;
+        const int i = real ? j / p.G : 0;
+        const uint4 *q = reinterpret_cast<const uint4 *>(
+            a.q + (int64_t(s.q0 + i) * H + h * p.G + (real ? j - i * p.G : 0)) * D);
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k)
+            *reinterpret_cast<uint4 *>(smem + C::OFF_Q + wg * C::OPERAND + operand_place(r, k)) =
+                real ? order_bf16(q[k]) : make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+    }
+    __syncthreads();
+
+    auto wait = [&](int i, uint32_t parity) -> bool { return wait_all(bar(i), parity & 1u, s_abort, a.err); };
+
+    if (rows <= 0) {
+        // no such rows (a bound on them sized the grid)
+    } else if (wg < 2) {
+        // ---------------- softmax: a row per thread ----------------
+        const int r = tid & 127, jr = 128 * wg + r, j = tile * T_ROWS + jr;
+        const bool real = jr < rows;
+        const int i = real ? j / p.G : 0;
+        int row_lo = 0, row_hi = 0;  // keys that the row sees
+        if (real) {
+            row_hi = min(s.n, max(0, s.shift + i + 1));
+            if (a.window) {
+                const int64_t pos = prefix ? a.prefix_len + query_shift(a, s.q0 + i) : int64_t(s.shift) + i;
+                row_lo = int(min(int64_t(row_hi), max(int64_t(0), pos - a.window + 1)));
+            }
+        }
+        const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
+        const uint32_t ts = tmem + lanes + uint32_t(C::COL_S + 128 * wg), to = tmem + lanes + uint32_t(C::COL_O + D * wg);
+        float m = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+        bool ok = true;
+        const int steps = wg == 0 || two ? N : 0;
+        if (wg == 1 && !two) {  // no rows: only the scales' stages are given back
+            for (int n = 0; n < N; ++n) {
+                ok = wait(C::VFULL + (n & 1), uint32_t(n >> 1));
+                if (!ok) break;
+                if (lane == 0) mbar_arrive(bar(C::SCFREE + (n & 1)));
+            }
+        }
+        // all rows of the warp see all keys of [all_lo, all_hi) (rows past the last are not looked at)
+        const int all_lo = __reduce_max_sync(0xffffffffu, real ? row_lo : 0);
+        const int all_hi = __reduce_min_sync(0xffffffffu, real ? row_hi : INT_MAX);
+        for (int n = 0; n < steps; ++n) {
+            const int t0 = (j0 + n) * CH;
+            const float4 *ks = reinterpret_cast<const float4 *>(smem + C::OFF_SC + 1024 * (n & 1));
+            const float4 *vs = ks + 32;
+            ok = wait(C::KFULL + (n & 1), uint32_t(n >> 1)) && wait(C::SREADY + wg, uint32_t(n));
+            if (!ok) break;
+            tc_fence_after();
+            const bool lost = *reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 8 + 4 * (n & 1)) != 0;
+            const bool slow = CAP || lost || t0 < all_lo || t0 + CH > all_hi;
+            // ---- the row's largest score (times log2 e) ----
+            float top = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < CH; c += 32) {
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(ts + uint32_t(c), v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    const float4 k = ks[(c + e) >> 2];
+                    float x0, x1, x2, x3;
+                    split2(f32x2_mul(pair2u(v[e], v[e + 1]), pair2(k.x, k.y)), x0, x1);
+                    split2(f32x2_mul(pair2u(v[e + 2], v[e + 3]), pair2(k.z, k.w)), x2, x3);
+                    if (CAP) {
+                        const float cap = a.softcap * kLog2e;
+                        x0 = cap * tanh_exp(x0), x1 = cap * tanh_exp(x1);
+                        x2 = cap * tanh_exp(x2), x3 = cap * tanh_exp(x3);
+                    }
+                    if (slow) {
+                        const int t = t0 + c + e;
+                        x0 = t >= row_lo && t < row_hi && !(lost && k.x == -INFINITY) ? x0 : -INFINITY;
+                        x1 = t + 1 >= row_lo && t + 1 < row_hi && !(lost && k.y == -INFINITY) ? x1 : -INFINITY;
+                        x2 = t + 2 >= row_lo && t + 2 < row_hi && !(lost && k.z == -INFINITY) ? x2 : -INFINITY;
+                        x3 = t + 3 >= row_lo && t + 3 < row_hi && !(lost && k.w == -INFINITY) ? x3 : -INFINITY;
+                        v[e] = __float_as_uint(x0), v[e + 1] = __float_as_uint(x1);
+                        v[e + 2] = __float_as_uint(x2), v[e + 3] = __float_as_uint(x3);
+                    }
+                    top = fmax3(fmax3(top, x0, x1), x2, x3);
+                }
+                if (slow) {  // the scores as they are used
+                    tmem_st_32x32b_x16(ts + uint32_t(c), reinterpret_cast<const uint32_t(&)[16]>(v[0]));
+                    tmem_st_32x32b_x16(ts + uint32_t(c + 16), reinterpret_cast<const uint32_t(&)[16]>(v[16]));
+                }
+            }
+            if (slow) tmem_wait_st();
+            // ---- the reference ----
+            const bool raise = top > m + 8.0f || (m == -INFINITY && top > -INFINITY);
+            if (__any_sync(0xffffffffu, raise)) {
+                const float nm = raise ? top : m;
+                const float f = raise && m > -INFINITY ? ex2(m - nm) : 1.0f;
+                m = nm;
+                l0 *= f;
+                l1 *= f;
+                if (n > 0) {
+                    ok = wait(C::ODONE + wg, uint32_t(n - 1));
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t v[32];
+                        tmem_ld_32x32b_x32(to + uint32_t(c), v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+                        tmem_st_32x32b_x16(to + uint32_t(c), reinterpret_cast<const uint32_t(&)[16]>(v[0]));
+                        tmem_st_32x32b_x16(to + uint32_t(c + 16), reinterpret_cast<const uint32_t(&)[16]>(v[16]));
+                    }
+                    tmem_wait_st();
+                }
+            }
+            const float ref = m > -INFINITY ? m : 0.0f;
+            // ---- weights, over the scores ----
+            const uint64_t minus = pair2(-ref, -ref);
+            uint64_t sum = pair2(l0, l1);
+#pragma unroll
+            for (int c = 0; c < CH; c += 32) {
+                uint32_t v[32], w[16];
+                tmem_ld_32x32b_x32(ts + uint32_t(c), v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    const float4 k = ks[(c + e) >> 2], z = vs[(c + e) >> 2];
+                    const uint64_t a0 = pair2u(v[e], v[e + 1]), a1 = pair2u(v[e + 2], v[e + 3]);
+                    float x0, x1, x2, x3;
+                    split2(slow ? add2(a0, minus) : fma2(a0, pair2(k.x, k.y), minus), x0, x1);
+                    split2(slow ? add2(a1, minus) : fma2(a1, pair2(k.z, k.w), minus), x2, x3);
+                    const uint64_t p0 = pair2(ex2(x0), ex2(x1)), p1 = pair2(ex2(x2), ex2(x3));
+                    sum = add2(sum, p0);
+                    sum = add2(sum, p1);
+                    float y0, y1, y2, y3;
+                    split2(f32x2_mul(p0, pair2(z.x, z.y)), y0, y1);
+                    split2(f32x2_mul(p1, pair2(z.z, z.w)), y2, y3);
+                    w[e >> 1] = pack_bf16x2(y0, y1);
+                    w[(e >> 1) + 1] = pack_bf16x2(y2, y3);
+                }
+                tmem_st_32x32b_x16(ts + uint32_t(c >> 1), w);
+            }
+            split2(sum, l0, l1);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar(C::PREADY + wg));
+                mbar_arrive(bar(C::SCFREE + (n & 1)));
+            }
+        }
+        // ---- the rows ----
+        if (steps > 0 && ok) ok = wait(C::ODONE + wg, uint32_t(N - 1));
+        if ((wg == 0 || two) && ok) {
+            tc_fence_after();
+            const float l = l0 + l1;
+            const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
+            const float lse = l == 0.0f ? -INFINITY : m + lg2(l);  // in powers of two
+            const int64_t at = int64_t(s.q0 + i) * H + h * p.G + (real ? j - i * p.G : 0);
+            const bool final = splits == 1 && !p.partial;
+            float *po = p.tile_o + (int64_t(prefix ? p.own_splits : 0) + split) * a.T * H * D + at * D;
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+                uint32_t v[32];
+                if (N > 0) {
+                    tmem_ld_32x32b_x32(to + uint32_t(c), v);
+                    tmem_wait_ld();
+                }
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                    // columns 2 i, 2 i + 1 of eight are the elements i, i + 4
+                    float o[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        o[(k >> 1) + 4 * (k & 1)] = N > 0 && l != 0.0f ? __uint_as_float(v[e + k]) * inv : 0.0f;
+                    if (!real) {
+                    } else if (final) {
+                        *reinterpret_cast<uint4 *>(a.out + at * D + c + e) =
+                            make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
+                                       pack_bf16x2(o[6], o[7]));
+                    } else {
+                        *reinterpret_cast<float4 *>(po + c + e) = make_float4(o[0], o[1], o[2], o[3]);
+                        *reinterpret_cast<float4 *>(po + c + e + 4) = make_float4(o[4], o[5], o[6], o[7]);
+                    }
+                }
+                __syncwarp();
+            }
+            if (real) {
+                if (!final) p.tile_l[(int64_t(prefix ? p.own_splits : 0) + split) * a.T * H + at] = lse;
+                else if (a.lse) a.lse[at] = lse * 0.6931471805599453f;
+            }
+        }
+        tc_fence_before();
+    } else if (wg == 2) {
+        // ---------------- codes into operands: a key per thread ----------------
+        const int r = tid & 127;
+        const float factor = CAP ? a.scale / a.softcap : a.scale * kLog2e;
+        constexpr int W = D / 32;  // 16-byte pieces of a row of codes
+        struct Row {
+            uint4 k[W], v[W];
+            float ks, vs;
+        };
+        auto page_of = [&](int n) -> int {
+            const int t = (j0 + n) * CH + r;
+            return n < N && t < s.n && t >= lo ? s.pages[t >> psh] : -1;
+        };
+        auto load = [&](int n, int page) {
+            Row w;
+            const int t = (j0 + n) * CH + r;
+            w.ks = w.vs = 0.0f;
+#pragma unroll
+            for (int i = 0; i < W; ++i) w.k[i] = w.v[i] = make_uint4(0, 0, 0, 0);
+            if (n < N && t < s.n && t >= lo) {
+                if (uint32_t(page) < uint32_t(a.c.pages)) {
+                    const int64_t row = ((int64_t(page) * Hk + h) << psh) + (t & ((1 << psh) - 1));
+                    const uint4 *k = reinterpret_cast<const uint4 *>(a.c.k_codes + row * (D / 2));
+                    const uint4 *v = reinterpret_cast<const uint4 *>(a.c.v_codes + row * (D / 2));
+#pragma unroll
+                    for (int i = 0; i < W; ++i) w.k[i] = k[i], w.v[i] = v[i];
+                    w.ks = a.c.k_scale[row] * factor;
+                    w.vs = a.c.v_scale[row];
+                } else {
+                    w.ks = -INFINITY;  // no such page: the mark by which the softmax leaves the key out
+                    atomicOr(a.err, kSiteKvAttention);
+                }
+            }
+            return w;
+        };
+        auto lay = [&](int off, const uint4 (&c)[W]) {
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                const uint32_t x[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    *reinterpret_cast<uint4 *>(smem + off + operand_place(r, 4 * i + k)) = codes_bf16(x[k]);
+            }
+        };
+        bool ok = true;
+        Row now = load(0, page_of(0));
+        int page = page_of(1);
+        for (int n = 0; n < N; ++n) {
+            const int st = n & 1;
+            const uint32_t ph = uint32_t(n >> 1) ^ 1u;
+            const Row next = load(n + 1, page);
+            page = page_of(n + 2);
+            const bool lost = named_barrier_any(1, 128, now.ks == -INFINITY && now.vs == 0.0f);
+            ok = ok && wait(C::KFREE + st, ph) && wait(C::SCFREE + st, ph);
+            if (!ok) continue;  // the warpgroup's barrier wants every warp, also one that has given up
+            if (r == 0) *reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 8 + 4 * st) = lost;
+            lay(C::OFF_K + st * C::OPERAND, now.k);
+            float *sc = reinterpret_cast<float *>(smem + C::OFF_SC + 1024 * st);
+            sc[r] = now.ks;
+            sc[128 + r] = now.vs;
+            fence_proxy_async_smem();
+            mbar_arrive(bar(C::KFULL + st));
+            ok = wait(C::VFREE + st, ph);
+            if (!ok) continue;
+            lay(C::OFF_V + st * C::OPERAND, now.v);
+            fence_proxy_async_smem();
+            mbar_arrive(bar(C::VFULL + st));
+            now = next;
+        }
+    } else {
+        // ---------------- products ----------------
+        constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128), idesc_o = idesc_bf16_f32_bn(128, D);
+        const int nq = two ? 2 : 1;
+        auto scores = [&](int n, int q) {  // S(q) = Q(q) K(n)^T
+            if (elect_one()) {
+                const uint32_t qa = sbase + uint32_t(C::OFF_Q + q * C::OPERAND);
+                const uint32_t ka = sbase + uint32_t(C::OFF_K + (n & 1) * C::OPERAND);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = uint32_t((k >> 2) * C::HALF + 32 * (k & 3));
+                    mma_ss(tmem + uint32_t(C::COL_S + 128 * q), sdesc_kmajor_sw128(qa + off), sdesc_kmajor_sw128(ka + off),
+                           idesc_s, k != 0);
+                }
+                tc_commit(bar(C::SREADY + q));
+            }
+            __syncwarp();
+        };
+        bool ok = N > 0 && wait(C::KFULL, 0u);
+        if (ok) {
+            tc_fence_after();
+            for (int q = 0; q < nq; ++q) scores(0, q);
+            if (elect_one()) tc_commit(bar(C::KFREE));
+            __syncwarp();
+        }
+        for (int n = 0; n < N && ok; ++n) {
+            ok = wait(C::VFULL + (n & 1), uint32_t(n >> 1));
+            if (ok && n + 1 < N) ok = wait(C::KFULL + ((n + 1) & 1), uint32_t((n + 1) >> 1));
+            for (int q = 0; q < nq && ok; ++q) {
+                ok = wait(C::PREADY + q, uint32_t(n));
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {  // O(q) += P(q) V(n)
+                    const uint32_t va = sbase + uint32_t(C::OFF_V + (n & 1) * C::OPERAND);
+#pragma unroll
+                    for (int k = 0; k < CH / 16; ++k)
+                        mma_ts(tmem + uint32_t(C::COL_O + D * q), tmem + uint32_t(C::COL_S + 128 * q + 8 * k),
+                               sdesc_nmajor_sw128(va + uint32_t(2048 * k), C::HALF), idesc_o, n != 0 || k != 0);
+                    tc_commit(bar(C::ODONE + q));
+                }
+                __syncwarp();
+                if (n + 1 < N) scores(n + 1, q);
+            }
+            if (ok && elect_one()) {
+                tc_commit(bar(C::VFREE + (n & 1)));
+                if (n + 1 < N) tc_commit(bar(C::KFREE + ((n + 1) & 1)));
+            }
+            __syncwarp();
+        }
+        // every product has ended before the block's TMEM is given back
+        if (elect_one()) tc_commit(bar(C::DONE));
+        __syncwarp();
+        wait_bounded_err(bar(C::DONE), 0u, s_abort, kSiteKvWait, kWaitLimitNs, true, a.err);
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 12) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D, bool CAP>
+cudaError_t launch_inst(const Plan &p, bool prefix, int splits, int device, cudaStream_t stream) {
+    using C = TCfg<D>;
+    auto kern = kq_kv_tile_kernel<D, CAP>;
+    static std::once_flag once[64];
+    static cudaError_t attr_err[64];
+    if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
+    std::call_once(once[device], [&] {
+        attr_err[device] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    });
+    if (attr_err[device] != cudaSuccess) return attr_err[device];
+    const int64_t tiles = kv_tiles(prefix ? p.a.T : p.a.max_q, p.G), units_b = prefix ? 1 : p.a.B;
+    const int64_t grid = tiles * units_b * p.a.c.heads * splits;
+    if (grid >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    return launch_overlapped(kern, unsigned(grid), T_THREADS, C::SMEM, stream, p, int(prefix), splits, int(tiles),
+                             int(units_b));
+}
+
+}  // namespace
+
+cudaError_t launch_kv_tile(const kv::Plan &p, bool prefix, int splits, int device, cudaStream_t stream) {
+    if (p.a.c.D == 128)
+        return p.a.softcap > 0.0f ? launch_inst<128, true>(p, prefix, splits, device, stream)
+                                  : launch_inst<128, false>(p, prefix, splits, device, stream);
+    return p.a.softcap > 0.0f ? launch_inst<64, true>(p, prefix, splits, device, stream)
+                              : launch_inst<64, false>(p, prefix, splits, device, stream);
+}
+
+}  // namespace kq

@@ -149,6 +149,16 @@ def test_windows(kq, window):
     verify(kq, make([150, 900], [150, 200], 4, 2, 128, 16, window), window=window)
 
 
+@pytest.mark.parametrize("nqs", [[1, 1, 3], [70, 90, 33]])
+def test_pages_below_the_window_are_not_looked_at(kq, nqs):
+    """A sliding-window cache gives such pages back: their entries may hold anything."""
+    keys, window = [700, 300, 1500], 100
+    s = make(keys, nqs, 4, 2, 128, 16, 77)
+    for b, (n, m) in enumerate(zip(keys, nqs)):
+        s["table"][b, :max(0, n - m - window + 1) // 16] = -7
+    verify(kq, s, window=window)
+
+
 @pytest.mark.parametrize("softcap", [0.5, 5.0, 30.0])
 def test_capped_scores(kq, softcap):
     verify(kq, make([1, 17, 100, 700], [1] * 4, 4, 2, 128, 16, 5, q_std=6.0), softcap=softcap)
