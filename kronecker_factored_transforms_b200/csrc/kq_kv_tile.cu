@@ -57,7 +57,12 @@ struct TCfg {
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
-// TMEM store, 16 columns; and the pairs arithmetic.
+template <bool B>
+struct Is {
+    static constexpr bool value = B;
+};
+
+// Pairs of fp32 values.
 __device__ __forceinline__ uint64_t pair2(float a, float b) {
     uint64_t d;
     asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
@@ -218,39 +223,42 @@ __global__ void __launch_bounds__(T_THREADS, 1)
             const bool slow = CAP || lost || t0 < all_lo || t0 + CH > all_hi;
             // ---- the row's largest score (times log2 e) ----
             float top = -INFINITY;
+            if (!slow) {
+#pragma unroll 1
+                for (int c = 0; c < CH; c += 32) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(ts + uint32_t(c), v);
+                    tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < CH; c += 32) {
-                uint32_t v[32];
-                tmem_ld_32x32b_x32(ts + uint32_t(c), v);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    const float4 k = ks[(c + e) >> 2];
-                    float x0, x1, x2, x3;
-                    split2(f32x2_mul(pair2u(v[e], v[e + 1]), pair2(k.x, k.y)), x0, x1);
-                    split2(f32x2_mul(pair2u(v[e + 2], v[e + 3]), pair2(k.z, k.w)), x2, x3);
-                    if (CAP) {
-                        const float cap = a.softcap * kLog2e;
-                        x0 = cap * tanh_exp(x0), x1 = cap * tanh_exp(x1);
-                        x2 = cap * tanh_exp(x2), x3 = cap * tanh_exp(x3);
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 k = ks[(c + e) >> 2];
+                        float x0, x1, x2, x3;
+                        split2(f32x2_mul(pair2u(v[e], v[e + 1]), pair2(k.x, k.y)), x0, x1);
+                        split2(f32x2_mul(pair2u(v[e + 2], v[e + 3]), pair2(k.z, k.w)), x2, x3);
+                        top = fmax3(fmax3(top, x0, x1), x2, x3);
                     }
-                    if (slow) {
+                }
+            } else {
+                // the scores as they are used (capped, -inf where the row does not see) go back to their place
+#pragma unroll 1
+                for (int c = 0; c < CH; c += 16) {
+                    uint32_t v[16];
+                    tmem_ld_32x32b_x16(ts + uint32_t(c), v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float k = reinterpret_cast<const float *>(ks)[c + e];
                         const int t = t0 + c + e;
-                        x0 = t >= row_lo && t < row_hi && !(lost && k.x == -INFINITY) ? x0 : -INFINITY;
-                        x1 = t + 1 >= row_lo && t + 1 < row_hi && !(lost && k.y == -INFINITY) ? x1 : -INFINITY;
-                        x2 = t + 2 >= row_lo && t + 2 < row_hi && !(lost && k.z == -INFINITY) ? x2 : -INFINITY;
-                        x3 = t + 3 >= row_lo && t + 3 < row_hi && !(lost && k.w == -INFINITY) ? x3 : -INFINITY;
-                        v[e] = __float_as_uint(x0), v[e + 1] = __float_as_uint(x1);
-                        v[e + 2] = __float_as_uint(x2), v[e + 3] = __float_as_uint(x3);
+                        float x = __uint_as_float(v[e]) * k;
+                        if (CAP) x = a.softcap * kLog2e * tanh_exp(x);
+                        if (t < row_lo || t >= row_hi || (lost && k == -INFINITY)) x = -INFINITY;
+                        v[e] = __float_as_uint(x);
+                        top = fmaxf(top, x);
                     }
-                    top = fmax3(fmax3(top, x0, x1), x2, x3);
+                    tmem_st_32x32b_x16(ts + uint32_t(c), v);
                 }
-                if (slow) {  // the scores as they are used
-                    tmem_st_32x32b_x16(ts + uint32_t(c), reinterpret_cast<const uint32_t(&)[16]>(v[0]));
-                    tmem_st_32x32b_x16(ts + uint32_t(c + 16), reinterpret_cast<const uint32_t(&)[16]>(v[16]));
-                }
+                tmem_wait_st();
             }
-            if (slow) tmem_wait_st();
             // ---- the reference ----
             const bool raise = top > m + 8.0f || (m == -INFINITY && top > -INFINITY);
             if (__any_sync(0xffffffffu, raise)) {
@@ -263,15 +271,14 @@ __global__ void __launch_bounds__(T_THREADS, 1)
                     ok = wait(C::ODONE + wg, uint32_t(n - 1));
                     if (!ok) break;
                     tc_fence_after();
-#pragma unroll
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t v[32];
-                        tmem_ld_32x32b_x32(to + uint32_t(c), v);
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t v[16];
+                        tmem_ld_32x32b_x16(to + uint32_t(c), v);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
-                        tmem_st_32x32b_x16(to + uint32_t(c), reinterpret_cast<const uint32_t(&)[16]>(v[0]));
-                        tmem_st_32x32b_x16(to + uint32_t(c + 16), reinterpret_cast<const uint32_t(&)[16]>(v[16]));
+                        for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+                        tmem_st_32x32b_x16(to + uint32_t(c), v);
                     }
                     tmem_wait_st();
                 }
@@ -280,29 +287,41 @@ __global__ void __launch_bounds__(T_THREADS, 1)
             // ---- weights, over the scores ----
             const uint64_t minus = pair2(-ref, -ref);
             uint64_t sum = pair2(l0, l1);
+            auto weights = [&](auto raw) {
+#pragma unroll 1
+                for (int c = 0; c < CH; c += 32) {
+                    uint32_t v[32], w[16];
+                    tmem_ld_32x32b_x32(ts + uint32_t(c), v);
+                    tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < CH; c += 32) {
-                uint32_t v[32], w[16];
-                tmem_ld_32x32b_x32(ts + uint32_t(c), v);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    const float4 k = ks[(c + e) >> 2], z = vs[(c + e) >> 2];
-                    const uint64_t a0 = pair2u(v[e], v[e + 1]), a1 = pair2u(v[e + 2], v[e + 3]);
-                    float x0, x1, x2, x3;
-                    split2(slow ? add2(a0, minus) : fma2(a0, pair2(k.x, k.y), minus), x0, x1);
-                    split2(slow ? add2(a1, minus) : fma2(a1, pair2(k.z, k.w), minus), x2, x3);
-                    const uint64_t p0 = pair2(ex2(x0), ex2(x1)), p1 = pair2(ex2(x2), ex2(x3));
-                    sum = add2(sum, p0);
-                    sum = add2(sum, p1);
-                    float y0, y1, y2, y3;
-                    split2(f32x2_mul(p0, pair2(z.x, z.y)), y0, y1);
-                    split2(f32x2_mul(p1, pair2(z.z, z.w)), y2, y3);
-                    w[e >> 1] = pack_bf16x2(y0, y1);
-                    w[(e >> 1) + 1] = pack_bf16x2(y2, y3);
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 z = vs[(c + e) >> 2];
+                        uint64_t a0 = pair2u(v[e], v[e + 1]), a1 = pair2u(v[e + 2], v[e + 3]);
+                        if constexpr (decltype(raw)::value) {
+                            const float4 k = ks[(c + e) >> 2];
+                            a0 = fma2(a0, pair2(k.x, k.y), minus);
+                            a1 = fma2(a1, pair2(k.z, k.w), minus);
+                        } else {
+                            a0 = add2(a0, minus);
+                            a1 = add2(a1, minus);
+                        }
+                        float x0, x1, x2, x3;
+                        split2(a0, x0, x1);
+                        split2(a1, x2, x3);
+                        const uint64_t p0 = pair2(ex2(x0), ex2(x1)), p1 = pair2(ex2(x2), ex2(x3));
+                        sum = add2(sum, p0);
+                        sum = add2(sum, p1);
+                        float y0, y1, y2, y3;
+                        split2(f32x2_mul(p0, pair2(z.x, z.y)), y0, y1);
+                        split2(f32x2_mul(p1, pair2(z.z, z.w)), y2, y3);
+                        w[e >> 1] = pack_bf16x2(y0, y1);
+                        w[(e >> 1) + 1] = pack_bf16x2(y2, y3);
+                    }
+                    tmem_st_32x32b_x16(ts + uint32_t(c >> 1), w);
                 }
-                tmem_st_32x32b_x16(ts + uint32_t(c >> 1), w);
-            }
+            };
+            if (slow) weights(Is<false>{});
+            else weights(Is<true>{});
             split2(sum, l0, l1);
             tmem_wait_st();
             tc_fence_before();
