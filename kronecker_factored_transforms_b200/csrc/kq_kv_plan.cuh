@@ -29,9 +29,8 @@ __device__ __forceinline__ float lg2(float x) {
 __device__ __forceinline__ float tanh_exp(float z) {
     return 1.0f - __fdividef(2.0f, ex2(z * (2.0f * kLog2e)) + 1.0f);
 }
-// Wait for a phase, suspended at first; gives up as wait_bounded_err does.
+// Wait for a phase; gives up as wait_bounded_err does.
 __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile int *abort, unsigned int *err) {
-    if (__all_sync(0xffffffffu, tc::mbar_try_wait_for(bar, parity, 20000u))) return true;
     return __all_sync(0xffffffffu,
                       tc::wait_bounded_err(bar, parity, abort, kSiteKvWait, tc::kWaitLimitNs, false, err));
 }

@@ -13,12 +13,13 @@
 //     the order 0 4 1 5 2 6 3 7; queries are laid in the same order, and the output is
 //     put right where it leaves.
 //   - scores S = Q K^T into TMEM, one warpgroup per row tile for the softmax, a thread
-//     per row: x = S ks with the key's scale (times the softmax scale), its maximum, then
-//     p = 2^(x - m); p times the value's scale goes back over S as bf16, O += P V.  The
-//     scales never meet the codes, and the sum of p is fp32 with unrounded terms.  A
-//     weight's rounding to bf16 (2^-9 at most) is of the size of the output's own.
-//   - m follows the row's maximum only when it passes m + 8 (weights stay under 2^8):
-//     O has to be rescaled then, which is rare.
+//     per row: x = S ks with the key's scale (times the softmax scale), p = 2^(x - m);
+//     p times the value's scale goes back over S as bf16, O += P V.  The scales never
+//     meet the codes, and the sum of p is fp32 with unrounded terms.  A weight's rounding
+//     to bf16 (2^-9 at most) is of the size of the output's own.
+//   - one pass over the scores: m is the maximum of the row's first chunk, and a weight
+//     may pass 1, as fp32 and bf16 have the range (up to 2^60 here).  When a chunk's
+//     largest passed 2^8, m is raised before the next one, which rescales O: rare.
 //   - the two row tiles are half a step apart: while one warpgroup is at its softmax
 //     the tensor core works for the other.
 // Keys that a row does not see, past its place or out of its window, are looked at only
@@ -50,7 +51,7 @@ struct TCfg {
     static constexpr int OFF_V = OFF_K + 2 * OPERAND;
     static constexpr int OFF_SC = OFF_V + 2 * OPERAND;  // per stage 128 key scales, 128 value scales
     static constexpr int OFF_BAR = OFF_SC + 2 * 1024;
-    enum { KFULL = 0, KFREE = 2, VFULL = 4, VFREE = 6, SREADY = 8, PREADY = 10, ODONE = 12, SCFREE = 14, DONE = 16, NBAR = 17 };
+    enum { KFULL = 0, KFREE = 2, VFULL = 4, VFREE = 6, SREADY = 8, PREADY = 10, ODONE = 12, SCFREE = 14, DONE = 16, QREADY = 17, NBAR = 18 };
     static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
     static constexpr int SMEM = OFF_MISC + 16 + 1024;  // TMEM base, abort flag, per stage whether keys lack a page
     static constexpr int COL_S = 0, COL_O = 256;  // TMEM columns: S of tile q at 128 q, O at 256 + D q
@@ -133,6 +134,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
             mbar_init(bar(C::SCFREE + i), 8);
         }
         mbar_init(bar(C::DONE), 1);
+        mbar_init(bar(C::QREADY), 256);
         *s_abort = 0;
         fence_mbar_init();
     }
@@ -166,7 +168,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
     griddep_launch_dependents();
 
     // ---- queries: bf16 rows as operands; rows past the last are zeros ----
-    if (rows > 0 && N > 0 && wg < 2 && (wg == 0 || two)) {
+    if (wg < 2) {
         const int r = tid & 127, j = tile * T_ROWS + 128 * wg + r;
         const bool real = 128 * wg + r < rows;
         const int i = real ? j / p.G : 0;
@@ -177,8 +179,8 @@ __global__ void __launch_bounds__(T_THREADS, 1)
             *reinterpret_cast<uint4 *>(smem + C::OFF_Q + wg * C::OPERAND + operand_place(r, k)) =
                 real ? order_bf16(q[k]) : make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
+        mbar_arrive(bar(C::QREADY));
     }
-    __syncthreads();
 
     auto wait = [&](int i, uint32_t parity) -> bool { return wait_all(bar(i), parity & 1u, s_abort, a.err); };
 
@@ -199,7 +201,8 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         }
         const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
         const uint32_t ts = tmem + lanes + uint32_t(C::COL_S + 128 * wg), to = tmem + lanes + uint32_t(C::COL_O + D * wg);
-        float m = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+        float m = 0.0f, l0 = 0.0f, l1 = 0.0f;  // the reference, and the sum of the weights in two parts
+        bool seen = !real;                     // the reference is set: some chunk had a key that the row sees
         bool ok = true;
         const int steps = wg == 0 || two ? N : 0;
         if (wg == 1 && !two) {  // no rows: only the scales' stages are given back
@@ -212,6 +215,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         // all rows of the warp see all keys of [all_lo, all_hi) (rows past the last are not looked at)
         const int all_lo = __reduce_max_sync(0xffffffffu, real ? row_lo : 0);
         const int all_hi = __reduce_min_sync(0xffffffffu, real ? row_hi : INT_MAX);
+        float rise = 0.0f;  // how far the last chunk's largest score was over the reference
         for (int n = 0; n < steps; ++n) {
             const int t0 = (j0 + n) * CH;
             const float4 *ks = reinterpret_cast<const float4 *>(smem + C::OFF_SC + 1024 * (n & 1));
@@ -221,25 +225,32 @@ __global__ void __launch_bounds__(T_THREADS, 1)
             tc_fence_after();
             const bool lost = *reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 8 + 4 * (n & 1)) != 0;
             const bool slow = CAP || lost || t0 < all_lo || t0 + CH > all_hi;
-            // ---- the row's largest score (times log2 e) ----
-            float top = -INFINITY;
-            if (!slow) {
+            // The reference rises by `up`: O, whose last product has ended with S's, and the sums follow.
+            auto raise = [&](float up) {
+                const float f = ex2(-up);
+                m += up;
+                l0 *= f;
+                l1 *= f;
+                if (n > 0) {
 #pragma unroll 1
-                for (int c = 0; c < CH; c += 32) {
-                    uint32_t v[32];
-                    tmem_ld_32x32b_x32(ts + uint32_t(c), v);
-                    tmem_wait_ld();
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t v[16];
+                        tmem_ld_32x32b_x16(to + uint32_t(c), v);
+                        tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 k = ks[(c + e) >> 2];
-                        float x0, x1, x2, x3;
-                        split2(f32x2_mul(pair2u(v[e], v[e + 1]), pair2(k.x, k.y)), x0, x1);
-                        split2(f32x2_mul(pair2u(v[e + 2], v[e + 3]), pair2(k.z, k.w)), x2, x3);
-                        top = fmax3(fmax3(top, x0, x1), x2, x3);
+                        for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+                        tmem_st_32x32b_x16(to + uint32_t(c), v);
                     }
+                    tmem_wait_st();
                 }
-            } else {
-                // the scores as they are used (capped, -inf where the row does not see) go back to their place
+            };
+            if (__any_sync(0xffffffffu, rise > 8.0f)) raise(rise > 8.0f ? rise : 0.0f);
+            rise = 0.0f;
+            const bool first_keys = __any_sync(0xffffffffu, !seen);
+            if (slow || first_keys) {
+                // ---- the row's largest score; scores as they are used (capped, -inf where the row does not
+                // see) go back to their place ----
+                float top = -INFINITY;
 #pragma unroll 1
                 for (int c = 0; c < CH; c += 16) {
                     uint32_t v[16];
@@ -258,34 +269,13 @@ __global__ void __launch_bounds__(T_THREADS, 1)
                     tmem_st_32x32b_x16(ts + uint32_t(c), v);
                 }
                 tmem_wait_st();
-            }
-            // ---- the reference ----
-            const bool raise = top > m + 8.0f || (m == -INFINITY && top > -INFINITY);
-            if (__any_sync(0xffffffffu, raise)) {
-                const float nm = raise ? top : m;
-                const float f = raise && m > -INFINITY ? ex2(m - nm) : 1.0f;
-                m = nm;
-                l0 *= f;
-                l1 *= f;
-                if (n > 0) {
-                    ok = wait(C::ODONE + wg, uint32_t(n - 1));
-                    if (!ok) break;
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 16) {
-                        uint32_t v[16];
-                        tmem_ld_32x32b_x16(to + uint32_t(c), v);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
-                        tmem_st_32x32b_x16(to + uint32_t(c), v);
-                    }
-                    tmem_wait_st();
+                if (!seen && top > -INFINITY) {  // nothing has been summed yet: the reference may be anywhere
+                    seen = true;
+                    m = top;
                 }
+                if (__any_sync(0xffffffffu, top > m + 8.0f)) raise(top > m + 8.0f ? top - m : 0.0f);
             }
-            const float ref = m > -INFINITY ? m : 0.0f;
             // ---- weights, over the scores ----
-            const uint64_t minus = pair2(-ref, -ref);
             uint64_t sum = pair2(l0, l1);
             auto weights = [&](auto raw) {
 #pragma unroll 1
@@ -293,21 +283,56 @@ __global__ void __launch_bounds__(T_THREADS, 1)
                     uint32_t v[32], w[16];
                     tmem_ld_32x32b_x32(ts + uint32_t(c), v);
                     tmem_wait_ld();
+                    uint64_t minus = pair2(-m, -m);
+                    uint64_t x[16];
+                    float most = -INFINITY;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        x[e >> 1] = pair2u(v[e], v[e + 1]);
+                        x[(e >> 1) + 1] = pair2u(v[e + 2], v[e + 3]);
+                        if constexpr (decltype(raw)::value) {
+                            const float4 k = ks[(c + e) >> 2];
+                            x[e >> 1] = fma2(x[e >> 1], pair2(k.x, k.y), minus);
+                            x[(e >> 1) + 1] = fma2(x[(e >> 1) + 1], pair2(k.z, k.w), minus);
+                            float x0, x1, x2, x3;
+                            split2(x[e >> 1], x0, x1);
+                            split2(x[(e >> 1) + 1], x2, x3);
+                            most = fmax3(fmax3(most, x0, x1), x2, x3);
+                        } else {
+                            x[e >> 1] = add2(x[e >> 1], minus);
+                            x[(e >> 1) + 1] = add2(x[(e >> 1) + 1], minus);
+                        }
+                    }
+                    if constexpr (decltype(raw)::value) {
+                        rise = fmaxf(rise, most);
+                        if (__any_sync(0xffffffffu, most > 60.0f)) {
+                            // out of a weight's range: raise the reference here, and what the chunk has so far
+                            const float up = most > 60.0f ? most : 0.0f, f = ex2(-up);
+                            split2(sum, l0, l1);
+                            raise(up);
+                            sum = pair2(l0, l1);
+                            rise = fmaxf(rise - up, 0.0f);
+#pragma unroll 1
+                            for (int d = 0; d < (c >> 1); d += 16) {
+                                tmem_ld_32x32b_x16(ts + uint32_t(d), w);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    w[e] = pack_bf16x2(__uint_as_float(w[e] << 16) * f,
+                                                       __uint_as_float(w[e] & 0xffff0000u) * f);
+                                tmem_st_32x32b_x16(ts + uint32_t(d), w);
+                            }
+                            tmem_wait_st();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) x[e] = add2(x[e], pair2(-up, -up));
+                        }
+                    }
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
                         const float4 z = vs[(c + e) >> 2];
-                        uint64_t a0 = pair2u(v[e], v[e + 1]), a1 = pair2u(v[e + 2], v[e + 3]);
-                        if constexpr (decltype(raw)::value) {
-                            const float4 k = ks[(c + e) >> 2];
-                            a0 = fma2(a0, pair2(k.x, k.y), minus);
-                            a1 = fma2(a1, pair2(k.z, k.w), minus);
-                        } else {
-                            a0 = add2(a0, minus);
-                            a1 = add2(a1, minus);
-                        }
                         float x0, x1, x2, x3;
-                        split2(a0, x0, x1);
-                        split2(a1, x2, x3);
+                        split2(x[e >> 1], x0, x1);
+                        split2(x[(e >> 1) + 1], x2, x3);
                         const uint64_t p0 = pair2(ex2(x0), ex2(x1)), p1 = pair2(ex2(x2), ex2(x3));
                         sum = add2(sum, p0);
                         sum = add2(sum, p1);
@@ -320,7 +345,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
                     tmem_st_32x32b_x16(ts + uint32_t(c >> 1), w);
                 }
             };
-            if (slow) weights(Is<false>{});
+            if (slow || first_keys) weights(Is<false>{});
             else weights(Is<true>{});
             split2(sum, l0, l1);
             tmem_wait_st();
@@ -460,7 +485,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
             }
             __syncwarp();
         };
-        bool ok = N > 0 && wait(C::KFULL, 0u);
+        bool ok = N > 0 && wait(C::QREADY, 0u) && wait(C::KFULL, 0u);
         if (ok) {
             tc_fence_after();
             for (int q = 0; q < nq; ++q) scores(0, q);
