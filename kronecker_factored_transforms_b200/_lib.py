@@ -220,29 +220,55 @@ def kv_transform(Pq, Pk, Pv, alpha_k: float, alpha_v: float, rope=None, interlea
     return _Handle(st, [Pq, Pk, Pv, rope])
 
 
-def _on_device(fn: str, cache, call, *tensors) -> None:
-    """Calls with the cache's device current (the C entries work on the current one); the tensors lie there too."""
+# torch's current device and the raw current stream of a device: looked up on the first call.
+_current_device = None
+_raw_stream = None
+
+
+def _device_calls():
+    global _current_device, _raw_stream
     import torch
+    _current_device = torch.cuda.current_device
+    # the public way makes a Stream object, which takes as long as the launch
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _enter(fn: str, cache, stream, tensors):
+    """The stream (a C entry works on the current device: another one is an error here) and the tensors' addresses.
+
+    These calls take microseconds on the GPU for small batches, so this is kept short."""
+    if _raw_stream is None:
+        _device_calls()
+    device = cache.device
+    if _current_device() != device:
+        raise ValueError("%s: the cache lies on cuda:%d, the current device is cuda:%d" % (fn, device, _current_device()))
+    ptrs = []
     for t in tensors:
-        if t is not None and not isinstance(t, int) and t.get_device() != cache.device:
-            raise ValueError("%s: a tensor on %s, the cache on cuda:%d" % (fn, t.device, cache.device))
-    if torch.cuda.current_device() == cache.device:
-        _check(fn, call())
-    else:
-        with torch.cuda.device(cache.device):
-            _check(fn, call())
+        if t is None or t.__class__ is int:
+            ptrs.append(t)
+        elif t.get_device() != device:
+            raise ValueError("%s: a tensor on %s, the cache on cuda:%d" % (fn, t.device, device))
+        else:
+            ptrs.append(t.data_ptr())
+    if stream is None:
+        return _raw_stream(device) or None, ptrs
+    return _stream(stream), ptrs
 
 
 def kq_kv_append(cache, tf, q, q_stride: int, k, k_stride: int, v, v_stride: int, positions, slots, q_out, T: int,
                  q_heads: int, stream=None) -> None:
-    _on_device("kq_kv_append", cache, lambda: lib.kq_kv_append(
-        cache.ptr, tf.ptr, _ptr(q), int(q_stride), _ptr(k), int(k_stride), _ptr(v), int(v_stride), _ptr(positions),
-        _ptr(slots), _ptr(q_out), int(T), int(q_heads), _stream(stream)), q, k, v, positions, slots, q_out)
+    st, (q, k, v, positions, slots, q_out) = _enter("kq_kv_append", cache, stream, (q, k, v, positions, slots, q_out))
+    r = lib.kq_kv_append(cache.ptr, tf.ptr, q, q_stride, k, k_stride, v, v_stride, positions, slots, q_out, T, q_heads, st)
+    if r:
+        _check("kq_kv_append", r)
 
 
 def kq_kv_gather(cache, slots, k_out, v_out, T: int, stream=None) -> None:
-    _on_device("kq_kv_gather", cache, lambda: lib.kq_kv_gather(
-        cache.ptr, _ptr(slots), _ptr(k_out), _ptr(v_out), int(T), _stream(stream)), slots, k_out, v_out)
+    st, (slots, k_out, v_out) = _enter("kq_kv_gather", cache, stream, (slots, k_out, v_out))
+    r = lib.kq_kv_gather(cache.ptr, slots, k_out, v_out, T, st)
+    if r:
+        _check("kq_kv_gather", r)
 
 
 def kq_kv_attention_workspace_bytes(T: int, B: int, q_heads: int, kv_heads: int, head_dim: int, max_q: int) -> int:
@@ -253,20 +279,23 @@ def kq_kv_attention_workspace_bytes(T: int, B: int, q_heads: int, kv_heads: int,
 def kq_kv_attention(cache, q, q_start, page_table, max_pages: int, kv_len, scale: float, softcap: float, window: int,
                     out, lse, workspace, workspace_bytes: int, T: int, B: int, q_heads: int, max_q: int,
                     stream=None) -> None:
-    _on_device("kq_kv_attention", cache, lambda: lib.kq_kv_attention(
-        cache.ptr, _ptr(q), _ptr(q_start), _ptr(page_table), int(max_pages), _ptr(kv_len), float(scale),
-        float(softcap), int(window), _ptr(out), _ptr(lse), _ptr(workspace), int(workspace_bytes), int(T), int(B),
-        int(q_heads), int(max_q), _stream(stream)), q, q_start, page_table, kv_len, out, lse, workspace)
+    st, (q, q_start, page_table, kv_len, out, lse, workspace) = _enter(
+        "kq_kv_attention", cache, stream, (q, q_start, page_table, kv_len, out, lse, workspace))
+    r = lib.kq_kv_attention(cache.ptr, q, q_start, page_table, max_pages, kv_len, scale, softcap, window, out, lse,
+                            workspace, workspace_bytes, T, B, q_heads, max_q, st)
+    if r:
+        _check("kq_kv_attention", r)
 
 
 def kq_kv_attention_shared(cache, q, q_start, prefix_pages, prefix_len: int, page_table, max_pages: int, kv_len,
                            scale: float, softcap: float, window: int, out, lse, workspace, workspace_bytes: int,
                            T: int, B: int, q_heads: int, max_q: int, stream=None) -> None:
-    _on_device("kq_kv_attention_shared", cache, lambda: lib.kq_kv_attention_shared(
-        cache.ptr, _ptr(q), _ptr(q_start), _ptr(prefix_pages), int(prefix_len), _ptr(page_table), int(max_pages),
-        _ptr(kv_len), float(scale), float(softcap), int(window), _ptr(out), _ptr(lse), _ptr(workspace),
-        int(workspace_bytes), int(T), int(B), int(q_heads), int(max_q), _stream(stream)),
-        q, q_start, prefix_pages, page_table, kv_len, out, lse, workspace)
+    st, (q, q_start, prefix_pages, page_table, kv_len, out, lse, workspace) = _enter(
+        "kq_kv_attention_shared", cache, stream, (q, q_start, prefix_pages, page_table, kv_len, out, lse, workspace))
+    r = lib.kq_kv_attention_shared(cache.ptr, q, q_start, prefix_pages, prefix_len, page_table, max_pages, kv_len, scale,
+                                   softcap, window, out, lse, workspace, workspace_bytes, T, B, q_heads, max_q, st)
+    if r:
+        _check("kq_kv_attention_shared", r)
 
 
 def kq_transform(x, P1, P2, cinv, y_out, T: int, n1: int, n2: int, stream=None) -> None:
