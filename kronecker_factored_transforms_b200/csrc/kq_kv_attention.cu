@@ -798,10 +798,14 @@ constexpr int kSms = 148;          // of a B200; the tile kernel has one block o
 
 int row_tile(int64_t rows) { return rows <= 8 ? 8 : 16; }
 
-// Whether rows of one key head are the tile kernel's.  The row kernel takes up to two tiles of 8, for which
-// it reads every code once; beyond that it would read them again for every 16 rows, where the tile kernel's
-// tensor cores work on up to 256.
-bool many_rows(int64_t rows) { return rows > 16; }
+// Whether the rows of a key head and sequence, or of a key head and the prefix, are the tile kernel's.  The
+// row kernel reads the codes again (from L2) for every 8 or 16 rows; the tile kernel works on up to 256 at
+// once but has one block an SM and a longer way to its first product.  Measured in us, row against tile
+// kernel, head_dim 128, 24 sequences of 100 to 4100 keys on 4 key heads: 20 rows 28 against 41, 40 rows 35
+// against 42, 64 rows 50 against 46.  A prefix on 8 key heads: 32 rows 17 against 19 (1000 keys) and 28
+// against 29 (8000), 64 rows 20 against 21 (1000) but 70 against 37 (16000).
+bool many_rows(int64_t rows) { return rows > 48; }
+bool many_prefix_rows(int64_t rows) { return rows > 32; }
 
 // Blocks to cut a unit's keys over, where there are too few units for all SMs: the number that leaves the
 // fewest SMs idle in the last round of blocks, with a hundredth off for each further part to join.
@@ -824,7 +828,7 @@ uint64_t lay_out(Plan &p, unsigned char *base, int64_t T, int64_t B, int H, int 
                  int64_t pre_most) {
     const int G = H / Hk;
     p.G = G;
-    const bool own_tile = many_rows(int64_t(max_q) * G), pre_tile = many_rows(T * G);
+    const bool own_tile = many_rows(int64_t(max_q) * G), pre_tile = own_tile || many_prefix_rows(T * G);
     const int own = own_tile ? tile_splits(kv_tiles(max_q, G) * B * Hk, INT32_MAX) : 0;
     const int pre = pre_tile ? tile_splits(kv_tiles(T, G) * Hk, INT32_MAX) : 0;
     p.own_splits = own_tile ? tile_splits(kv_tiles(max_q, G) * B * Hk, own_most) : 0;
@@ -832,7 +836,7 @@ uint64_t lay_out(Plan &p, unsigned char *base, int64_t T, int64_t B, int H, int 
     p.rows_own = !own_tile;
     p.rows_prefix = pre_most && !pre_tile;
     p.partial = pre_most > 0;
-    const int R = row_tile(pre_tile ? int64_t(max_q) * G : T * G);
+    const int R = row_tile(int64_t(max_q) * G);
     const uint64_t rows = uint64_t(T) * H;
     uint64_t at = 0;
     auto take = [&](uint64_t bytes) {
@@ -899,8 +903,7 @@ cudaError_t launch_kv_attention(const KvAttnArgs &a, int num_sms, int device, cu
     const int64_t own_most = ((a.max_pages << a.c.page_shift) + CH - 1) / CH;
     const int64_t pre_most = a.prefix_pages ? (a.prefix_len + CH - 1) / CH : 0;
     lay_out(p, a.workspace, a.T, a.B, a.q_heads, a.c.heads, a.c.D, a.max_q, own_most, pre_most);
-    const int64_t rows = p.rows_prefix ? a.T * p.G : int64_t(a.max_q) * p.G;
-    const bool one = row_tile(rows) == 8;
+    const bool one = row_tile(int64_t(a.max_q) * p.G) == 8;
     if (a.c.D == 128)
         return one ? launch_all<128, 1>(p, num_sms, device, stream) : launch_all<128, 2>(p, num_sms, device, stream);
     return one ? launch_all<64, 1>(p, num_sms, device, stream) : launch_all<64, 2>(p, num_sms, device, stream);
