@@ -32,9 +32,9 @@
 // The sum of exp(x) is fp32 with unrounded terms.
 //
 // Work is split evenly: the (sequence, key head, row tile) units are laid in a row,
-// 64 keys a chunk, and every block takes the same number of chunks wherever that
-// cuts; its four warps take 16 keys of each chunk, each with its own ring of
-// cp.async stages and its own softmax state, joined at a unit's end.  A unit cut
+// 128 keys a chunk, and every block takes the same number of chunks wherever that
+// cuts; a warp of its own loads them into a ring of stages, four warps take 32 keys
+// of each chunk, with their own softmax states, joined at a unit's end.  A unit cut
 // by block borders leaves partial rows in the workspace, at most two per block,
 // which kq_kv_combine_kernel joins in a fixed order.
 #include <cuda_fp16.h>
@@ -53,6 +53,10 @@ constexpr int WARPS = 4;        // multiplying warps per block
 constexpr int MT = 2;           // tiles of 16 keys that each takes of a chunk
 static_assert(CH == 16 * MT * WARPS, "keys per chunk");
 constexpr int R_THREADS = 32 * (WARPS + 1);
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -174,7 +178,7 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
     int64_t *scan = reinterpret_cast<int64_t *>(smem + C::OFF_SCAN);  // warp sums; then the block's first chunk
     if (tid == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
-            mbar_init(bar(C::FULL + s), 1);
+            mbar_init(bar(C::FULL + s), 33);  // the loading warp's lanes once their copies have landed, and one more
             mbar_init(bar(C::EMPTY + s), WARPS);
         }
         mbar_init(bar(C::JOIN), WARPS);
@@ -224,7 +228,9 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
     __syncthreads();
 
     if (warp == WARPS) {
-        // ---------------- the loading warp: one chunk per stage, by bulk copies ----------------
+        // ---------------- the loading warp: one chunk per stage, 16 bytes a lane and copy ----------------
+        // (Bulk copies of a page's part would be fewer, but a lane's own takes its own pass through the
+        // instruction: 100 clocks for each, 3000 for a chunk of 16-key pages.)
         Walk<R> w;
         w.b = scan[0];
         w.s = load_seq<R>(p, w.b, false);
@@ -234,80 +240,84 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
         w.h = int(u0 / w.s.tiles);
         bool entire = w.c == w.s.c0;  // whether this block has had the unit from its first chunk on
         bool begins = true, first = true;
-        // lane i copies piece i of a chunk: the keys of a page that lie in it
-        const int gsh = (1 << psh) < CH ? psh : 31 - __clz(CH), pieces = CH >> gsh;
-        static_assert((CH & (CH - 1)) == 0 && 4 * (CH / 16) <= 32, "a lane per piece of a chunk");
-        const int piece = lane & (pieces - 1), what = lane / pieces;  // what: codes and scales of keys, of values
-        auto page_of = [&]() -> int {
-            const int t = w.c * CH + (piece << gsh);
-            return t < w.s.n && t + (1 << gsh) > w.s.lo ? w.s.pages[t >> psh] : -1;
+        constexpr int SUBS = CH / 16;
+        // lane i looks up the page of the chunk's keys 16 i .. 16 i + 15; -1: not wanted
+        auto page_of = [&](const Walk<R> &v) -> int {
+            const int t = v.c * CH + 16 * lane;
+            return lane < SUBS && t < v.s.n && t + 16 > v.s.lo ? v.s.pages[t >> psh] : -1;
         };
-        int page = page_of();
+        int page = page_of(w);
+        const uint8_t *const kc = a.c.k_codes + 16 * lane, *const vc = a.c.v_codes + 16 * lane;
         Ring rg;
-        int issued = 0;
         for (int i = 0; i < steps; ++i, rg.next(C::STAGES)) {
+            // the next chunk's pages are looked up while this one is copied
+            Walk<R> ahead = w;
+            int next_page = -1;
+            if (i + 1 < steps) {
+                ahead.next(p, seqs);
+                next_page = page_of(ahead);
+            }
             if (!wait_all(bar(C::EMPTY + rg.idx), rg.phase ^ 1u, s_abort, a.err)) break;
-            const int t = w.c * CH + (piece << gsh);
-            const bool wanted = t < w.s.n && t + (1 << gsh) > w.s.lo;
+            const int t = w.c * CH + 16 * lane;
+            const bool wanted = lane < SUBS && t < w.s.n && t + 16 > w.s.lo;
             const bool there = wanted && uint32_t(page) < uint32_t(a.c.pages);
-            if (wanted && !there && what == 0) atomicOr(a.err, kSiteKvAttention);
-            const uint32_t ok = __ballot_sync(0xffffffffu, there && lane < pieces);
+            if (wanted && !there) atomicOr(a.err, kSiteKvAttention);
+            const uint32_t ok = __ballot_sync(0xffffffffu, there);
+            const int64_t row = there ? ((int64_t(page) * Hk + w.h) << psh) + (t & ((1 << psh) - 1)) : 0;
+            const uint32_t dst = sbase + uint32_t(rg.idx * C::STAGE) + uint32_t(16 * lane);
+#pragma unroll
+            for (int s = 0; s < SUBS; ++s) {
+                const int64_t at = __shfl_sync(0xffffffffu, row, s) * (D / 2);
+                if (ok >> s & 1u) {
+#pragma unroll
+                    for (int k = 0; k < D / 64; ++k) {  // 16 rows of D / 2 bytes are D / 64 times 512
+                        cp_async16(dst + uint32_t(s * 8 * D + 512 * k), kc + at + 512 * k);
+                        cp_async16(dst + uint32_t(C::CODES + s * 8 * D + 512 * k), vc + at + 512 * k);
+                    }
+                }
+            }
+            const int64_t mine = __shfl_sync(0xffffffffu, row, lane >> 2) + 4 * (lane & 3);  // 4 keys' scales
+            if (ok >> (lane >> 2) & 1u) {
+                cp_async16(dst + uint32_t(2 * C::CODES), a.c.k_scale + mine);
+                cp_async16(dst + uint32_t(2 * C::CODES + 4 * CH), a.c.v_scale + mine);
+            }
+            if (begins) {
+                const int rows = min(R, w.s.m * p.G - w.tile * R), j = w.tile * R + lane, i0 = j / p.G;
+                const int64_t from = (int64_t(w.s.q0 + i0) * H + w.h * p.G + (j - i0 * p.G)) * D;
+                constexpr int PIECES = D / 8;  // 16-byte pieces of a query row
+#pragma unroll
+                for (int k = 0; k < R * PIECES / 32; ++k) {
+                    const int r = (32 * k + lane) / PIECES;
+                    const int64_t at = __shfl_sync(0xffffffffu, from, r);
+                    if (r < rows)
+                        cp_async16(dst + uint32_t(C::Q + 512 * k), a.q + at + 8 * (lane % PIECES));
+                }
+            }
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(C::FULL + rg.idx)) : "memory");
             const int last = w.s.c0 + w.s.N - 1;
             const bool ends = w.c == last || i + 1 == steps;
-            const int rows = begins ? min(R, w.s.m * p.G - w.tile * R) : 0;
             if (lane == 0) {
-                uint32_t flags = (begins ? uint32_t(kUnitBegins) : 0u) | (ends ? uint32_t(kUnitEnds) : 0u);
-                for (int s = 0; s < CH / 16; ++s)  // 16 keys s lie in piece (16 s) >> gsh
-                    if ((ok >> ((16 * s) >> gsh) & 1u) && w.c * CH + 16 * s < w.s.n) flags |= 1u << s;
-                Desc d;
-                d.t0 = w.c * CH;
-                d.n = w.s.n;
-                d.flags = flags;
-                d.shift = w.s.shift;
-                d.q0 = w.s.q0;
-                d.m = w.s.m;
-                d.h = w.h;
-                d.tile = w.tile;
-                d.place = entire && w.c == last ? kWhole : int(blockIdx.x) * 2 + (first && !entire ? 0 : 1);
-                d.prefix = w.b == a.B;
-                d.parts = !entire ? 0 : w.c == last ? 1 : ends ? sh.block_of(w0 + i + last - w.c) - int(blockIdx.x) + 1 : 0;
-                *reinterpret_cast<Desc *>(smem + C::OFF_DESC + 64 * rg.idx) = d;
-                const int n = __popc(ok) << gsh;
-                mbar_arrive_expect_tx(bar(C::FULL + rg.idx), uint32_t(n * (D + 8) + rows * D * 2));
-            }
-            __syncwarp();
-            if (there && what < 4) {
-                const int64_t row = ((int64_t(page) * Hk + w.h) << psh) + (t & ((1 << psh) - 1));
-                const bool codes = (what & 1) == 0, val = what >= 2;
-                const unsigned char *src =
-                    codes ? (val ? a.c.v_codes : a.c.k_codes) + row * (D / 2)
-                          : reinterpret_cast<const unsigned char *>((val ? a.c.v_scale : a.c.k_scale) + row);
-                const uint32_t per_key = codes ? D / 2 : 4;
-                const uint32_t dst = sbase + uint32_t(rg.idx * C::STAGE) + (codes ? 0 : 2 * C::CODES) +
-                                     (val ? (codes ? C::CODES : 4 * CH) : 0) + uint32_t(piece << gsh) * per_key;
-                bulk_load(dst, src, per_key << gsh, bar(C::FULL + rg.idx));
-            }
-            if (lane < rows) {
-                const int j = w.tile * R + lane, t = j / p.G;
-                bulk_load(sbase + uint32_t(rg.idx * C::STAGE + C::Q + lane * D * 2),
-                          a.q + (int64_t(w.s.q0 + t) * H + w.h * p.G + (j - t * p.G)) * D, D * 2, bar(C::FULL + rg.idx));
-            }
-            ++issued;
-            if (i + 1 < steps) {
-                w.next(p, seqs);
-                begins = w.c == w.s.c0;
-                if (begins) {
-                    entire = true;
-                    first = false;
+                Desc *d = reinterpret_cast<Desc *>(smem + C::OFF_DESC + 64 * rg.idx);
+                const uint32_t flags = ok | (begins ? uint32_t(kUnitBegins) : 0u) | (ends ? uint32_t(kUnitEnds) : 0u);
+                *reinterpret_cast<int4 *>(d) = make_int4(w.c * CH, w.s.n, int(flags), w.s.shift);
+                if (begins || ends) {
+                    *reinterpret_cast<int4 *>(&d->q0) = make_int4(w.s.q0, w.s.m, w.h, w.tile);
+                    d->place = entire && w.c == last ? kWhole : int(blockIdx.x) * 2 + (first && !entire ? 0 : 1);
+                    d->prefix = w.b == a.B;
+                    d->parts =
+                        !entire ? 0 : w.c == last ? 1 : ends ? sh.block_of(w0 + i + last - w.c) - int(blockIdx.x) + 1 : 0;
                 }
-                page = page_of();
+                mbar_arrive(bar(C::FULL + rg.idx));
+            }
+            w = ahead;
+            page = next_page;
+            begins = w.c == w.s.c0;
+            if (begins) {
+                entire = true;
+                first = false;
             }
         }
-        // every copy in flight lands before the block may end
-        Ring rd;
-        for (int i = 0; i < issued; ++i, rd.next(C::STAGES))
-            if (i + C::STAGES >= issued)
-                wait_bounded_err(bar(C::FULL + rd.idx), rd.phase, s_abort, kSiteKvWait, kWaitLimitNs, true, a.err);
+        cp_async_wait_all();  // every copy in flight lands before the block may end
         return;
     }
 
