@@ -87,8 +87,11 @@ __device__ __forceinline__ uint32_t and_xor(uint32_t w, uint32_t mask, uint32_t 
 __device__ __forceinline__ uint32_t nib_lo(uint32_t w) { return and_xor(w, 0x000f000fu, 0x00080008u); }
 __device__ __forceinline__ uint32_t nib_hi(uint32_t w) { return and_xor(w, 0x00f000f0u, 0x00800080u); }
 
-// The chunks of all units, dealt to the blocks: n each, and one more to the first `more`.  With
-// fewer chunks than blocks the last ones have none, so the blocks of a unit are consecutive.
+// The work of all units, dealt to the blocks: n places each, and one more to the first `more`.  A unit
+// is as many places as it has chunks, behind kUnitCost empty ones that stand for its start and end (its
+// queries made operands, its warps' rows joined: some 5000 clocks, where a chunk takes 1900).  A block
+// works on the chunks at its places; the blocks of a unit are consecutive.
+constexpr int kUnitCost = 3;
 struct Shares {
     int64_t n, more;
     __device__ __forceinline__ Shares(int64_t total, int ctas) {
@@ -96,9 +99,9 @@ struct Shares {
         more = total - n * ctas;
     }
     __device__ __forceinline__ int64_t begin(int64_t block) const { return n * block + min(block, more); }
-    __device__ __forceinline__ int block_of(int64_t chunk) const {
+    __device__ __forceinline__ int block_of(int64_t place) const {
         const int64_t big = (n + 1) * more;
-        return int(chunk < big ? chunk / (n + 1) : more + (chunk - big) / n);
+        return int(place < big ? place / (n + 1) : more + (place - big) / n);
     }
 };
 
@@ -133,7 +136,8 @@ struct RCfg {
     static constexpr int CODES = CH * D / 2;       // a chunk's codes, of keys or of values
     static constexpr int Q = 2 * CODES + 2 * CH * 4;  // the unit's query rows, where one begins
     static constexpr int STAGE = Q + R * D * 2;
-    static constexpr int PART = R * (D + 2) * 4;   // a warp's rows when a unit ends: values, reference, sum
+    static constexpr int PROW = D + 8;              // floats of a row of a part
+    static constexpr int PART = R * (PROW + 2) * 4;  // a warp's rows when a unit ends: values, reference, sum
     static constexpr int OFF_PART = STAGES * STAGE;
     static constexpr int OFF_DESC = OFF_PART + WARPS * PART;      // a Desc per stage
     static constexpr int OFF_BAR = OFF_DESC + STAGES * 64;
@@ -158,7 +162,7 @@ struct Desc {
     int pad[5];
 };
 static_assert(sizeof(Desc) == 64, "a stage's description");
-enum : uint32_t { kUnitBegins = 1u << 16, kUnitEnds = 1u << 17 };  // ends: or the block's share does
+enum : uint32_t { kUnitBegins = 1u << 16, kUnitEnds = 1u << 17, kShareEnds = 1u << 18 };  // unit: or its part here
 constexpr int kWhole = -1;
 
 template <int D, int NT, bool CAP>
@@ -194,7 +198,7 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
     int64_t mine = 0;
     for (int64_t b = s0; b < s1; ++b) {
         const Seq s = load_seq<R>(p, b, blockIdx.x == 0);
-        mine += int64_t(s.tiles) * s.N;
+        mine += int64_t(s.tiles) * (s.N + kUnitCost);
     }
     mine *= Hk;
     int64_t before = mine;
@@ -213,19 +217,23 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
     if (blockIdx.x >= total) return;
     const Shares sh(total, p.ctas);
     const int64_t w0 = sh.begin(blockIdx.x), w1 = sh.begin(blockIdx.x + 1);
-    const int steps = int(w1 - w0);
     __syncthreads();
     if (before <= w0 && w0 < before + mine) {
         int64_t at = before, b = s0;
         Seq s = load_seq<R>(p, b, false);
-        while (at + int64_t(s.tiles) * s.N * Hk <= w0) {
-            at += int64_t(s.tiles) * s.N * Hk;
+        while (at + int64_t(s.tiles) * (s.N + kUnitCost) * Hk <= w0) {
+            at += int64_t(s.tiles) * (s.N + kUnitCost) * Hk;
             s = load_seq<R>(p, ++b, false);
         }
+        // the unit of place w0, and the first chunk from there on: this unit's, as its chunks come last
+        const int64_t r = w0 - at, u = r / (s.N + kUnitCost), c = r - u * (s.N + kUnitCost) - kUnitCost;
         scan[0] = b;
-        scan[1] = w0 - at;
+        scan[1] = u;
+        scan[2] = c > 0 ? c : 0;
+        scan[3] = w0 + (c < 0 ? -c : 0);
     }
     __syncthreads();
+    if (scan[3] >= w1) return;  // places of a unit's start alone
 
     if (warp == WARPS) {
         // ---------------- the loading warp: one chunk per stage, 16 bytes a lane and copy ----------------
@@ -234,10 +242,10 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
         Walk<R> w;
         w.b = scan[0];
         w.s = load_seq<R>(p, w.b, false);
-        const int64_t r0 = scan[1], u0 = r0 / w.s.N;
-        w.c = w.s.c0 + int(r0 % w.s.N);
-        w.tile = int(u0 % w.s.tiles);
-        w.h = int(u0 / w.s.tiles);
+        w.c = w.s.c0 + int(scan[2]);
+        w.tile = int(scan[1] % w.s.tiles);
+        w.h = int(scan[1] / w.s.tiles);
+        int64_t place = scan[3];  // of the chunk
         bool entire = w.c == w.s.c0;  // whether this block has had the unit from its first chunk on
         bool begins = true, first = true;
         constexpr int SUBS = CH / 16;
@@ -249,11 +257,14 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
         int page = page_of(w);
         const uint8_t *const kc = a.c.k_codes + 16 * lane, *const vc = a.c.v_codes + 16 * lane;
         Ring rg;
-        for (int i = 0; i < steps; ++i, rg.next(C::STAGES)) {
+        for (bool more = true; more; rg.next(C::STAGES)) {
             // the next chunk's pages are looked up while this one is copied
             Walk<R> ahead = w;
             int next_page = -1;
-            if (i + 1 < steps) {
+            const int last = w.s.c0 + w.s.N - 1;
+            const int64_t next_place = place + 1 + (w.c == last ? kUnitCost : 0);
+            more = next_place < w1;
+            if (more) {
                 ahead.next(p, seqs);
                 next_page = page_of(ahead);
             }
@@ -294,23 +305,24 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
                 }
             }
             asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(C::FULL + rg.idx)) : "memory");
-            const int last = w.s.c0 + w.s.N - 1;
-            const bool ends = w.c == last || i + 1 == steps;
+            const bool ends = w.c == last || !more;
             if (lane == 0) {
                 Desc *d = reinterpret_cast<Desc *>(smem + C::OFF_DESC + 64 * rg.idx);
-                const uint32_t flags = ok | (begins ? uint32_t(kUnitBegins) : 0u) | (ends ? uint32_t(kUnitEnds) : 0u);
+                const uint32_t flags = ok | (begins ? uint32_t(kUnitBegins) : 0u) | (ends ? uint32_t(kUnitEnds) : 0u) |
+                                       (more ? 0u : uint32_t(kShareEnds));
                 *reinterpret_cast<int4 *>(d) = make_int4(w.c * CH, w.s.n, int(flags), w.s.shift);
                 if (begins || ends) {
                     *reinterpret_cast<int4 *>(&d->q0) = make_int4(w.s.q0, w.s.m, w.h, w.tile);
                     d->place = entire && w.c == last ? kWhole : int(blockIdx.x) * 2 + (first && !entire ? 0 : 1);
                     d->prefix = w.b == a.B;
                     d->parts =
-                        !entire ? 0 : w.c == last ? 1 : ends ? sh.block_of(w0 + i + last - w.c) - int(blockIdx.x) + 1 : 0;
+                        !entire ? 0 : w.c == last ? 1 : ends ? sh.block_of(place + last - w.c) - int(blockIdx.x) + 1 : 0;
                 }
                 mbar_arrive(bar(C::FULL + rg.idx));
             }
             w = ahead;
             page = next_page;
+            place = next_place;
             begins = w.c == w.s.c0;
             if (begins) {
                 entire = true;
@@ -335,10 +347,11 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
     Ring rg;
     uint32_t joins = 0;
     const int og = order(g);
-    for (int step = 0; step < steps; ++step, rg.next(C::STAGES)) {
+    for (bool more = true; more; rg.next(C::STAGES)) {
         if (!wait_all(bar(C::FULL + rg.idx), rg.phase, s_abort, a.err)) break;
         const Desc *desc = reinterpret_cast<const Desc *>(smem + C::OFF_DESC + 64 * rg.idx);
         const uint32_t flags = desc->flags;
+        more = (flags & kShareEnds) == 0;
         if (flags & kUnitBegins) {
             // ---- a unit begins: its queries ----
             const int q0 = desc->q0, m = desc->m, tile = desc->tile, shift = desc->shift, n = desc->n;
@@ -611,13 +624,13 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
                     l += __shfl_xor_sync(0xffffffffu, l, 8);
                     l += __shfl_xor_sync(0xffffffffu, l, 16);
                     if (g == 0) {
-                        part[R * D + row] = l == 0.0f ? kNone : ref[nt][k];
-                        part[R * D + R + row] = l;
+                        part[R * C::PROW + row] = l == 0.0f ? kNone : ref[nt][k];
+                        part[R * C::PROW + R + row] = l;
                     }
 #pragma unroll
                     for (int mt = 0; mt < D / 16; ++mt) {
-                        // elements g D / 8 + 2 mt, + 1
-                        *reinterpret_cast<float2 *>(part + row * D + g * (D / 8) + 2 * mt) =
+                        // elements g D / 8 + 2 mt, + 1, where lanes write without conflicts
+                        *reinterpret_cast<float2 *>(part + row * C::PROW + 16 * mt + 2 * g) =
                             make_float2(o[nt][mt][k], o[nt][mt][k + 2]);
                     }
                 }
@@ -635,16 +648,18 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
                 const int row = u / (D / 4), d = 4 * (u % (D / 4));
                 float top = kNone;
 #pragma unroll
-                for (int w = 0; w < WARPS; ++w) top = fmaxf(top, all[w * (C::PART / 4) + R * D + row]);
+                for (int w = 0; w < WARPS; ++w) top = fmaxf(top, all[w * (C::PART / 4) + R * C::PROW + row]);
                 float l = 0.0f;
                 float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
                 for (int w = 0; w < WARPS; ++w) {
                     const float *q = all + w * (C::PART / 4);
-                    const float f = ex2(q[R * D + row] - top);
-                    const float4 z = *reinterpret_cast<const float4 *>(q + row * D + d);
-                    l += q[R * D + R + row] * f;
-                    v.x += z.x * f, v.y += z.y * f, v.z += z.z * f, v.w += z.w * f;
+                    const float f = ex2(q[R * C::PROW + row] - top);
+                    const int at = row * C::PROW + 8 * (d % (D / 8)) + 2 * (d / (D / 8));
+                    const float2 y = *reinterpret_cast<const float2 *>(q + at);
+                    const float2 z = *reinterpret_cast<const float2 *>(q + at + 16);
+                    l += q[R * C::PROW + R + row] * f;
+                    v.x += y.x * f, v.y += y.y * f, v.z += z.x * f, v.w += z.y * f;
                 }
                 const float inv = l > 0.0f ? 0x1p24f / l : l == 0.0f ? 0.0f : l;
                 const float lse = l == 0.0f ? -INFINITY : top + lg2(l);  // in powers of two
