@@ -23,8 +23,7 @@
 //   - the two row tiles are half a step apart: while one warpgroup is at its softmax
 //     the tensor core works for the other.
 // Keys that a row does not see, past its place or out of its window, are looked at only
-// in the chunks where a warp's rows have any; those and capped scores go through TMEM
-// once more.
+// in the chunks where a warp's rows have any; those scores go through TMEM once more.
 //
 // One unit = 256 rows of a key head and sequence, cut over `splits` blocks along its keys
 // where there are fewer units than SMs; partial rows then go to the workspace for
@@ -86,6 +85,17 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
+}
+
+// tanh of four numbers, with one reciprocal: tanh z = 1 - 2 / (e^2z + 1), and past 9 it is 1 to fp32.
+__device__ __forceinline__ void tanh4(float &a, float &b, float &c, float &d) {
+    auto e = [](float z) { return ex2(fminf(fmaxf(z, -9.5f), 9.5f) * (2.0f * kLog2e)) + 1.0f; };
+    const float ea = e(a), eb = e(b), ec = e(c), ed = e(d), ab = ea * eb, cd = ec * ed;
+    const float r = __fdividef(-2.0f, ab * cd), rab = r * cd, rcd = r * ab;  // the product is under 2^112
+    a = fmaf(rab, eb, 1.0f);
+    b = fmaf(rab, ea, 1.0f);
+    c = fmaf(rcd, ed, 1.0f);
+    d = fmaf(rcd, ec, 1.0f);
 }
 
 // Eight codes as bf16 integers, pairs (0, 4), (1, 5), (2, 6), (3, 7): (code + 8) | 0x4300 is 136 + code.
@@ -224,7 +234,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
             if (!ok) break;
             tc_fence_after();
             const bool lost = *reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 8 + 4 * (n & 1)) != 0;
-            const bool slow = CAP || lost || t0 < all_lo || t0 + CH > all_hi;
+            const bool slow = lost || t0 < all_lo || t0 + CH > all_hi;
             // The reference rises by `up`: O, whose last product has ended with S's, and the sums follow.
             auto raise = [&](float up) {
                 const float f = ex2(-up);
@@ -248,25 +258,30 @@ __global__ void __launch_bounds__(T_THREADS, 1)
             rise = 0.0f;
             const bool first_keys = __any_sync(0xffffffffu, !seen);
             if (slow || first_keys) {
-                // ---- the row's largest score; scores as they are used (capped, -inf where the row does not
-                // see) go back to their place ----
+                // ---- the row's largest score; where some keys are not seen, the scores with -inf for those
+                // go back to their place ----
                 float top = -INFINITY;
 #pragma unroll 1
-                for (int c = 0; c < CH; c += 16) {
-                    uint32_t v[16];
-                    tmem_ld_32x32b_x16(ts + uint32_t(c), v);
+                for (int c = 0; c < CH; c += 32) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(ts + uint32_t(c), v);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
+                    for (int e = 0; e < 32; ++e) {
                         const float k = reinterpret_cast<const float *>(ks)[c + e];
-                        const int t = t0 + c + e;
                         float x = __uint_as_float(v[e]) * k;
                         if (CAP) x = a.softcap * kLog2e * tanh_exp(x);
-                        if (t < row_lo || t >= row_hi || (lost && k == -INFINITY)) x = -INFINITY;
-                        v[e] = __float_as_uint(x);
+                        if (slow) {
+                            const int t = t0 + c + e;
+                            if (t < row_lo || t >= row_hi || (lost && k == -INFINITY)) x = -INFINITY;
+                            v[e] = __float_as_uint(x);
+                        }
                         top = fmaxf(top, x);
                     }
-                    tmem_st_32x32b_x16(ts + uint32_t(c), v);
+                    if (slow) {
+                        tmem_st_32x32b_x16(ts + uint32_t(c), reinterpret_cast<const uint32_t(&)[16]>(v[0]));
+                        tmem_st_32x32b_x16(ts + uint32_t(c + 16), reinterpret_cast<const uint32_t(&)[16]>(v[16]));
+                    }
                 }
                 tmem_wait_st();
                 if (!seen && top > -INFINITY) {  // nothing has been summed yet: the reference may be anywhere
@@ -283,31 +298,56 @@ __global__ void __launch_bounds__(T_THREADS, 1)
                     uint32_t v[32], w[16];
                     tmem_ld_32x32b_x32(ts + uint32_t(c), v);
                     tmem_wait_ld();
-                    uint64_t minus = pair2(-m, -m);
-                    uint64_t x[16];
-                    float most = -INFINITY;
+                    // x = S ks - m (capped: cap tanh(S ks) - m), or the prepared scores less m; p = 2^x
+                    uint64_t more;  // what the block adds to the sum
+                    float most[4];
+                    auto block = [&] {
+                        const uint64_t minus = pair2(-m, -m);
+                        more = pair2(0.0f, 0.0f);
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        x[e >> 1] = pair2u(v[e], v[e + 1]);
-                        x[(e >> 1) + 1] = pair2u(v[e + 2], v[e + 3]);
-                        if constexpr (decltype(raw)::value) {
-                            const float4 k = ks[(c + e) >> 2];
-                            x[e >> 1] = fma2(x[e >> 1], pair2(k.x, k.y), minus);
-                            x[(e >> 1) + 1] = fma2(x[(e >> 1) + 1], pair2(k.z, k.w), minus);
+                        for (int k = 0; k < 4; ++k) most[k] = -INFINITY;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            uint64_t a0 = pair2u(v[e], v[e + 1]), a1 = pair2u(v[e + 2], v[e + 3]);
                             float x0, x1, x2, x3;
-                            split2(x[e >> 1], x0, x1);
-                            split2(x[(e >> 1) + 1], x2, x3);
-                            most = fmax3(fmax3(most, x0, x1), x2, x3);
-                        } else {
-                            x[e >> 1] = add2(x[e >> 1], minus);
-                            x[(e >> 1) + 1] = add2(x[(e >> 1) + 1], minus);
+                            if constexpr (decltype(raw)::value) {
+                                const float4 k = ks[(c + e) >> 2];
+                                if constexpr (CAP) {
+                                    split2(f32x2_mul(a0, pair2(k.x, k.y)), x0, x1);
+                                    split2(f32x2_mul(a1, pair2(k.z, k.w)), x2, x3);
+                                    tanh4(x0, x1, x2, x3);
+                                    const uint64_t cap = pair2(a.softcap * kLog2e, a.softcap * kLog2e);
+                                    a0 = fma2(pair2(x0, x1), cap, minus);
+                                    a1 = fma2(pair2(x2, x3), cap, minus);
+                                } else {
+                                    a0 = fma2(a0, pair2(k.x, k.y), minus);
+                                    a1 = fma2(a1, pair2(k.z, k.w), minus);
+                                }
+                                split2(a0, x0, x1);
+                                split2(a1, x2, x3);
+                                most[(e >> 1) & 2] = fmax3(most[(e >> 1) & 2], x0, x1);
+                                most[((e >> 1) & 2) + 1] = fmax3(most[((e >> 1) & 2) + 1], x2, x3);
+                            } else {
+                                split2(add2(a0, minus), x0, x1);
+                                split2(add2(a1, minus), x2, x3);
+                            }
+                            const float4 z = vs[(c + e) >> 2];
+                            const uint64_t p0 = pair2(ex2(x0), ex2(x1)), p1 = pair2(ex2(x2), ex2(x3));
+                            more = add2(more, add2(p0, p1));
+                            float y0, y1, y2, y3;
+                            split2(f32x2_mul(p0, pair2(z.x, z.y)), y0, y1);
+                            split2(f32x2_mul(p1, pair2(z.z, z.w)), y2, y3);
+                            w[e >> 1] = pack_bf16x2(y0, y1);
+                            w[(e >> 1) + 1] = pack_bf16x2(y2, y3);
                         }
-                    }
+                    };
+                    block();
                     if constexpr (decltype(raw)::value) {
-                        rise = fmaxf(rise, most);
-                        if (__any_sync(0xffffffffu, most > 60.0f)) {
-                            // out of a weight's range: raise the reference here, and what the chunk has so far
-                            const float up = most > 60.0f ? most : 0.0f, f = ex2(-up);
+                        const float top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+                        if (__any_sync(0xffffffffu, top > 60.0f)) {
+                            // out of a weight's range: raise the reference here, and what the chunk has so far,
+                            // and do the block again
+                            const float up = top > 60.0f ? top : 0.0f, f = ex2(-up);
                             split2(sum, l0, l1);
                             raise(up);
                             sum = pair2(l0, l1);
@@ -323,29 +363,15 @@ __global__ void __launch_bounds__(T_THREADS, 1)
                                 tmem_st_32x32b_x16(ts + uint32_t(d), w);
                             }
                             tmem_wait_st();
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) x[e] = add2(x[e], pair2(-up, -up));
+                            block();
                         }
+                        rise = fmaxf(rise, fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])));
                     }
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 z = vs[(c + e) >> 2];
-                        float x0, x1, x2, x3;
-                        split2(x[e >> 1], x0, x1);
-                        split2(x[(e >> 1) + 1], x2, x3);
-                        const uint64_t p0 = pair2(ex2(x0), ex2(x1)), p1 = pair2(ex2(x2), ex2(x3));
-                        sum = add2(sum, p0);
-                        sum = add2(sum, p1);
-                        float y0, y1, y2, y3;
-                        split2(f32x2_mul(p0, pair2(z.x, z.y)), y0, y1);
-                        split2(f32x2_mul(p1, pair2(z.z, z.w)), y2, y3);
-                        w[e >> 1] = pack_bf16x2(y0, y1);
-                        w[(e >> 1) + 1] = pack_bf16x2(y2, y3);
-                    }
+                    sum = add2(sum, more);
                     tmem_st_32x32b_x16(ts + uint32_t(c >> 1), w);
                 }
             };
-            if (slow || first_keys) weights(Is<false>{});
+            if (slow) weights(Is<false>{});
             else weights(Is<true>{});
             split2(sum, l0, l1);
             tmem_wait_st();
