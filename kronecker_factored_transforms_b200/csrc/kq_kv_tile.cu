@@ -89,7 +89,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 
 // tanh of four numbers, with one reciprocal: tanh z = 1 - 2 / (e^2z + 1), and past 9 it is 1 to fp32.
 __device__ __forceinline__ void tanh4(float &a, float &b, float &c, float &d) {
-    auto e = [](float z) { return ex2(fminf(fmaxf(z, -9.5f), 9.5f) * (2.0f * kLog2e)) + 1.0f; };
+    auto e = [](float z) {
+        float y;  // z within +-9.5; a NaN stays one
+        asm("{\n\t.reg .f32 t;\n\tmax.NaN.f32 t, %1, 0fC1180000;\n\tmin.NaN.f32 %0, t, 0f41180000;\n\t}" : "=f"(y) : "f"(z));
+        return ex2(y * (2.0f * kLog2e)) + 1.0f;
+    };
     const float ea = e(a), eb = e(b), ec = e(c), ed = e(d), ab = ea * eb, cd = ec * ed;
     const float r = __fdividef(-2.0f, ab * cd), rab = r * cd, rcd = r * ab;  // the product is under 2^112
     a = fmaf(rab, eb, 1.0f);
@@ -159,8 +163,19 @@ __global__ void __launch_bounds__(T_THREADS, 1)
     int u = id / splits;
     const int h = u % Hk;
     u /= Hk;
-    const int64_t b = prefix ? a.B : u % units_b;
-    const int tile = tiles - 1 - u / units_b;  // the last rows of a chunk have the most keys: they come first
+    // The longest units first: sequences by falling length (up to 32 of them), and the last rows of a chunk,
+    // which see the most keys, before its first.
+    int64_t b = prefix ? a.B : u / tiles;
+    if (!prefix && units_b <= 32) {
+        const int len = lane < units_b ? a.kv_len[lane] : INT_MIN;
+        int rank = 0;
+        for (int k = 0; k < units_b; ++k) {
+            const int other = __shfl_sync(0xffffffffu, len, k);
+            rank += other > len || (other == len && k < lane);
+        }
+        b = __ffs(__ballot_sync(0xffffffffu, lane < units_b && rank == int(b))) - 1;
+    }
+    const int tile = tiles - 1 - u % tiles;
     const Seq s = load_seq<T_ROWS>(p, b, tile == 0 && h == 0 && split == 0 && tid == 0 && !prefix);
     const int rows = min(T_ROWS, s.m * p.G - tile * T_ROWS);
     const int first = tile * T_ROWS / p.G, last = (tile * T_ROWS + max(rows, 1) - 1) / p.G;  // queries
@@ -179,15 +194,23 @@ __global__ void __launch_bounds__(T_THREADS, 1)
 
     // ---- queries: bf16 rows as operands; rows past the last are zeros ----
     if (wg < 2) {
+        // a warp brings 32 rows, whole rows side by side: a lane 16 bytes of 256 / D rows a step
         const int r = tid & 127, j = tile * T_ROWS + 128 * wg + r;
         const bool real = 128 * wg + r < rows;
         const int i = real ? j / p.G : 0;
-        const uint4 *q = reinterpret_cast<const uint4 *>(
-            a.q + (int64_t(s.q0 + i) * H + h * p.G + (real ? j - i * p.G : 0)) * D);
+        const uint16_t *mine = real ? a.q + (int64_t(s.q0 + i) * H + h * p.G + (j - i * p.G)) * D : nullptr;
+        constexpr int PIECES = D / 8, PER = 32 / PIECES;
+        uint4 q[32 / PER];
 #pragma unroll
-        for (int k = 0; k < D / 8; ++k)
-            *reinterpret_cast<uint4 *>(smem + C::OFF_Q + wg * C::OPERAND + operand_place(r, k)) =
-                real ? order_bf16(q[k]) : make_uint4(0, 0, 0, 0);
+        for (int k = 0; k < 32 / PER; ++k) {
+            const uint64_t from = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(mine), k * PER + lane / PIECES);
+            q[k] = make_uint4(0, 0, 0, 0);
+            if (from) q[k] = reinterpret_cast<const uint4 *>(from)[lane % PIECES];
+        }
+#pragma unroll
+        for (int k = 0; k < 32 / PER; ++k)
+            *reinterpret_cast<uint4 *>(smem + C::OFF_Q + wg * C::OPERAND +
+                                       operand_place((r & ~31) + k * PER + lane / PIECES, lane % PIECES)) = order_bf16(q[k]);
         fence_proxy_async_smem();
         mbar_arrive(bar(C::QREADY));
     }
@@ -223,6 +246,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
             }
         }
         // all rows of the warp see all keys of [all_lo, all_hi) (rows past the last are not looked at)
+        const bool no_rows = !__any_sync(0xffffffffu, real);
         const int all_lo = __reduce_max_sync(0xffffffffu, real ? row_lo : 0);
         const int all_hi = __reduce_min_sync(0xffffffffu, real ? row_hi : INT_MAX);
         float rise = 0.0f;  // how far the last chunk's largest score was over the reference
@@ -233,6 +257,13 @@ __global__ void __launch_bounds__(T_THREADS, 1)
             ok = wait(C::KFULL + (n & 1), uint32_t(n >> 1)) && wait(C::SREADY + wg, uint32_t(n));
             if (!ok) break;
             tc_fence_after();
+            if (no_rows) {  // this warp's weights are never read
+                if (lane == 0) {
+                    mbar_arrive(bar(C::PREADY + wg));
+                    mbar_arrive(bar(C::SCFREE + (n & 1)));
+                }
+                continue;
+            }
             const bool lost = *reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 8 + 4 * (n & 1)) != 0;
             const bool slow = lost || t0 < all_lo || t0 + CH > all_hi;
             // The reference rises by `up`: O, whose last product has ended with S's, and the sums follow.
@@ -261,6 +292,21 @@ __global__ void __launch_bounds__(T_THREADS, 1)
                 // ---- the row's largest score; where some keys are not seen, the scores with -inf for those
                 // go back to their place ----
                 float top = -INFINITY;
+                if (!slow) {
+#pragma unroll 1
+                    for (int c = 0; c < CH; c += 32) {
+                        uint32_t v[32];
+                        tmem_ld_32x32b_x32(ts + uint32_t(c), v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 k = ks[(c + e) >> 2];
+                            top = fmax3(top, __uint_as_float(v[e]) * k.x, __uint_as_float(v[e + 1]) * k.y);
+                            top = fmax3(top, __uint_as_float(v[e + 2]) * k.z, __uint_as_float(v[e + 3]) * k.w);
+                        }
+                    }
+                    if (CAP) top = a.softcap * kLog2e * tanh_exp(top);  // which rises with its argument
+                } else
 #pragma unroll 1
                 for (int c = 0; c < CH; c += 32) {
                     uint32_t v[32];
@@ -271,17 +317,13 @@ __global__ void __launch_bounds__(T_THREADS, 1)
                         const float k = reinterpret_cast<const float *>(ks)[c + e];
                         float x = __uint_as_float(v[e]) * k;
                         if (CAP) x = a.softcap * kLog2e * tanh_exp(x);
-                        if (slow) {
-                            const int t = t0 + c + e;
-                            if (t < row_lo || t >= row_hi || (lost && k == -INFINITY)) x = -INFINITY;
-                            v[e] = __float_as_uint(x);
-                        }
+                        const int t = t0 + c + e;
+                        if (t < row_lo || t >= row_hi || (lost && k == -INFINITY)) x = -INFINITY;
+                        v[e] = __float_as_uint(x);
                         top = fmaxf(top, x);
                     }
-                    if (slow) {
-                        tmem_st_32x32b_x16(ts + uint32_t(c), reinterpret_cast<const uint32_t(&)[16]>(v[0]));
-                        tmem_st_32x32b_x16(ts + uint32_t(c + 16), reinterpret_cast<const uint32_t(&)[16]>(v[16]));
-                    }
+                    tmem_st_32x32b_x16(ts + uint32_t(c), reinterpret_cast<const uint32_t(&)[16]>(v[0]));
+                    tmem_st_32x32b_x16(ts + uint32_t(c + 16), reinterpret_cast<const uint32_t(&)[16]>(v[16]));
                 }
                 tmem_wait_st();
                 if (!seen && top > -INFINITY) {  // nothing has been summed yet: the reference may be anywhere
@@ -391,8 +433,11 @@ __global__ void __launch_bounds__(T_THREADS, 1)
             const float lse = l == 0.0f ? -INFINITY : m + lg2(l);  // in powers of two
             const int64_t at = int64_t(s.q0 + i) * H + h * p.G + (real ? j - i * p.G : 0);
             const bool final = splits == 1 && !p.partial;
-            float *po = p.tile_o + (int64_t(prefix ? p.own_splits : 0) + split) * a.T * H * D + at * D;
-#pragma unroll
+            float *po = p.tile_o + (int64_t(prefix ? p.own_splits : 0) + split) * a.T * H * D;
+            // 32 columns at a time through the warp's 4 KB of the queries' place (its products have ended), a
+            // row's 16-byte pieces exchanged by row, so that a store takes 128 bytes of 4 rows
+            unsigned char *own = smem + C::OFF_Q + wg * C::OPERAND + (warp & 3) * 4096;
+#pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 uint32_t v[32];
                 if (N > 0) {
@@ -406,14 +451,23 @@ __global__ void __launch_bounds__(T_THREADS, 1)
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
                         o[(k >> 1) + 4 * (k & 1)] = N > 0 && l != 0.0f ? __uint_as_float(v[e + k]) * inv : 0.0f;
-                    if (!real) {
-                    } else if (final) {
-                        *reinterpret_cast<uint4 *>(a.out + at * D + c + e) =
-                            make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
-                                       pack_bf16x2(o[6], o[7]));
-                    } else {
-                        *reinterpret_cast<float4 *>(po + c + e) = make_float4(o[0], o[1], o[2], o[3]);
-                        *reinterpret_cast<float4 *>(po + c + e + 4) = make_float4(o[4], o[5], o[6], o[7]);
+                    *reinterpret_cast<float4 *>(own + 128 * lane + (((e / 4) ^ (lane & 7)) << 4)) =
+                        make_float4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<float4 *>(own + 128 * lane + (((e / 4 + 1) ^ (lane & 7)) << 4)) =
+                        make_float4(o[4], o[5], o[6], o[7]);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int row = 4 * k + (lane >> 3);
+                    const int64_t to_row = __shfl_sync(0xffffffffu, real ? at : int64_t(-1), row);
+                    const float4 o = *reinterpret_cast<const float4 *>(own + 128 * row + (((lane ^ row) & 7) << 4));
+                    if (to_row >= 0) {
+                        if (final)
+                            *reinterpret_cast<uint2 *>(a.out + to_row * D + c + 4 * (lane & 7)) =
+                                make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+                        else
+                            *reinterpret_cast<float4 *>(po + to_row * D + c + 4 * (lane & 7)) = o;
                     }
                 }
                 __syncwarp();
