@@ -832,15 +832,17 @@ int row_tile(int64_t rows) { return rows <= 8 ? 8 : 16; }
 bool many_rows(int64_t rows) { return rows > 48; }
 bool many_prefix_rows(int64_t rows) { return rows > 32; }
 
-// Blocks to cut a unit's keys over, where there are too few units for all SMs: the number that leaves the
-// fewest SMs idle in the last round of blocks, with a hundredth off for each further part to join.
-int tile_splits(int64_t units, int64_t most) {
+// Blocks to cut a unit's keys over, where there are too few units for all SMs, up to two rounds of blocks:
+// the number that ends first, a block being as long as its chunks and four more (its start and its rows'
+// end: some 17000 clocks, where a chunk takes 4500), and a part to join a third of one.
+int most_splits(int64_t units) { return units < 2 * kSms ? int(2 * kSms / units < 32 ? 2 * kSms / units : 32) : 1; }
+int tile_splits(int64_t units, int64_t chunks) {
     int best = 1;
-    double good = 0.0;
-    for (int s = 1; s <= 32 && s <= most && units * s <= 4 * kSms; ++s) {
-        const int64_t blocks = units * s, rounds = (blocks + kSms - 1) / kSms;
-        const double used = double(blocks) / double(rounds * kSms) - 0.01 * s;
-        if (used > good) best = s, good = used;
+    double least = 0.0;
+    for (int s = 1; s <= most_splits(units) && s <= chunks; ++s) {
+        const double rounds = double((units * s + kSms - 1) / kSms);
+        const double cost = rounds * (4.0 + double((chunks + s - 1) / s)) + 0.33 * s;
+        if (s == 1 || cost < least) best = s, least = cost;
     }
     return best;
 }
@@ -854,8 +856,8 @@ uint64_t lay_out(Plan &p, unsigned char *base, int64_t T, int64_t B, int H, int 
     const int G = H / Hk;
     p.G = G;
     const bool own_tile = many_rows(int64_t(max_q) * G), pre_tile = own_tile || many_prefix_rows(T * G);
-    const int own = own_tile ? tile_splits(kv_tiles(max_q, G) * B * Hk, INT32_MAX) : 0;
-    const int pre = pre_tile ? tile_splits(kv_tiles(T, G) * Hk, INT32_MAX) : 0;
+    const int own = own_tile ? most_splits(kv_tiles(max_q, G) * B * Hk) : 0;
+    const int pre = pre_tile ? most_splits(kv_tiles(T, G) * Hk) : 0;
     p.own_splits = own_tile ? tile_splits(kv_tiles(max_q, G) * B * Hk, own_most) : 0;
     p.pre_splits = pre_most && pre_tile ? tile_splits(kv_tiles(T, G) * Hk, pre_most) : 0;
     p.rows_own = !own_tile;
