@@ -29,18 +29,10 @@ __device__ __forceinline__ float lg2(float x) {
 __device__ __forceinline__ float tanh_exp(float z) {
     return 1.0f - __fdividef(2.0f, ex2(z * (2.0f * kLog2e)) + 1.0f);
 }
-// Wait for a phase, looking every `ns` nanoseconds (0: without a pause) so that waiting warps leave the
-// issue slots to the others; gives up as wait_bounded_err does.
-__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile int *abort, unsigned int *err,
-                                         uint32_t ns = 0) {
-    bool ok = tc::mbar_try_wait(bar, parity);
-    if (ns)
-        for (int i = 0; i < 1000 && !ok; ++i) {
-            __nanosleep(ns);
-            ok = tc::mbar_try_wait(bar, parity);
-        }
-    if (!ok) ok = tc::wait_bounded_err(bar, parity, abort, kSiteKvWait, tc::kWaitLimitNs, false, err);
-    return __all_sync(0xffffffffu, ok);
+// Wait for a phase; gives up as wait_bounded_err does.
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile int *abort, unsigned int *err) {
+    return __all_sync(0xffffffffu,
+                      tc::wait_bounded_err(bar, parity, abort, kSiteKvWait, tc::kWaitLimitNs, false, err));
 }
 
 // ---- which keys and rows a unit has ---------------------------------------------

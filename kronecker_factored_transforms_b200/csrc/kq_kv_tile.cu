@@ -40,7 +40,6 @@ using namespace tc;
 
 constexpr int T_THREADS = 416;  // two warpgroups of softmax, one of codes, a warp of MMAs
 constexpr int T_ROWS = 256;
-constexpr uint32_t kPauseM = 20, kPauseD = 200, kPauseS = 20;  // ns between looks, by role
 
 template <int D>
 struct TCfg {
@@ -229,8 +228,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         mbar_arrive(bar(C::QREADY));
     }
 
-    const uint32_t pause = warp == 12 ? kPauseM : wg == 2 ? kPauseD : kPauseS;
-    auto wait = [&](int i, uint32_t parity) -> bool { return wait_all(bar(i), parity & 1u, s_abort, a.err, pause); };
+    auto wait = [&](int i, uint32_t parity) -> bool { return wait_all(bar(i), parity & 1u, s_abort, a.err); };
 
     if (rows <= 0) {
         // no such rows (a bound on them sized the grid)
