@@ -355,8 +355,8 @@ kq_status kq_kv_append(const kq_kv_cache *cache, const kq_kv_transform *tf, cons
 
 /*
  * kq_kv_gather -- the rows at T slots as the values they stand for: k_out and
- * v_out [T, kv_heads, head_dim] device bf16, 16-byte aligned, code * s rounded
- * once (for handing cached tokens to another program, and for checks).  A
+ * v_out [T, kv_heads, head_dim] device bf16, 16-byte aligned, code * s in fp32,
+ * then bf16 (for handing cached tokens to another program, and for checks).  A
  * negative slot gives zeros; a slot past the last page too, and kq_device_error
  * then reports 65536.  Slots may repeat.  Outputs must not overlap the cache,
  * the slots or one another.  Asynchronous on `stream`; allocates nothing.
@@ -397,8 +397,11 @@ kq_status kq_kv_gather(const kq_kv_cache *cache, const int64_t *slots, uint16_t 
  *             (their rows stay as they were) and kq_device_error reports 131072.
  * A page number outside the cache, or a kv_len past the table, is never followed:
  * such keys count as masked and kq_device_error reports 131072.
- * Sizes: T, B >= 0 (0 is a no-op), q_heads a multiple of kv_heads with at most
- * 1024 heads, T * q_heads < 2^31, max_pages * page_size < 2^31.
+ * Sizes: T >= 0, 0 <= B <= 65535 (0 is a no-op; sequences may have no queries), q_heads
+ * a multiple of kv_heads with at most 1024 heads, T * q_heads < 2^31,
+ * max_pages * page_size < 2^30, prefix_len < 2^30.
+ * The scales in the cache are not negative and, where a query sees their row, finite;
+ * rows that it does not see may hold anything.
  * Scores and softmax sums are fp32, and the products' accumulators too.  The same
  * inputs give the same bits.  Nothing is read back to the host: sequences may
  * grow between replays of a captured graph.
@@ -432,7 +435,10 @@ kq_status kq_kv_attention_shared(const kq_kv_cache *cache, const uint16_t *q, co
                                  uint16_t *out, float *lse, void *workspace, uint64_t workspace_bytes, int64_t T,
                                  int64_t B, int q_heads, int max_q, kq_stream_t stream);
 
-/* Workspace bytes of the two calls above (0 for sizes they refuse). */
+/*
+ * Workspace bytes of the two calls above (0 for sizes they refuse), for exactly these T, B
+ * and max_q (1 where q_start is NULL): smaller calls may need more, as they are cut finer.
+ */
 uint64_t kq_kv_attention_workspace_bytes(int64_t T, int64_t B, int q_heads, int kv_heads, int head_dim, int max_q);
 
 /*
@@ -440,7 +446,8 @@ uint64_t kq_kv_attention_workspace_bytes(int64_t T, int64_t B, int q_heads, int 
  * kernels set when a bounded wait gives up (they then skip their remaining
  * work instead of hanging).  Synchronises `stream`.  *code receives 0 when
  * no wait timed out and no index was refused since the last call, else the sum
- * of the site codes (65536 and 131072: the cache's calls, see there).
+ * of the site codes (65536 and 131072: indices that the cache's calls refused, see
+ * there; 262144 and 524288: a wait of kq_kv_attention, of kq_kv_append).
  * Returns KQ_ERR_NULL for a NULL code, KQ_ERR_CUDA if the read fails.
  */
 kq_status kq_device_error(kq_stream_t stream, int *code);

@@ -493,6 +493,8 @@ kq_status kq_kv_gather(const kq_kv_cache *cache, const int64_t *slots, uint16_t 
 }
 
 namespace {
+constexpr int64_t kMaxSequences = 65535, kMaxKeys = int64_t(1) << 30;
+
 kq_status kv_attention(const kq_kv_cache *cache, const uint16_t *q, const int32_t *q_start,
                        const int32_t *prefix_pages, int64_t prefix_len, const int32_t *page_table, int64_t max_pages,
                        const int32_t *kv_len, float scale, float softcap, int window, uint16_t *out, float *lse,
@@ -502,9 +504,8 @@ kq_status kv_attention(const kq_kv_cache *cache, const uint16_t *q, const int32_
     if (T == 0 || B == 0) return KQ_OK;
     kq_status st = check_cache(cache);
     if (st != KQ_OK) return st;
-    if (q_heads % cache->kv_heads != 0 || T >= (int64_t(1) << 31) / q_heads || B > T || B > 65535 ||
-        (!q_start && T != B) || max_pages >= (int64_t(1) << 31) / cache->page_size ||
-        prefix_len >= (int64_t(1) << 30) || max_pages > INT64_MAX / (4 * B))
+    if (q_heads % cache->kv_heads != 0 || T >= (int64_t(1) << 31) / q_heads || B > kMaxSequences ||
+        (!q_start && T != B) || max_pages >= kMaxKeys / cache->page_size || prefix_len >= kMaxKeys)
         return KQ_ERR_SHAPE;
     if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.0f || window < 0 || max_q < 1)
         return KQ_ERR_ARG;
@@ -576,7 +577,7 @@ kq_status kq_kv_attention_shared(const kq_kv_cache *cache, const uint16_t *q, co
 
 uint64_t kq_kv_attention_workspace_bytes(int64_t T, int64_t B, int q_heads, int kv_heads, int head_dim, int max_q) {
     if (T <= 0 || B <= 0 || q_heads < 1 || q_heads > 1024 || kv_heads < 1 || q_heads % kv_heads != 0 || max_q < 1 ||
-        (head_dim != 64 && head_dim != 128) || T >= (int64_t(1) << 31) / q_heads)
+        (head_dim != 64 && head_dim != 128) || T >= (int64_t(1) << 31) / q_heads || B > kMaxSequences)
         return 0;
     return kq::kv_attention_workspace_bytes(T, B, q_heads, kv_heads, head_dim, int(max_q > T ? T : max_q));
 }

@@ -467,8 +467,9 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     ks[mt][k] = sc[16 * mt + og + 8 * k];
-                    // a scale of 0 (a row of zeros) counts as 2^-100 here: its codes are 0 anyway
-                    lv[mt][k] = fmaxf(lg2(sc[CH + 16 * mt + og + 8 * k]), -100.0f);
+                    // a scale of 0 (a row of zeros) counts as 2^-100 here: its codes are 0 anyway; an infinite
+                    // one as 2^128, so that a score of -inf leaves that key out too
+                    lv[mt][k] = fminf(fmaxf(lg2(sc[CH + 16 * mt + og + 8 * k]), -100.0f), 128.0f);
                 }
 #pragma unroll
                 for (int w = 0; w < W; ++w) {
@@ -706,9 +707,8 @@ __global__ void __launch_bounds__(128) kq_kv_combine_kernel(const __grid_constan
     int row[2] = {0, 0};
     if (p.rows_own) rec[0] = p.parts[at];
     if (p.rows_prefix) rec[1] = p.parts[rows + at];
-    if ((p.rows_own && (rec[0].y < 1 || rec[0].x < 0 || rec[0].x + rec[0].y > p.ctas)) ||
-        (p.rows_prefix && (rec[1].y < 1 || rec[1].x < 0 || rec[1].x + rec[1].y > p.ctas)))
-        return;  // a row past the bound on queries
+    auto sound = [&](const int2 &r) { return r.y >= 1 && r.y <= p.ctas && r.x >= 0 && r.x <= p.ctas - r.y; };
+    if ((p.rows_own && !sound(rec[0])) || (p.rows_prefix && !sound(rec[1]))) return;  // a row past the bound on queries
     if (!p.partial && p.rows_own && rec[0].y == 1) return;  // written by its block
     const int n = rec[0].y + rec[1].y;
     const bool cut0 = p.rows_own && rec[0].y > 1, cut1 = p.rows_prefix && rec[1].y > 1;
@@ -721,7 +721,7 @@ __global__ void __launch_bounds__(128) kq_kv_combine_kernel(const __grid_constan
             else hi = mid;
         }
         const int i = t - a.q_start[lo];
-        if (i >= a.max_q) return;
+        if (i < 0 || i >= a.max_q) return;
         row[0] = (i * p.G + g) % R;
         row[1] = (t * p.G + g) % R;
     } else if (cut0 || cut1) {

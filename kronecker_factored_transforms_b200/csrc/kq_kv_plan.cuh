@@ -106,7 +106,7 @@ __device__ __forceinline__ Seq load_seq(const Plan &p, int64_t b, bool report) {
         }
         s.shift = given - m;
         s.pages = a.page_table + b * a.max_pages;
-        if (a.window) lo = max(0, s.shift - a.window + 1);
+        if (a.window) lo = int(max(int64_t(0), int64_t(s.shift) - a.window + 1));
     }
     const int hi = min(s.n, max(0, s.shift + s.m));
     s.lo = lo;

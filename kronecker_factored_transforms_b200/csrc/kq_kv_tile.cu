@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
     const int first = tile * T_ROWS / p.G, last = (tile * T_ROWS + max(rows, 1) - 1) / p.G;  // queries
     // keys that some row of the tile sees
     int hi = min(s.n, max(0, s.shift + last + 1)), lo = 0;
-    if (a.window && !prefix) lo = min(max(0, s.shift + first - a.window + 1), hi);
+    if (a.window && !prefix) lo = int(min(int64_t(hi), max(int64_t(0), int64_t(s.shift) + first - a.window + 1)));
     const int c0 = lo / CH, chunks = (hi + CH - 1) / CH - c0;
     const int j0 = c0 + int(int64_t(chunks) * split / splits), j1 = c0 + int(int64_t(chunks) * (split + 1) / splits);
     const int N = j1 - j0;  // chunks of this block
@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
 #pragma unroll
                     for (int i = 0; i < W; ++i) w.k[i] = k[i], w.v[i] = v[i];
                     w.ks = a.c.k_scale[row] * factor;
-                    w.vs = a.c.v_scale[row];
+                    w.vs = fminf(a.c.v_scale[row], 0x1.fffffep127f);  // a weight of 0 leaves any row out
                 } else {
                     w.ks = -INFINITY;  // no such page: the mark by which the softmax leaves the key out
                     atomicOr(a.err, kSiteKvAttention);

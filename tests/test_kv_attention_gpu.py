@@ -149,6 +149,36 @@ def test_windows(kq, window):
     verify(kq, make([150, 900], [150, 200], 4, 2, 128, 16, window), window=window)
 
 
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 100])
+@pytest.mark.parametrize("prefix", [0, 300])
+def test_the_largest_windows(kq, window, prefix):
+    """More queries than keys: a query's place less the window passes 32 bits."""
+    verify(kq, make([2, 0, 40], [5, 3, 1], 4, 2, 64, 16, 21, prefix=prefix), window=window)
+    verify(kq, make([100, 5], [150, 70], 4, 2, 64, 16, 22, prefix=prefix), window=window)
+
+
+@pytest.mark.parametrize("prefix", [0, 300])
+def test_more_sequences_than_tokens(kq, prefix):
+    """Idle slots of a batch that bring no query."""
+    verify(kq, make([40, 7, 0, 300, 5, 9], [0, 1, 0, 0, 1, 0], 4, 2, 128, 16, 23, prefix=prefix))
+    verify(kq, make([40] * 90, [0] * 70 + [60] + [0] * 19, 4, 2, 128, 16, 24, prefix=prefix))
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+@pytest.mark.parametrize("m,softcap", [(4, 0.0), (80, 0.0), (80, 20.0)])
+def test_scales_of_rows_that_a_query_does_not_see(kq, bad, m, softcap):
+    """A key that only the last query sees, and one before every window, do not reach the others."""
+    keys, window = 300, 100
+    s = make([keys], [m], 4, 2, 128, 16, 25)
+    for t in (keys - 1, keys - m - window):
+        for pool in (s["pool"][1], s["pool"][3]):
+            pool[s["tables"][0][t // 16], :, t % 16] = bad
+    out, lse = launch(kq, s, softcap, window)
+    ref = attention(s["q"][:m], s["pool"], s["tables"], [keys], [m], s["scale"], softcap, window)
+    check_attention(out[:m - 1], lse[:m - 1], [r[:m - 1] for r in ref])
+    assert kq.kq_device_error() == 0
+
+
 @pytest.mark.parametrize("nqs", [[1, 1, 3], [70, 90, 33]])
 def test_pages_below_the_window_are_not_looked_at(kq, nqs):
     """A sliding-window cache gives such pages back: their entries may hold anything."""
