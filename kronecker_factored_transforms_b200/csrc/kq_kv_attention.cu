@@ -708,11 +708,12 @@ __global__ void __launch_bounds__(128) kq_kv_combine_kernel(const __grid_constan
     if (p.rows_own) rec[0] = p.parts[at];
     if (p.rows_prefix) rec[1] = p.parts[rows + at];
     auto sound = [&](const int2 &r) { return r.y >= 1 && r.y <= p.ctas && r.x >= 0 && r.x <= p.ctas - r.y; };
-    if ((p.rows_own && !sound(rec[0])) || (p.rows_prefix && !sound(rec[1]))) return;  // a row past the bound on queries
+    const bool tiled = p.few && rec[0].x == -1 && rec[0].y == p.own_splits, rows_own = p.rows_own && !tiled;
+    if ((rows_own && !sound(rec[0])) || (p.rows_prefix && !sound(rec[1]))) return;  // a row past the bound on queries
     if (!p.partial && p.rows_own && rec[0].y == 1) return;  // written by its block
     const int n = rec[0].y + rec[1].y;
-    const bool cut0 = p.rows_own && rec[0].y > 1, cut1 = p.rows_prefix && rec[1].y > 1;
-    if (a.q_start && (cut0 || cut1 || !p.rows_own)) {  // the row's place in its unit's tile; whether it is bounded away
+    const bool cut0 = rows_own && rec[0].y > 1, cut1 = p.rows_prefix && rec[1].y > 1;
+    if (a.q_start && (cut0 || cut1 || !rows_own)) {  // the row's place in its unit's tile; whether it is bounded away
         const int t = int(at / H), g = int(at - int64_t(t) * H) % p.G;
         int lo = 0, hi = int(a.B);
         while (lo < hi) {
@@ -733,7 +734,7 @@ __global__ void __launch_bounds__(128) kq_kv_combine_kernel(const __grid_constan
     auto place = [&](int k, const float *&o, const float *&l) -> int64_t {
         const int u = k >= rec[0].y;
         const int i = u ? k - rec[0].y : k;
-        if (u ? !p.rows_prefix : !p.rows_own) {
+        if (u ? !p.rows_prefix : !rows_own) {
             o = p.tile_o, l = p.tile_l;
             return int64_t((u ? p.own_splits : 0) + i) * rows + at;
         }
@@ -829,7 +830,8 @@ int row_tile(int64_t rows) { return rows <= 8 ? 8 : 16; }
 // kernel, head_dim 128, 24 sequences of 100 to 4100 keys on 4 key heads: 20 rows 28 against 41, 40 rows 35
 // against 42, 64 rows 50 against 46.  A prefix on 8 key heads: 32 rows 17 against 19 (1000 keys) and 28
 // against 29 (8000), 64 rows 20 against 21 (1000) but 70 against 37 (16000).
-bool many_rows(int64_t rows) { return rows > 48; }
+constexpr int kManyRows = 48;
+bool many_rows(int64_t rows) { return rows > kManyRows; }
 bool many_prefix_rows(int64_t rows) { return rows > 32; }
 
 // Blocks to cut a unit's keys over, where there are too few units for all SMs, up to two rounds of blocks:
@@ -856,11 +858,19 @@ uint64_t lay_out(Plan &p, unsigned char *base, int64_t T, int64_t B, int H, int 
     const int G = H / Hk;
     p.G = G;
     const bool own_tile = many_rows(int64_t(max_q) * G), pre_tile = own_tile || many_prefix_rows(T * G);
-    const int own = own_tile ? most_splits(kv_tiles(max_q, G) * B * Hk) : 0;
+    // Sequences that are far from even, as prompts and single tokens at once: those with few rows are the row
+    // kernel's.  (8 key heads of 4, us with both kernels against the tile kernel alone: 1024 queries of one
+    // sequence and 63 single ones on 2000 keys each 129 against 203, 512 and 255 on 1000 155 against 368, 1024
+    // and 15 on 2000 86 against 84.)  Of the others, the units to expect:
+    p.few = own_tile && T * 5 < B * max_q * 3 ? kManyRows : 0;
+    const int64_t places = kv_own_tiles(T, B, max_q, G, p.few);
+    const int64_t expect = kv_tiles(max_q, G) + kv_own_tiles(T - max_q, B - 1, max_q, G, p.few);
+    const int64_t own_units = (expect < places ? expect : places) * Hk;
+    const int own = own_tile ? most_splits(own_units) : 0;
     const int pre = pre_tile ? most_splits(kv_tiles(T, G) * Hk) : 0;
-    p.own_splits = own_tile ? tile_splits(kv_tiles(max_q, G) * B * Hk, own_most) : 0;
+    p.own_splits = own_tile ? tile_splits(own_units, own_most) : 0;
     p.pre_splits = pre_most && pre_tile ? tile_splits(kv_tiles(T, G) * Hk, pre_most) : 0;
-    p.rows_own = !own_tile;
+    p.rows_own = !own_tile || p.few;
     p.rows_prefix = pre_most && !pre_tile;
     p.partial = pre_most > 0;
     const int R = row_tile(int64_t(max_q) * G);
@@ -872,10 +882,10 @@ uint64_t lay_out(Plan &p, unsigned char *base, int64_t T, int64_t B, int H, int 
         return r;
     };
     p.parts = reinterpret_cast<int2 *>(take(rows * 2 * 8));
-    p.slot_o = reinterpret_cast<float *>(take(own_tile ? 0 : uint64_t(kMaxCtas) * 2 * R * D * 4));
-    p.slot_l = reinterpret_cast<float *>(take(own_tile ? 0 : uint64_t(kMaxCtas) * 2 * R * 4));
-    p.whole_o = reinterpret_cast<float *>(take(own_tile ? 0 : rows * 2 * D * 4));
-    p.whole_l = reinterpret_cast<float *>(take(own_tile ? 0 : rows * 2 * 4));
+    p.slot_o = reinterpret_cast<float *>(take(!p.rows_own ? 0 : uint64_t(kMaxCtas) * 2 * R * D * 4));
+    p.slot_l = reinterpret_cast<float *>(take(!p.rows_own ? 0 : uint64_t(kMaxCtas) * 2 * R * 4));
+    p.whole_o = reinterpret_cast<float *>(take(!p.rows_own ? 0 : rows * 2 * D * 4));
+    p.whole_l = reinterpret_cast<float *>(take(!p.rows_own ? 0 : rows * 2 * 4));
     p.tile_o = reinterpret_cast<float *>(take(uint64_t(own + pre) * rows * D * 4));
     p.tile_l = reinterpret_cast<float *>(take(uint64_t(own + pre) * rows * 4));
     return at;
@@ -907,11 +917,10 @@ template <int D, int NT>
 cudaError_t launch_all(Plan &p, int num_sms, int device, cudaStream_t stream) {
     cudaError_t e = cudaSuccess;
     p.ctas = 0;
-    if (p.rows_own)
+    if (p.own_splits) e = launch_kv_tile(p, false, p.own_splits, device, stream);
+    if (e == cudaSuccess && p.rows_own)
         e = p.a.softcap > 0.0f ? launch_rows<D, NT, true>(p, num_sms, device, stream)
                                : launch_rows<D, NT, false>(p, num_sms, device, stream);
-    else
-        e = launch_kv_tile(p, false, p.own_splits, device, stream);
     if (e == cudaSuccess && p.pre_splits) e = launch_kv_tile(p, true, p.pre_splits, device, stream);
     if (e != cudaSuccess || (!p.rows_own && !p.partial && p.own_splits == 1)) return e;
     return launch_combine<D, 8 * NT>(p, stream);

@@ -11,7 +11,8 @@
 namespace kq {
 namespace kv {
 
-constexpr int CH = 128;  // keys per chunk
+constexpr int CH = 128;         // keys per chunk
+constexpr int kTileRows = 256;  // rows of a block of the tile kernel
 enum : unsigned { kSiteKvWait = 262144u };
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -39,15 +40,19 @@ __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile
 
 // The launch as its kernels see it.  "Sequence" B, where there is a shared prefix,
 // is the prefix with the queries of all sequences.  Own keys and the prefix's are each
-// the row kernel's or the tile kernel's.
+// the row kernel's or the tile kernel's; own keys of a batch whose sequences differ much in
+// their queries (prompts and single tokens at once) are both's: a sequence with up to `few`
+// rows per key head is the row kernel's.
 struct Plan {
     KvAttnArgs a;
     int G;             // query heads per key head
     int partial;       // a prefix is there: every kernel's rows are parts, joined at the end
-    int rows_own, rows_prefix;   // the row kernel has the own keys, the prefix's
+    int rows_own, rows_prefix;   // the row kernel has own keys, the prefix's
+    int few;           // where both kernels have own keys: the most rows of a sequence of the row kernel; else 0
     int own_splits, pre_splits;  // the tile kernel's parts of a row, of own keys and of the prefix's (0: not its)
     int ctas;          // blocks of the row kernel
-    int2 *parts;       // [2][T * H] for every row: the first block that has keys of it, and how many have
+    int2 *parts;       // [2][T * H] for every row of the row kernel: the first block that has keys of it, and how
+                       // many have; with `few`, -1 and own_splits for one of the tile kernel
     float *slot_o;     // [ctas][2][R][D] partial rows: a block's first unit, its last unit
     float *slot_l;     // [ctas][2][R]
     float *whole_o;    // [2][T * H][D] rows whose keys lay in one block (own keys; the prefix's)
@@ -108,6 +113,8 @@ __device__ __forceinline__ Seq load_seq(const Plan &p, int64_t b, bool report) {
         s.pages = a.page_table + b * a.max_pages;
         if (a.window) lo = int(max(int64_t(0), int64_t(s.shift) - a.window + 1));
     }
+    // the other kernel's: no rows here
+    if (p.few && b != a.B && (s.m * p.G > p.few) != (R == kTileRows)) s.m = 0;
     const int hi = min(s.n, max(0, s.shift + s.m));
     s.lo = lo;
     s.c0 = min(lo, max(hi - 1, 0)) / CH;
@@ -132,7 +139,18 @@ __device__ __forceinline__ int query_shift(const KvAttnArgs &a, int t) {
 }  // namespace kv
 
 // Row tiles (256 rows of a key head) of m queries with G heads each.
-inline int64_t kv_tiles(int64_t m, int G) { return (m * G + 255) / 256; }
+inline int64_t kv_tiles(int64_t m, int G) { return (m * G + kv::kTileRows - 1) / kv::kTileRows; }
+// The own keys' row tiles have places, per key head, of which a sequence's first lies at own_place of its first
+// query: no two sequences' meet, as a part of r rows has at most r / 256 + 1 tiles and, beside a row kernel, more
+// than `few` rows.  T tokens have own_place(T, B) at most.
+__host__ __device__ inline int64_t own_place(int64_t q, int64_t b, int G, int few) {
+    return q * G / kv::kTileRows + (G <= few ? q * G / (few + 1) : b);
+}
+// Places to launch: those, or what all sequences have at the bound of queries.
+inline int64_t kv_own_tiles(int64_t T, int64_t B, int max_q, int G, int few) {
+    const int64_t full = kv_tiles(max_q, G) * B, any = own_place(T, B, G, few);
+    return full < any ? full : any;
+}
 // The tile kernel over the own keys of all sequences, or over the prefix.
 cudaError_t launch_kv_tile(const kv::Plan &p, bool prefix, int splits, int device, cudaStream_t stream);
 

@@ -25,6 +25,7 @@
 // Keys that a row does not see, past its place or out of its window, are looked at only
 // in the chunks where a warp's rows have any; those scores go through TMEM once more.
 //
+// The grid has a place for every tile that the tokens could have; a sequence's tiles are found in the block.
 // One unit = 256 rows of a key head and sequence, cut over `splits` blocks along its keys
 // where there are fewer units than SMs; partial rows then go to the workspace for
 // kq_kv_combine_kernel.
@@ -39,7 +40,6 @@ using namespace kv;
 using namespace tc;
 
 constexpr int T_THREADS = 416;  // two warpgroups of softmax, one of codes, a warp of MMAs
-constexpr int T_ROWS = 256;
 
 template <int D>
 struct TCfg {
@@ -139,7 +139,7 @@ __device__ __forceinline__ uint32_t operand_place(int r, int u) {
 
 template <int D, bool CAP>
 __global__ void __launch_bounds__(T_THREADS, 1)
-    kq_kv_tile_kernel(const __grid_constant__ Plan p, int prefix, int splits, int tiles, int units_b) {
+    kq_kv_tile_kernel(const __grid_constant__ Plan p, int prefix, int splits, int own_tiles) {
     using C = TCfg<D>;
     extern __shared__ __align__(1024) unsigned char t_raw[];
     const uint32_t raw_addr = smem_u32(t_raw), sbase = (raw_addr + 1023u) & ~1023u;
@@ -176,22 +176,49 @@ __global__ void __launch_bounds__(T_THREADS, 1)
     int u = id / splits;
     const int h = u % Hk;
     u /= Hk;
-    // The longest units first: sequences by falling length (up to 32 of them), and the last rows of a chunk,
-    // which see the most keys, before its first.
-    int64_t b = prefix ? a.B : u / tiles;
-    if (!prefix && units_b <= 32) {
-        const int len = lane < units_b ? a.kv_len[lane] : INT_MIN;
-        int rank = 0;
-        for (int k = 0; k < units_b; ++k) {
-            const int other = __shfl_sync(0xffffffffu, len, k);
-            rank += other > len || (other == len && k < lane);
+    int64_t b = a.B;
+    bool none = false;
+    if (!prefix && a.B <= 32) {
+        // The longest units first: sequences by falling length, each with the tiles that it has.
+        int len = INT_MIN, has = 0;
+        if (lane < a.B) {
+            len = a.kv_len[lane];
+            has = load_seq<kTileRows>(p, lane, false).tiles;
         }
-        b = __ffs(__ballot_sync(0xffffffffu, lane < units_b && rank == int(b))) - 1;
+        int before = 0;
+        for (int k = 0; k < int(a.B); ++k) {
+            const int other = __shfl_sync(0xffffffffu, len, k), its = __shfl_sync(0xffffffffu, has, k);
+            if (other > len || (other == len && k < lane)) before += its;
+        }
+        const uint32_t at = __ballot_sync(0xffffffffu, before <= u && u < before + has);
+        none = at == 0;
+        b = none ? 0 : __ffs(at) - 1;
+        u -= __shfl_sync(0xffffffffu, before, int(b));
+    } else if (!prefix && own_tiles) {
+        b = u / own_tiles;
+        u -= int(b) * own_tiles;
+    } else if (!prefix) {
+        // the last sequence whose place is at or before u, 32 looked at in a step
+        auto begin = [&](int64_t k) {
+            int q0, m;
+            queries_of(a, k, q0, m);
+            return own_place(q0, k, p.G, p.few);
+        };
+        int64_t lo = 0, hi = a.B;
+        while (hi - lo > 1) {
+            const int64_t step = (hi - lo + 31) / 32, k = lo + lane * step;
+            const int n = max(1, __popc(__ballot_sync(0xffffffffu, k < hi && begin(k) <= u)));
+            lo += (n - 1) * step;
+            hi = min(hi, lo + step);
+        }
+        b = lo;
+        u = int(max(int64_t(0), u - begin(b)));
     }
-    const int tile = tiles - 1 - u % tiles;
-    const Seq s = load_seq<T_ROWS>(p, b, tile == 0 && h == 0 && split == 0 && tid == 0 && !prefix);
-    const int rows = min(T_ROWS, s.m * p.G - tile * T_ROWS);
-    const int first = tile * T_ROWS / p.G, last = (tile * T_ROWS + max(rows, 1) - 1) / p.G;  // queries
+    const Seq s = load_seq<kTileRows>(p, b, u == 0 && h == 0 && split == 0 && tid == 0 && !prefix);
+    none |= u >= s.tiles;
+    const int tile = none ? 0 : s.tiles - 1 - u;  // the last rows of a chunk, which see the most keys, before its first
+    const int rows = none ? 0 : min(kTileRows, s.m * p.G - tile * kTileRows);
+    const int first = tile * kTileRows / p.G, last = (tile * kTileRows + max(rows, 1) - 1) / p.G;  // queries
     // keys that some row of the tile sees
     int hi = min(s.n, max(0, s.shift + last + 1)), lo = 0;
     if (a.window && !prefix) lo = int(min(int64_t(hi), max(int64_t(0), int64_t(s.shift) + first - a.window + 1)));
@@ -208,7 +235,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
     // ---- queries: bf16 rows as operands; rows past the last are zeros ----
     if (wg < 2) {
         // a warp brings 32 rows, whole rows side by side: a lane 16 bytes of 256 / D rows a step
-        const int r = tid & 127, j = tile * T_ROWS + 128 * wg + r;
+        const int r = tid & 127, j = tile * kTileRows + 128 * wg + r;
         const bool real = 128 * wg + r < rows;
         const int i = real ? j / p.G : 0;
         const uint16_t *mine = real ? a.q + (int64_t(s.q0 + i) * H + h * p.G + (j - i * p.G)) * D : nullptr;
@@ -234,7 +261,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         // no such rows (a bound on them sized the grid)
     } else if (wg < 2) {
         // ---------------- softmax: a row per thread ----------------
-        const int r = tid & 127, jr = 128 * wg + r, j = tile * T_ROWS + jr;
+        const int r = tid & 127, jr = 128 * wg + r, j = tile * kTileRows + jr;
         const bool real = jr < rows;
         const int i = real ? j / p.G : 0;
         int row_lo = 0, row_hi = 0;  // keys that the row sees
@@ -515,6 +542,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
                 __syncwarp();
             }
             if (real) {
+                if (p.few && !prefix && split == 0) p.parts[at] = make_int2(-1, splits);
                 if (!final) p.tile_l[(int64_t(prefix ? p.own_splits : 0) + split) * a.T * H + at] = lse;
                 else if (a.lse) a.lse[at] = lse * 0.6931471805599453f;
             }
@@ -663,11 +691,13 @@ cudaError_t launch_inst(const Plan &p, bool prefix, int splits, int device, cuda
         attr_err[device] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     });
     if (attr_err[device] != cudaSuccess) return attr_err[device];
-    const int64_t tiles = kv_tiles(prefix ? p.a.T : p.a.max_q, p.G), units_b = prefix ? 1 : p.a.B;
-    const int64_t grid = tiles * units_b * p.a.c.heads * splits;
+    // where that is no more, every sequence has the places of one at the bound of queries: own_tiles
+    const int64_t full = kv_tiles(p.a.max_q, p.G);
+    const int64_t tiles = prefix ? kv_tiles(p.a.T, p.G) : kv_own_tiles(p.a.T, p.a.B, p.a.max_q, p.G, p.few);
+    const int64_t grid = tiles * p.a.c.heads * splits;
     if (grid >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-    return launch_overlapped(kern, unsigned(grid), T_THREADS, C::SMEM, stream, p, int(prefix), splits, int(tiles),
-                             int(units_b));
+    return launch_overlapped(kern, unsigned(grid), T_THREADS, C::SMEM, stream, p, int(prefix), splits,
+                             int(tiles == full * p.a.B ? full : 0));
 }
 
 }  // namespace

@@ -136,6 +136,30 @@ def test_chunks_of_prompts(kq, D, G, nqs, keys):
     verify(kq, make(keys, nqs, G, 2, D, 16, 10 * G + D + 1))
 
 
+def spread(keys, nqs):
+    """As many keys as queries at least, and more for some."""
+    return [max(m, (keys * (i % 5)) // 4 + i) for i, m in enumerate(nqs)]
+
+
+@pytest.mark.parametrize("D,G,nqs,keys,kw", [
+    (128, 4, [1, 1, 200, 1, 2], 400, {}), (64, 4, [12, 13, 1, 0, 1, 100, 1, 1], 300, {}),
+    (128, 4, [1] * 40 + [90] + [1] * 10, 700, {}), (64, 8, [3, 0, 7, 6, 1] * 9 + [300], 500, dict(window=60)),
+    (128, 2, [1, 600, 1, 1], 9000, dict(softcap=8.0)), (128, 4, [1] * 30 + [150, 20] + [1] * 30, 500, dict(prefix=333)),
+    (64, 50, [1] * 20 + [8] + [1] * 20, 200, {}), (128, 4, [100] + [61] * 35, 150, {}),
+    (64, 1, [49] + [48, 1, 1, 1] * 12, 100, dict(prefix=50, window=90))])
+def test_prompts_and_single_tokens_at_once(kq, D, G, nqs, keys, kw):
+    """Sequences with few rows and with many, each for its own kernel."""
+    kw = dict(kw)
+    s = make(spread(keys, nqs), nqs, G, 2, D, 16, len(nqs) + G, prefix=kw.pop("prefix", 0))
+    verify(kq, s, **kw)
+    verify(kq, s, max_q=max(nqs) + 37, **kw)
+
+
+def test_single_tokens_under_a_high_bound(kq):
+    nqs = [1] * 70
+    verify(kq, make(spread(600, nqs), nqs, 4, 2, 128, 16, 31), max_q=4096)
+
+
 @pytest.mark.parametrize("nqs,keys", [([4, 3], [2, 0]), ([1, 20], [0, 5]), ([200], [150]), ([64, 64], [0, 1])])
 def test_more_queries_than_keys(kq, nqs, keys):
     """The first queries see nothing: zeros and -infinity."""
@@ -289,6 +313,25 @@ def test_refused_indexes_are_masked(kq, nqs):
     out, _ = launch(kq, s)
     torch.cuda.synchronize()
     assert kq.kq_device_error() == 131072 and torch.isfinite(out[:s["T"]].float()).all()
+
+
+def test_queries_past_the_bound_stay_beside_single_tokens(kq):
+    nqs = [1, 300, 1, 1, 1, 90]
+    s = make(spread(400, nqs), nqs, 4, 2, 128, 16, 32)
+    T, H = s["T"] + 3, 8
+    out = torch.full((T, H, 128), 5.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T, H), 6.0, device="cuda")
+    n = kq.kq_kv_attention_workspace_bytes(T, 6, H, 2, 128, 120)
+    ws = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
+    kq.kq_kv_attention(kq.kv_cache(*s["pool"]), s["q"], s["q_start"], s["table"], s["width"], s["kv_len"], s["scale"],
+                       0.0, 0, out, lse, ws, n, T, 6, H, 120)
+    torch.cuda.synchronize()
+    assert kq.kq_device_error() == 131072
+    ref = attention(s["q"][:s["T"]], s["pool"], s["tables"], s["keys"], nqs, s["scale"])
+    done = torch.ones(T, dtype=torch.bool)
+    done[1 + 120:1 + 300] = done[s["T"]:] = False
+    assert (out[~done] == 5.0).all() and (lse[~done] == 6.0).all()
+    check_attention(out[done], lse[done], [r[done[:s["T"]]] for r in ref])
 
 
 def test_queries_past_the_bound_stay(kq):
