@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
         *s_abort = 0;
         fence_mbar_init();
     }
-    griddep_wait();
+    begin_launch(p);
     griddep_launch_dependents();
 
     // ---- the block's share: chunks [w0, w1) of all ----
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
         if (w < warp) before += scan[w];
         total += scan[w];
     }
-    if (blockIdx.x >= total) return;
+    if (blockIdx.x >= total) return end_launch(p);
     const Shares sh(total, p.ctas);
     const int64_t w0 = sh.begin(blockIdx.x), w1 = sh.begin(blockIdx.x + 1);
     __syncthreads();
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
         scan[3] = w0 + (c < 0 ? -c : 0);
     }
     __syncthreads();
-    if (scan[3] >= w1) return;  // places of a unit's start alone
+    if (scan[3] >= w1) return end_launch(p);  // places of a unit's start alone
 
     if (warp == WARPS) {
         // ---------------- the loading warp: one chunk per stage, 16 bytes a lane and copy ----------------
@@ -684,6 +684,7 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::EMPTY + rg.idx));
     }
+    end_launch(p);
 }
 
 // ---- joining partial rows ---------------------------------------------------------
@@ -917,10 +918,16 @@ template <int D, int NT>
 cudaError_t launch_all(Plan &p, int num_sms, int device, cudaStream_t stream) {
     cudaError_t e = cudaSuccess;
     p.ctas = 0;
-    if (p.own_splits) e = launch_kv_tile(p, false, p.own_splits, device, stream);
-    if (e == cudaSuccess && p.rows_own)
+    p.later = 0;
+    if (p.own_splits) {
+        e = launch_kv_tile(p, false, p.own_splits, device, stream);
+        p.later = 1;
+    }
+    if (e == cudaSuccess && p.rows_own) {
         e = p.a.softcap > 0.0f ? launch_rows<D, NT, true>(p, num_sms, device, stream)
                                : launch_rows<D, NT, false>(p, num_sms, device, stream);
+        p.later = 1;
+    }
     if (e == cudaSuccess && p.pre_splits) e = launch_kv_tile(p, true, p.pre_splits, device, stream);
     if (e != cudaSuccess || (!p.rows_own && !p.partial && p.own_splits == 1)) return e;
     return launch_combine<D, 8 * NT>(p, stream);

@@ -51,6 +51,7 @@ struct Plan {
     int few;           // where both kernels have own keys: the most rows of a sequence of the row kernel; else 0
     int own_splits, pre_splits;  // the tile kernel's parts of a row, of own keys and of the prefix's (0: not its)
     int ctas;          // blocks of the row kernel
+    int later;         // this launch follows another of the same call (see begin_launch)
     int2 *parts;       // [2][T * H] for every row of the row kernel: the first block that has keys of it, and how
                        // many have; with `few`, -1 and own_splits for one of the tile kernel
     float *slot_o;     // [ctas][2][R][D] partial rows: a block's first unit, its last unit
@@ -71,6 +72,18 @@ struct Seq {
     int tiles;     // row tiles
     const int32_t *pages;
 };
+
+// The row and tile kernels of one call need nothing of one another, so a later one of them does not wait for the
+// one before but for its end: its blocks start as the other's give up their SMs.  What they both read was complete
+// when the first one's blocks passed their wait, and they let a later launch begin only after it.  The last
+// one's end is then the end of all.  (A prefix of 6007 keys behind the own keys of 200 sequences: 90 -> 85 us.)
+__device__ __forceinline__ void begin_launch(const Plan &p) {
+    if (p.later) __threadfence();
+    else griddep_wait();
+}
+__device__ __forceinline__ void end_launch(const Plan &p) {
+    if (p.later) griddep_wait();
+}
 
 // First query token and number of queries of sequence b, within the T tokens whatever q_start holds.
 __device__ __forceinline__ void queries_of(const KvAttnArgs &a, int64_t b, int &q0, int &m) {

@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         tmem_alloc(sbase + C::OFF_MISC, 512);
         tmem_relinquish();
     }
-    griddep_wait();
+    begin_launch(p);
 
     // ---- the block's unit: rows, and its part of their keys ----
     const int id = int(blockIdx.x), split = id % splits;
@@ -678,6 +678,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+    end_launch(p);
 }
 
 template <int D, bool CAP>
