@@ -178,7 +178,7 @@ __device__ __forceinline__ void rotated_row(const unsigned char *xrow, const flo
     const uint4 *x = reinterpret_cast<const uint4 *>(xrow);
     const int half = rope_dim >> 1;
     if (inter) {
-        for (int i = 8 * which; i < rope_dim; i += 16) {
+        auto eight = [&](int i) {
             float v[8];
             unpack8(x[i >> 3], v);
             const float4 c = __ldg(reinterpret_cast<const float4 *>(cs + (i >> 1)));
@@ -191,7 +191,13 @@ __device__ __forceinline__ void rotated_row(const unsigned char *xrow, const flo
                 v[2 * e + 1] = fmaf(b, cc[e], a * ss[e]);
             }
             put(i, v);
+        };
+        if (rope_dim == D) {  // the usual case, unrolled so that the table's loads run ahead
+#pragma unroll
+            for (int i = 0; i < D; i += 16) eight(i + 8 * which);
+            return;
         }
+        for (int i = 8 * which; i < rope_dim; i += 16) eight(i);
     } else {
         auto eight = [&](int i) {
             float a[8], b[8];
@@ -216,7 +222,7 @@ __device__ __forceinline__ void rotated_row(const unsigned char *xrow, const flo
             put(i, a);
             put(i + half, b);
         };
-        if (rope_dim == D) {  // the usual case, unrolled so that the table's loads run ahead
+        if (rope_dim == D) {
 #pragma unroll
             for (int i = 0; i < D / 2; i += 16) eight(i + 8 * which);
             return;
@@ -629,10 +635,13 @@ static cudaError_t launch_append_inst(const KvAppendArgs &a, int num_sms, int de
     });
     if (attr_err[device] != cudaSuccess) return attr_err[device];
     // Blocks for each kind: one more at a time to the kind whose blocks have the most to do.  A tile of keys
-    // takes about 1.6 times, one of values 1.0 times what one of queries does.
+    // takes about 1.6 times, one of values 1.0 times what one of queries does, and the rotation more the fewer
+    // heads there are: a warp's rows then read as many rows of the table (65536 tokens of 8 query heads on one
+    // key head: 199 us without the terms for that, 124 with them).
     const int64_t tiles[3] = {(a.T * a.q_heads + 127) / 128, (a.T * a.c.heads + 127) / 128,
                               (a.T * a.c.heads + 127) / 128};
-    const double cost[3] = {1.0, 1.6, 1.0};
+    const double turn = double(a.rope_dim) / D;
+    const double cost[3] = {1.0 + (a.q_heads ? 0.5 * turn / a.q_heads : 0.0), 1.6 + 2.5 * turn / a.c.heads, 1.0};
     int blocks[3] = {tiles[0] > 0, 1, 1};
     for (int n = blocks[0] + 2; n < num_sms; ++n) {
         int most = -1;
