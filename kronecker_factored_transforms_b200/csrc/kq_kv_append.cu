@@ -19,8 +19,9 @@
 //   - two teams, each with 256 TMEM columns: eight warps turn rows into terms (128
 //     columns; two warps share the rows of a TMEM quarter, every second 16 bytes each),
 //     four take the fp32 rows (128 columns) while the eight are at their next tile.
-//     The keys' largest term waits for the products of the other two and takes their
-//     columns (smallest first: the tensor core truncates the sum at every addition).
+//     The keys' largest term waits, in the row's place, for the products of the other two
+//     and takes their columns (smallest first: the tensor core truncates the sum at every
+//     addition).
 //   - one block an SM, all its tiles of one kind, so that it needs one factor.
 //
 // Codes of exact arithmetic: fp32 leaves y / s uncertain by up to kBorder of its
@@ -383,25 +384,31 @@ __global__ void __launch_bounds__(A_THREADS, 1)
         const bool inter = a.rope_interleaved != 0;
         for (; tile < tiles; tile += 2 * step, ++turns) {
             const int stage = int(turns & 1u);
-            const unsigned char *x = place0 + stage * C::STAGE;
+            unsigned char *x = place0 + stage * C::STAGE;
+            auto one_term = [&] {  // what lies in the row's place
+#pragma unroll 1
+                for (int i = 0; i < D / 16; ++i) {
+                    const uint4 u = reinterpret_cast<const uint4 *>(x)[2 * i + which];
+                    tmem_st_32x32b_x4(ta + uint32_t(4 * (2 * i + which)), u.x, u.y, u.z, u.w);
+                }
+            };
             const float *cs = a.rope + int64_t(uint32_t(pos0) < uint32_t(a.rope_positions) ? pos0 : 0) * a.rope_dim;
             look(tile + 4 * step, x2, pos2);
             cp_async_wait<1>();
             named_barrier_sync(3 + pair, 256);  // the other warp's pieces
             multiplied();
             if (kind == 2) {
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    const uint4 u = reinterpret_cast<const uint4 *>(x)[2 * i + which];
-                    tmem_st_32x32b_x4(ta + uint32_t(4 * (2 * i + which)), u.x, u.y, u.z, u.w);
-                }
+                one_term();
                 multiply(1, false, true);
             } else {
-                // queries: both terms; keys: the second and third, and then the first
+                // queries: both terms; keys: the second and third, and then the first, which waits in the row's place
                 rotated_row<D>(x, cs, a.rope_dim, inter, which, [&](int i, float (&v)[8]) {
                     uint32_t w[4];
                     take_term(v, w);
-                    if (kind == 1) take_term(v, w);
+                    if (kind == 1) {
+                        *reinterpret_cast<uint4 *>(x + 2 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+                        take_term(v, w);
+                    }
                     tmem_st_32x32b_x4(ta + uint32_t(i >> 1), w[0], w[1], w[2], w[3]);
                     tmem_st_32x32b_x4(ta + 64 + uint32_t(i >> 1), pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
                                       pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
@@ -409,11 +416,7 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                 multiply(2, false, kind == 0);
                 if (kind == 1) {
                     multiplied();
-                    rotated_row<D>(x, cs, a.rope_dim, inter, which, [&](int i, float (&v)[8]) {
-                        uint32_t w[4];
-                        take_term(v, w);
-                        tmem_st_32x32b_x4(ta + uint32_t(i >> 1), w[0], w[1], w[2], w[3]);
-                    });
+                    one_term();
                     multiply(1, true, true);
                 }
             }
@@ -635,13 +638,13 @@ static cudaError_t launch_append_inst(const KvAppendArgs &a, int num_sms, int de
     });
     if (attr_err[device] != cudaSuccess) return attr_err[device];
     // Blocks for each kind: one more at a time to the kind whose blocks have the most to do.  A tile of keys
-    // takes about 1.6 times, one of values 1.0 times what one of queries does, and the rotation more the fewer
+    // takes about 1.4 times, one of values 1.0 times what one of queries does, and the rotation more the fewer
     // heads there are: a warp's rows then read as many rows of the table (65536 tokens of 8 query heads on one
-    // key head: 199 us without the terms for that, 124 with them).
+    // key head: 149 us without the terms for that, 112 with them).
     const int64_t tiles[3] = {(a.T * a.q_heads + 127) / 128, (a.T * a.c.heads + 127) / 128,
                               (a.T * a.c.heads + 127) / 128};
     const double turn = double(a.rope_dim) / D;
-    const double cost[3] = {1.0 + (a.q_heads ? 0.5 * turn / a.q_heads : 0.0), 1.6 + 2.5 * turn / a.c.heads, 1.0};
+    const double cost[3] = {1.0 + (a.q_heads ? 0.5 * turn / a.q_heads : 0.0), 1.4 + 1.5 * turn / a.c.heads, 1.0};
     int blocks[3] = {tiles[0] > 0, 1, 1};
     for (int n = blocks[0] + 2; n < num_sms; ++n) {
         int most = -1;
