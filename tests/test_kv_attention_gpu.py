@@ -226,6 +226,20 @@ def test_scores_far_apart(kq):
         verify(kq, s)
 
 
+@pytest.mark.parametrize("softcap", [0.0, 150.0])
+@pytest.mark.parametrize("nqs", [[1, 3], [70, 150], [2, 150]])
+def test_scores_that_jump_on_the_way(kq, nqs, softcap):
+    """Key scales that rise, or fall, by magnitudes inside a chunk of 128 keys and between chunks: the largest score so
+    far is passed by hundreds, late in a long row."""
+    steps = [(0, 1e-3), (300, 0.05), (555, 3.0), (640, 0.2), (1000, 12.0), (1663, 40.0)]
+    for turn in (steps, [(t, f) for (t, _), (_, f) in zip(steps, steps[::-1])]):
+        s = make([2100, 1700], nqs, 4, 2, 128, 16, 18)
+        for b, n in enumerate(s["keys"]):
+            for t in range(n):
+                s["pool"][1][s["tables"][b][t // 16], :, t % 16] *= [f for at, f in turn if at <= t][-1]
+        verify(kq, s, softcap=softcap)
+
+
 @pytest.mark.parametrize("mid", [1e-12, 1e-4, 1e3, 1e8])
 def test_value_scales_of_any_size(kq, mid):
     s = make([300, 20, 1], [1, 1, 1], 4, 2, 128, 16, 9)
@@ -395,7 +409,9 @@ def test_refused_prefix_pages(kq):
 # ---- streams, graphs, order -----------------------------------------------------------
 
 CASES = [dict(keys=[900, 33, 0, 410], nqs=[1] * 4, prefix=0), dict(keys=[700, 300], nqs=[90, 150], prefix=0),
-         dict(keys=[20, 33, 0, 300] * 10, nqs=[1] * 40, prefix=600)]
+         dict(keys=[20, 33, 0, 300] * 10, nqs=[1] * 40, prefix=600),
+         dict(keys=[20, 700, 33, 300, 64], nqs=[1, 90, 1, 7, 2], prefix=0),
+         dict(keys=[20, 700, 33, 300, 64], nqs=[1, 90, 1, 7, 2], prefix=200)]
 
 
 @pytest.mark.parametrize("case", CASES)
@@ -405,6 +421,26 @@ def test_same_inputs_same_bits(kq, case):
     for _ in range(20):
         again = launch(kq, s)
         assert torch.equal(first[0][:s["T"]], again[0][:s["T"]]) and torch.equal(first[1], again[1])
+
+
+def test_calls_in_a_row_on_one_workspace(kq):
+    """Different batches one behind another, nothing between them: no call meets what another left."""
+    sets = [make(G=8, Hk=2, D=128, page=16, seed=40 + i, **case) for i, case in enumerate(CASES)]
+    alone = [[t.clone() for t in launch(kq, s)] for s in sets]
+    torch.cuda.synchronize()
+    most = max(kq.kq_kv_attention_workspace_bytes(s["T"] + 3, s["B"], 16, 2, 128, max(s["nqs"])) for s in sets)
+    ws = torch.full((most,), 0xFF, dtype=torch.uint8, device="cuda")
+    order = [(i * 7 + i // 5) % len(sets) for i in range(60)]
+    outs = [torch.full_like(alone[i][0], 5.0) for i in order]
+    for s in sets:
+        launch(kq, s)  # handles made, kernels loaded
+    torch.cuda.synchronize()
+    for i, o in zip(order, outs):
+        launch(kq, sets[i], lse=False, out=o, workspace=ws)
+    torch.cuda.synchronize()
+    for i, o in zip(order, outs):
+        assert torch.equal(o, alone[i][0]), i
+    assert kq.kq_device_error() == 0
 
 
 @pytest.mark.parametrize("case", CASES)
