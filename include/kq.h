@@ -407,7 +407,8 @@ kq_status kq_kv_gather(const kq_kv_cache *cache, const int64_t *slots, uint16_t 
  * grow between replays of a captured graph.
  * Returns KQ_ERR_SHAPE, KQ_ERR_UNSUPPORTED (head_dim, page_size), KQ_ERR_NULL,
  * KQ_ERR_ALIGN, KQ_ERR_ARG (scale, softcap, window, max_q, workspace too small,
- * overlapping buffers), KQ_ERR_CUDA.  Asynchronous on `stream`.
+ * overlapping buffers), KQ_ERR_CUDA.  Asynchronous on `stream`; allocates nothing.
+ * As every entry, it works on the current device, which the buffers must lie on.
  */
 kq_status kq_kv_attention(const kq_kv_cache *cache, const uint16_t *q, const int32_t *q_start,
                           const int32_t *page_table, int64_t max_pages, const int32_t *kv_len, float scale,

