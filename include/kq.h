@@ -387,6 +387,7 @@ kq_status kq_kv_gather(const kq_kv_cache *cache, const int64_t *slots, uint16_t 
  *             query sees are read (the rest may hold anything).
  * kv_len      [B] device int32 (below 0 counts as 0).
  * scale       finite; softcap finite and >= 0 (0: none); window >= 0 (0: none).
+ *             1.5 scale, 1.5 softcap and scale / softcap are finite too.
  * out         [T, q_heads, head_dim] device bf16, 16-byte aligned, written.
  * lse         [T, q_heads] device fp32, written, or NULL.
  * workspace   device scratch of kq_kv_attention_workspace_bytes(...) bytes,

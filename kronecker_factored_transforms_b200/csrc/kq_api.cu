@@ -509,6 +509,10 @@ kq_status kv_attention(const kq_kv_cache *cache, const uint16_t *q, const int32_
         return KQ_ERR_SHAPE;
     if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.0f || window < 0 || max_q < 1)
         return KQ_ERR_ARG;
+    // what the kernels multiply by: scale log2(e), scale / softcap and softcap log2(e)
+    if (!std::isfinite(scale * 1.5f) || !std::isfinite(softcap * 1.5f) ||
+        (softcap > 0.0f && !std::isfinite(scale / softcap)))
+        return KQ_ERR_ARG;
     if (!q || !page_table || !kv_len || !out || !workspace || (prefix_len > 0 && !prefix_pages)) return KQ_ERR_NULL;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16) || !aligned(page_table, 4) ||
         !aligned(kv_len, 4) || (q_start && !aligned(q_start, 4)) || (lse && !aligned(lse, 4)) ||

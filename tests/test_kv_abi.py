@@ -119,7 +119,8 @@ def attend(kq, c=None, shared=False, no_cache=False, **kw):
 @pytest.mark.parametrize("kw,status", [
     (dict(T=-1), "SHAPE"), (dict(B=-1), "SHAPE"), (dict(H=0), "SHAPE"), (dict(H=7), "SHAPE"), (dict(H=1026), "SHAPE"),
     (dict(B=65536), "SHAPE"), (dict(qs=None), "SHAPE"), (dict(pages=0), "SHAPE"), (dict(pages=2 ** 27), "SHAPE"),
-    (dict(T=2 ** 29, B=1), "SHAPE"), (dict(scale=math.inf), "ARG"), (dict(scale=math.nan), "ARG"),
+    (dict(T=2 ** 29, B=1), "SHAPE"), (dict(scale=math.inf), "ARG"), (dict(scale=math.nan), "ARG"), (dict(scale=3e38), "ARG"), (dict(cap=3e38), "ARG"),
+    (dict(scale=1.0, cap=1e-39), "ARG"),
     (dict(cap=-1.0), "ARG"), (dict(cap=math.inf), "ARG"), (dict(window=-1), "ARG"), (dict(max_q=0), "ARG"),
     (dict(q=None), "NULL"), (dict(tab=None), "NULL"), (dict(len=None), "NULL"), (dict(out=None), "NULL"),
     (dict(ws=None), "NULL"), (dict(q=Q + 8), "ALIGN"), (dict(out=OUT + 2), "ALIGN"), (dict(ws=WS + 8), "ALIGN"),

@@ -136,6 +136,18 @@ def test_chunks_of_prompts(kq, D, G, nqs, keys):
     verify(kq, make(keys, nqs, G, 2, D, 16, 10 * G + D + 1))
 
 
+@pytest.mark.parametrize("page", [32, 64, 128, 256])
+def test_chunks_on_pages_of_any_size(kq, page):
+    verify(kq, make([700, 90, 257], [70, 90, 1], 4, 2, 128, page, page))
+    verify(kq, make([700, 90, 257], [70, 90, 100], 2, 3, 64, page, page + 1, prefix=301), window=200)
+
+
+@pytest.mark.parametrize("G,nqs,keys", [(1024, [1, 1], [300, 17]), (128, [1, 3, 1], [129, 300, 1]), (49, [1], [700])])
+def test_one_key_head_of_many_query_heads(kq, G, nqs, keys):
+    verify(kq, make(keys, nqs, G, 1, 128, 16, G))
+    verify(kq, make(keys, nqs, G, 1, 64, 16, G, prefix=200), softcap=9.0)
+
+
 def spread(keys, nqs):
     """As many keys as queries at least, and more for some."""
     return [max(m, (keys * (i % 5)) // 4 + i) for i, m in enumerate(nqs)]
@@ -391,6 +403,18 @@ def test_prefix_of_length_zero_and_equal_results(kq):
     a, la = verify(kq, s)
     b, lb = verify(kq, s, shared=True)
     assert torch.equal(a, b) and torch.equal(la, lb)
+
+
+@pytest.mark.parametrize("G,B,prefix", [(4, 5, 100), (2, 90, 700), (64, 3, 50)])
+def test_shared_prefix_of_single_tokens_without_starts(kq, G, B, prefix):
+    keys = [(7 * i) % 150 for i in range(B)]
+    s = make(keys, [1] * B, G, 2, 128, 16, G + B, prefix=prefix)
+    with_starts = launch(kq, s, T=B)
+    without = launch(kq, s, T=B, q_start=False)
+    torch.cuda.synchronize()
+    assert torch.equal(with_starts[0], without[0]) and torch.equal(with_starts[1], without[1])
+    ref = attention(s["q"][:B], s["pool"], s["tables"], keys, [1] * B, s["scale"], 0.0, 0, (s["prefix_list"], prefix))
+    check_attention(without[0][:B], without[1][:B], ref)
 
 
 def test_shared_prefix_long(kq):
