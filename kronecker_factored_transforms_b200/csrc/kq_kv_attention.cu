@@ -708,49 +708,40 @@ __global__ void __launch_bounds__(128) kq_kv_combine_kernel(const __grid_constan
     const int64_t at = WARPS_PER_ROW == 4 ? blockIdx.x : int64_t(blockIdx.x) * 4 + warp;
     const bool real = at < rows && at < int64_t(all_queries(a)) * H;  // not padding behind the last sequence
     if (!real) return;
+    const int t = int(at / H), g = int(at - int64_t(t) * H) % p.G;
     // own keys: parts of the row kernel (as its records say) or of the tile kernel, and so for the prefix's
-    int2 rec[2] = {make_int2(0, p.own_splits), make_int2(0, p.pre_splits)};
-    int row[2] = {0, 0};
-    if (p.rows_own) rec[0] = p.parts[at];
-    if (p.rows_prefix) rec[1] = p.parts[rows + at];
+    int2 rec0 = make_int2(0, p.own_splits), rec1 = make_int2(0, p.pre_splits);
+    int row0 = 0, row1 = 0;
+    if (p.rows_own) rec0 = p.parts[at];
+    if (p.rows_prefix) rec1 = p.parts[rows + at];
     auto sound = [&](const int2 &r) { return r.y >= 1 && r.y <= p.ctas && r.x >= 0 && r.x <= p.ctas - r.y; };
-    const bool tiled = p.few && rec[0].x == -1 && rec[0].y == p.own_splits, rows_own = p.rows_own && !tiled;
-    if ((rows_own && !sound(rec[0])) || (p.rows_prefix && !sound(rec[1]))) return;  // a row past the bound on queries
-    if (!p.partial && p.rows_own && rec[0].y == 1) return;  // written by its block
-    const int n = rec[0].y + rec[1].y;
-    const bool cut0 = rows_own && rec[0].y > 1, cut1 = p.rows_prefix && rec[1].y > 1;
-    if (a.q_start && (cut0 || cut1 || !rows_own)) {  // the row's place in its unit's tile; whether it is bounded away
-        const int t = int(at / H), g = int(at - int64_t(t) * H) % p.G;
-        int lo = 0, hi = int(a.B);
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (a.q_start[mid + 1] <= t) lo = mid + 1;
-            else hi = mid;
-        }
-        const int i = t - a.q_start[lo];
+    const bool tiled = p.few && rec0.x == -1 && rec0.y == p.own_splits, rows_own = p.rows_own && !tiled;
+    if ((rows_own && !sound(rec0)) || (p.rows_prefix && !sound(rec1))) return;  // a row past the bound on queries
+    if (!p.partial && p.rows_own && rec0.y == 1) return;  // written by its block
+    const int n = rec0.y + rec1.y;
+    const bool cut0 = rows_own && rec0.y > 1, cut1 = p.rows_prefix && rec1.y > 1;
+    if (cut0 || cut1 || !rows_own) {  // the row's place in its unit's tile; whether it is bounded away
+        const int i = a.q_start ? t - a.q_start[seq_of(a, t)] : 0;  // the query's number in its sequence
         if (i < 0 || i >= a.max_q) return;
-        row[0] = (i * p.G + g) % R;
-        row[1] = (t * p.G + g) % R;
-    } else if (cut0 || cut1) {
-        const int t = int(at / H), g = int(at - int64_t(t) * H) % p.G;
-        row[0] = g % R;
-        row[1] = (t * p.G + g) % R;
+        row0 = (i * p.G + g) % R;
+        row1 = (t * p.G + g) % R;
     }
     // Where part k lies: the rows and sums that it is among, and its index there.
     auto place = [&](int k, const float *&o, const float *&l) -> int64_t {
-        const int u = k >= rec[0].y;
-        const int i = u ? k - rec[0].y : k;
+        const int u = k >= rec0.y;
+        const int i = u ? k - rec0.y : k;
         if (u ? !p.rows_prefix : !rows_own) {
             o = p.tile_o, l = p.tile_l;
             return int64_t((u ? p.own_splits : 0) + i) * rows + at;
         }
-        if (rec[u].y == 1) {
+        const int2 rec = u ? rec1 : rec0;
+        if (rec.y == 1) {
             o = p.whole_o, l = p.whole_l;
             return u * rows + at;
         }
         o = p.slot_o, l = p.slot_l;
         // a unit's first block holds it as its last unit, the others as their first
-        return (int64_t(rec[u].x + i) * 2 + (i == 0 ? 1 : 0)) * R + row[u];
+        return (int64_t(rec.x + i) * 2 + (i == 0 ? 1 : 0)) * R + (u ? row1 : row0);
     };
     float top = -INFINITY, wsum = 0.0f;
     float v[D / 32];

@@ -136,6 +136,19 @@ __device__ __forceinline__ Seq load_seq(const Plan &p, int64_t b, bool report) {
     return s;
 }
 
+// The sequence of token t (the last that begins at or before it), by a warp: 32 looked at in a step.
+__device__ __forceinline__ int seq_of(const KvAttnArgs &a, int t) {
+    int lo = 0, hi = int(a.B);
+    const int lane = threadIdx.x & 31;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32, k = lo + lane * step;
+        const int n = max(1, __popc(__ballot_sync(0xffffffffu, k < hi && a.q_start[k] <= t)));
+        lo += (n - 1) * step;
+        hi = min(hi, lo + step);
+    }
+    return lo;
+}
+
 // Position of token t's queries among the keys of its sequence (for windows over a prefix).
 __device__ __forceinline__ int query_shift(const KvAttnArgs &a, int t) {
     if (!a.q_start) return a.kv_len[t] > 0 ? a.kv_len[t] - 1 : -1;
