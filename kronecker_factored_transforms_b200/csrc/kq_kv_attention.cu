@@ -758,6 +758,19 @@ __global__ void __launch_bounds__(128) kq_kv_combine_kernel(const __grid_constan
             src += from * D;
             l = sums[from];
         }
+        // the first parts' values are on their way before the sums are known
+        constexpr int AHEAD = 4;
+        const int cnt = min(32, (n - k0 + WARPS_PER_ROW - 1) / WARPS_PER_ROW);
+        auto value = [&](int k) {
+            const float *sk = reinterpret_cast<const float *>(
+                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), k));
+            if constexpr (D == 128) return reinterpret_cast<const float4 *>(sk)[lane];
+            else return reinterpret_cast<const float2 *>(sk)[lane];
+        };
+        decltype(value(0)) z[AHEAD];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+            if (k < cnt) z[k] = value(k);
         float m = l;
 #pragma unroll
         for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -771,23 +784,17 @@ __global__ void __launch_bounds__(128) kq_kv_combine_kernel(const __grid_constan
         wsum = wsum * f + s;
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) v[e] *= f;
-        const int cnt = min(32, (n - k0 + WARPS_PER_ROW - 1) / WARPS_PER_ROW);
-#pragma unroll 4
-        for (int k = 0; k < cnt; ++k) {
+        auto add = [&](int k, const auto &y) {
             const float wk = __shfl_sync(0xffffffffu, w, k);  // 0 for a part without keys, whose values may be anything
-            const float *sk = reinterpret_cast<const float *>(
-                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), k));
-            if constexpr (D == 128) {
-                const float4 z = reinterpret_cast<const float4 *>(sk)[lane];
-                if (wk != 0.0f) {
-                    v[0] = fmaf(z.x, wk, v[0]), v[1] = fmaf(z.y, wk, v[1]);
-                    v[2] = fmaf(z.z, wk, v[2]), v[3] = fmaf(z.w, wk, v[3]);
-                }
-            } else {
-                const float2 z = reinterpret_cast<const float2 *>(sk)[lane];
-                if (wk != 0.0f) v[0] = fmaf(z.x, wk, v[0]), v[1] = fmaf(z.y, wk, v[1]);
-            }
-        }
+            if (wk == 0.0f) return;
+            v[0] = fmaf(y.x, wk, v[0]), v[1] = fmaf(y.y, wk, v[1]);
+            if constexpr (D == 128) v[2] = fmaf(y.z, wk, v[2]), v[3] = fmaf(y.w, wk, v[3]);
+        };
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+            if (k < cnt) add(k, z[k]);
+#pragma unroll 4
+        for (int k = AHEAD; k < cnt; ++k) add(k, value(k));
     }
     if constexpr (WARPS_PER_ROW == 4) {
 #pragma unroll
