@@ -150,7 +150,9 @@ struct RCfg {
     static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;           // abort flag
     static constexpr int OFF_SCAN = (OFF_MISC + 4 + 15) & ~15;
     static constexpr int SMEM = OFF_SCAN + 8 * (WARPS + 1) + 16;
-    static constexpr int OCC = NT == 1 ? 3 : 2;    // blocks per SM
+    // blocks per SM, as registers and shared memory allow (head_dim 64, 64 sequences of 4000 keys, 8 key heads of 4:
+    // 82 us with three, 54 with four, 59 with five and 72 registers)
+    static constexpr int OCC = NT == 1 ? (D == 64 ? 4 : 3) : 2;
     static_assert((SMEM + 1024) * OCC <= 227 * 1024, "shared memory of the resident blocks");
     static_assert(STAGE % 128 == 0 && OFF_PART % 16 == 0 && OFF_BAR % 8 == 0, "alignment");
 };
