@@ -94,7 +94,8 @@ def check(s, alpha_k=0.9, alpha_v=0.8, inter=False, skip=()):
 @pytest.mark.parametrize("T,H,Hk,D,page,rope,inter", [
     (1, 32, 8, 128, 16, 128, False), (1, 1, 1, 64, 16, 64, True), (3, 5, 5, 128, 32, 0, False),
     (17, 14, 2, 128, 16, 64, True), (67, 28, 4, 128, 64, 128, True), (130, 12, 12, 64, 16, 32, False),
-    (257, 8, 1, 128, 256, 16, False), (1000, 6, 3, 64, 128, 48, True), (2051, 16, 8, 128, 16, 128, False)])
+    (257, 8, 1, 128, 256, 16, False), (1000, 6, 3, 64, 128, 48, True), (2051, 16, 8, 128, 16, 128, False),
+    (40011, 2, 1, 128, 16, 112, False), (9000, 4, 2, 64, 16, 48, False), (30000, 1, 1, 128, 16, 128, True)])
 def test_append(kq, T, H, Hk, D, page, rope, inter):
     s = make(T, H, Hk, D, page, rope, T * 7 + H)
     append(kq, s, inter=inter)
