@@ -39,9 +39,9 @@
 // which kq_kv_combine_kernel joins in a fixed order.
 //
 // Measured, head_dim 128 and 8 key heads: 4 sequences of 65 to 131 thousand keys, 4 query
-// heads a key head, 100 us (4.3 TB/s of 6.55; issue slots 56 % busy, ALU 52 %: some 500
+// heads a key head, 97 us (4.4 TB/s of 6.55; issue slots 56 % busy, ALU 52 %: some 500
 // instructions for 32 keys and warp); 64 sequences of 60 to 8192 keys, 8 query heads a key
-// head, 41 us (2.4 TB/s); one token on 1531 keys 11 us.
+// head, 37 us (2.6 TB/s); one token on 1531 keys 10 us.
 #include <cuda_fp16.h>
 
 #include <mutex>
