@@ -148,6 +148,25 @@ def test_one_key_head_of_many_query_heads(kq, G, nqs, keys):
     verify(kq, make(keys, nqs, G, 1, 64, 16, G, prefix=200), softcap=9.0)
 
 
+@pytest.mark.parametrize("G,D,nqs,keys,kw", [
+    (4, 128, [8192], [8192], {}), (8, 64, [5000, 1, 3000, 1, 1], [5100, 7000, 3000, 1, 9000], dict(window=700)),
+    (2, 128, [40, 64], [131072, 100001], {}), (1, 128, [20000], [21003], dict(softcap=20.0)),
+    (4, 64, [1] * 300 + [2000], [500] * 300 + [2000], {})])
+def test_long_prompts(kq, G, D, nqs, keys, kw):
+    """Many row tiles, and many keys for a few; sampled queries as sequences of their own against the 64-bit form."""
+    s = make(keys, nqs, G, 2, D, 64, len(nqs) + D)
+    out, lse = launch(kq, s, **kw)
+    torch.cuda.synchronize()
+    assert kq.kq_device_error() == 0 and (out[s["T"]:] == 5.0).all()
+    g = torch.Generator().manual_seed(sum(nqs))
+    b = [0, len(nqs) - 1] + torch.randint(len(nqs), (22,), generator=g).tolist()
+    i = [0, nqs[-1] - 1] + [int(torch.randint(nqs[x], (1,), generator=g)) for x in b[2:]]
+    at = [sum(nqs[:x]) + y for x, y in zip(b, i)]
+    ref = attention(s["q"][at], s["pool"], [s["tables"][x] for x in b], [keys[x] - nqs[x] + y + 1 for x, y in zip(b, i)],
+                    [1] * len(at), s["scale"], kw.get("softcap", 0.0), kw.get("window", 0))
+    check_attention(out[at], lse[at], ref)
+
+
 def spread(keys, nqs):
     """As many keys as queries at least, and more for some."""
     return [max(m, (keys * (i % 5)) // 4 + i) for i, m in enumerate(nqs)]
