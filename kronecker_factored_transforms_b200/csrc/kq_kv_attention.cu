@@ -510,11 +510,23 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const float f = ks[mt][k >> 1] * mult[nt][k & 1];
-                        float v;
-                        if (CAP) v = fmaf(tanh_exp(x[mt][nt][k] * f), a.softcap * kLog2e, -ref[nt][k & 1]);
-                        else v = fmaf(x[mt][nt][k], f, -ref[nt][k & 1]);
-                        x[mt][nt][k] = v;
+                        if (CAP) x[mt][nt][k] *= f;
+                        else x[mt][nt][k] = fmaf(x[mt][nt][k], f, -ref[nt][k & 1]);
                     }
+            if constexpr (CAP) {
+                const uint64_t cap = pair2(a.softcap * kLog2e, a.softcap * kLog2e);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float(&y)[4] = x[mt][nt];
+                        uint64_t z0 = pair2(y[0], y[1]), z1 = pair2(y[2], y[3]);
+                        tanh_pairs(z0, z1);
+                        const uint64_t minus = pair2(-ref[nt][0], -ref[nt][1]);
+                        split2(fma2(z0, cap, minus), y[0], y[1]);
+                        split2(fma2(z1, cap, minus), y[2], y[3]);
+                    }
+            }
             if (!inner) {
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)

@@ -26,9 +26,97 @@ __device__ __forceinline__ float lg2(float x) {
     asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// tanh as 1 - 2 / (e^2z + 1): off by about 2^-22, absolutely.
-__device__ __forceinline__ float tanh_exp(float z) {
-    return 1.0f - __fdividef(2.0f, ex2(z * (2.0f * kLog2e)) + 1.0f);
+// Pairs of fp32 values.
+__device__ __forceinline__ uint64_t pair2(float a, float b) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t pair2u(uint32_t a, uint32_t b) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ void split2(uint64_t d, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(d));
+}
+__device__ __forceinline__ void split2u(uint64_t d, uint32_t &a, uint32_t &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(d));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// The tanh of a cap.  Its error has to be relative: a cap far above the scores multiplies it, and scores far below
+// the cap are to stay as they are.
+//
+// tanh within +-1/2: z q(z^2), q of degree 5 fitted to tanh there by least squares with weights that level the error
+// (under 1e-10; fp32's own rounding is 3e-8).
+__device__ __forceinline__ uint64_t tanh_small(uint64_t z) {
+    using tc::f32x2_mul;
+    const uint64_t u = f32x2_mul(z, z);
+    uint64_t q = pair2(-0.00646002684f, -0.00646002684f);
+    q = fma2(q, u, pair2(0.0211690962f, 0.0211690962f));
+    q = fma2(q, u, pair2(-0.0538669676f, -0.0538669676f));
+    q = fma2(q, u, pair2(0.133326113f, 0.133326113f));
+    q = fma2(q, u, pair2(-0.333333105f, -0.333333105f));
+    q = fma2(q, u, pair2(1.0f, 1.0f));
+    return f32x2_mul(q, z);
+}
+// tanh of any numbers: z p(z^2) / q(z^2) within +-9, past which tanh is 1 to fp32; p and q of degree 4, fitted to
+// tanh there by least squares on q's multiple, with weights that level the relative error (2e-8).  No coefficient is
+// negative, so that fp32 loses two bits at most.  z p and q of a pair; a NaN stays one.
+__device__ __forceinline__ void tanh_parts(uint64_t &z, uint64_t &q) {
+    using tc::f32x2_mul;
+    auto within = [](float x) {
+        float y;
+        asm("{\n\t.reg .f32 t;\n\tmax.NaN.f32 t, %1, 0fC1100000;\n\tmin.NaN.f32 %0, t, 0f41100000;\n\t}" : "=f"(y) : "f"(x));
+        return y;
+    };
+    float a, b;
+    split2(z, a, b);
+    z = pair2(within(a), within(b));
+    const uint64_t u = f32x2_mul(z, z);
+    uint64_t p = pair2(1.33545539e-08f, 1.33545539e-08f);
+    p = fma2(p, u, pair2(2.06090008e-05f, 2.06090008e-05f));
+    p = fma2(p, u, pair2(0.00349558308f, 0.00349558308f));
+    p = fma2(p, u, pair2(0.133810207f, 0.133810207f));
+    p = fma2(p, u, pair2(1.0f, 1.0f));
+    z = f32x2_mul(z, p);
+    q = pair2(7.77651337e-07f, 7.77651337e-07f);
+    q = fma2(q, u, pair2(0.000328562659f, 0.000328562659f));
+    q = fma2(q, u, pair2(0.0258769635f, 0.0258769635f));
+    q = fma2(q, u, pair2(0.467143357f, 0.467143357f));
+    q = fma2(q, u, pair2(1.0f, 1.0f));
+}
+// Of two pairs, with one reciprocal (q is under 2^9 each).
+__device__ __forceinline__ void tanh_pairs(uint64_t &a, uint64_t &b) {
+    using tc::f32x2_mul;
+    uint64_t qa, qb;
+    tanh_parts(a, qa);
+    tanh_parts(b, qb);
+    float x0, x1;
+    const uint64_t ab = f32x2_mul(qa, qb);  // the first of both, the second of both
+    split2(ab, x0, x1);
+    const float r = __fdividef(1.0f, x0 * x1);
+    const uint64_t rab = pair2(r * x1, r * x0);
+    a = f32x2_mul(a, f32x2_mul(rab, qb));
+    b = f32x2_mul(b, f32x2_mul(rab, qa));
+}
+__device__ __forceinline__ float tanh_any(float z) {
+    uint64_t p = pair2(z, z), q;
+    tanh_parts(p, q);
+    float n, d, same;
+    split2(p, n, same);
+    split2(q, d, same);
+    return __fdividef(n, d);
 }
 // Wait for a phase; gives up as wait_bounded_err does.
 __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile int *abort, unsigned int *err) {

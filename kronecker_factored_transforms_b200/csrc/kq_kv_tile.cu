@@ -68,59 +68,6 @@ struct Is {
     static constexpr bool value = B;
 };
 
-// Pairs of fp32 values.
-__device__ __forceinline__ uint64_t pair2(float a, float b) {
-    uint64_t d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
-    return d;
-}
-__device__ __forceinline__ uint64_t pair2u(uint32_t a, uint32_t b) {
-    uint64_t d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(a), "r"(b));
-    return d;
-}
-__device__ __forceinline__ void split2(uint64_t d, float &a, float &b) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(d));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
-// tanh of four numbers, with one reciprocal: tanh z = 1 - 2 / (e^2z + 1), and past 9 it is 1 to fp32.
-__device__ __forceinline__ void tanh4(float &a, float &b, float &c, float &d) {
-    auto e = [](float z) {
-        float y;  // z within +-9.5; a NaN stays one
-        asm("{\n\t.reg .f32 t;\n\tmax.NaN.f32 t, %1, 0fC1180000;\n\tmin.NaN.f32 %0, t, 0f41180000;\n\t}" : "=f"(y) : "f"(z));
-        return ex2(y * (2.0f * kLog2e)) + 1.0f;
-    };
-    const float ea = e(a), eb = e(b), ec = e(c), ed = e(d), ab = ea * eb, cd = ec * ed;
-    const float r = __fdividef(-2.0f, ab * cd), rab = r * cd, rcd = r * ab;  // the product is under 2^112
-    a = fmaf(rab, eb, 1.0f);
-    b = fmaf(rab, ea, 1.0f);
-    c = fmaf(rcd, ed, 1.0f);
-    d = fmaf(rcd, ec, 1.0f);
-}
-
-// tanh of two numbers within +-1/2: z q(z^2), q of degree 5 fitted to tanh there by least squares with
-// weights that level the error (under 1e-10; fp32's own rounding is 3e-8).
-__device__ __forceinline__ uint64_t tanh_small(uint64_t z) {
-    const uint64_t u = f32x2_mul(z, z);
-    uint64_t q = pair2(-0.00646002684f, -0.00646002684f);
-    q = fma2(q, u, pair2(0.0211690962f, 0.0211690962f));
-    q = fma2(q, u, pair2(-0.0538669676f, -0.0538669676f));
-    q = fma2(q, u, pair2(0.133326113f, 0.133326113f));
-    q = fma2(q, u, pair2(-0.333333105f, -0.333333105f));
-    q = fma2(q, u, pair2(1.0f, 1.0f));
-    return f32x2_mul(q, z);
-}
-
 // Eight codes as bf16 integers, pairs (0, 4), (1, 5), (2, 6), (3, 7): (code + 8) | 0x4300 is 136 + code.
 __device__ __forceinline__ uint4 codes_bf16(uint32_t w) {
     uint32_t o[4];
@@ -351,18 +298,34 @@ __global__ void __launch_bounds__(T_THREADS, 1)
                             top = fmax3(top, __uint_as_float(v[e + 2]) * k.z, __uint_as_float(v[e + 3]) * k.w);
                         }
                     }
-                    if (CAP) top = a.softcap * kLog2e * tanh_exp(top);  // which rises with its argument
+                    if (CAP) top = a.softcap * kLog2e * tanh_any(top);  // which rises with its argument
                 } else
 #pragma unroll 1
                 for (int c = 0; c < CH; c += 32) {
                     uint32_t v[32];
                     tmem_ld_32x32b_x32(ts + uint32_t(c), v);
                     tmem_wait_ld();
+                    if constexpr (CAP) {
+                        float far = 0.0f;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            v[e] = __float_as_uint(__uint_as_float(v[e]) * reinterpret_cast<const float *>(ks)[c + e]);
+                            far = fmaxf(far, fabsf(__uint_as_float(v[e])));
+                        }
+                        const bool small = __all_sync(0xffffffffu, far <= 0.5f);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            uint64_t a0 = pair2u(v[e], v[e + 1]), a1 = pair2u(v[e + 2], v[e + 3]);
+                            if (small) a0 = tanh_small(a0), a1 = tanh_small(a1);
+                            else tanh_pairs(a0, a1);
+                            split2u(a0, v[e], v[e + 1]);
+                            split2u(a1, v[e + 2], v[e + 3]);
+                        }
+                    }
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
                         const float k = reinterpret_cast<const float *>(ks)[c + e];
-                        float x = __uint_as_float(v[e]) * k;
-                        if (CAP) x = a.softcap * kLog2e * tanh_exp(x);
+                        float x = __uint_as_float(v[e]) * (CAP ? a.softcap * kLog2e : k);
                         const int t = t0 + c + e;
                         if (t < row_lo || t >= row_hi || (lost && k == -INFINITY)) x = -INFINITY;
                         v[e] = __float_as_uint(x);
@@ -407,11 +370,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
                                         a0 = tanh_small(a0);
                                         a1 = tanh_small(a1);
                                     } else {
-                                        split2(a0, x0, x1);
-                                        split2(a1, x2, x3);
-                                        tanh4(x0, x1, x2, x3);
-                                        a0 = pair2(x0, x1);
-                                        a1 = pair2(x2, x3);
+                                        tanh_pairs(a0, a1);
                                     }
                                     const uint64_t cap = pair2(a.softcap * kLog2e, a.softcap * kLog2e);
                                     a0 = fma2(a0, cap, minus);
