@@ -20,6 +20,8 @@
 //   - one pass over the scores: m is the maximum of the row's first chunk, and a weight
 //     may pass 1, as fp32 and bf16 have the range (up to 2^60 here).  When a chunk's
 //     largest passed 2^8, m is raised before the next one, which rescales O: rare.
+//     A chunk with a value scale over 2^40, whose product with 2^60 would leave the
+//     range, is looked at first as a masked one is, and its weights stay under 2^8.
 //   - the two row tiles are half a step apart: while one warpgroup is at its softmax
 //     the tensor core works for the other.
 // Keys that a row does not see, past its place or out of its window, are looked at only
@@ -58,7 +60,7 @@ struct TCfg {
     static constexpr int OFF_BAR = OFF_SC + 2 * 1024;
     enum { KFULL = 0, KFREE = 2, VFULL = 4, VFREE = 6, SREADY = 8, PREADY = 10, ODONE = 12, SCFREE = 14, DONE = 16, QREADY = 17, NBAR = 18 };
     static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
-    static constexpr int SMEM = OFF_MISC + 16 + 1024;  // TMEM base, abort flag, per stage whether keys lack a page
+    static constexpr int SMEM = OFF_MISC + 16 + 1024;  // TMEM base, abort flag, per stage whether it is special
     static constexpr int COL_S = 0, COL_O = 256;  // TMEM columns: S of tile q at 128 q, O at 256 + D q
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
@@ -257,8 +259,9 @@ __global__ void __launch_bounds__(T_THREADS, 1)
                 }
                 continue;
             }
-            const bool lost = *reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 8 + 4 * (n & 1)) != 0;
-            const bool slow = lost || t0 < all_lo || t0 + CH > all_hi;
+            // a key without a page, or a value scale over 2^40
+            const bool special = *reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 8 + 4 * (n & 1)) != 0;
+            const bool slow = special || t0 < all_lo || t0 + CH > all_hi;
             // The reference rises by `up`: O, whose last product has ended with S's, and the sums follow.
             auto raise = [&](float up) {
                 const float f = ex2(-up);
@@ -327,7 +330,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
                         const float k = reinterpret_cast<const float *>(ks)[c + e];
                         float x = __uint_as_float(v[e]) * (CAP ? a.softcap * kLog2e : k);
                         const int t = t0 + c + e;
-                        if (t < row_lo || t >= row_hi || (lost && k == -INFINITY)) x = -INFINITY;
+                        if (t < row_lo || t >= row_hi || (special && k == -INFINITY)) x = -INFINITY;
                         v[e] = __float_as_uint(x);
                         top = fmaxf(top, x);
                     }
@@ -565,10 +568,10 @@ __global__ void __launch_bounds__(T_THREADS, 1)
             const uint32_t ph = uint32_t(n >> 1) ^ 1u;
             const Row next = load(n + 1, page);
             page = page_of(n + 2);
-            const bool lost = named_barrier_any(1, 128, now.ks == -INFINITY && now.vs == 0.0f);
+            const bool special = named_barrier_any(1, 128, (now.ks == -INFINITY && now.vs == 0.0f) || now.vs > 0x1p40f);
             ok = ok && wait(C::KFREE + st, ph) && wait(C::SCFREE + st, ph);
             if (!ok) continue;  // the warpgroup's barrier wants every warp, also one that has given up
-            if (r == 0) *reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 8 + 4 * st) = lost;
+            if (r == 0) *reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 8 + 4 * st) = special;
             lay(C::OFF_K + st * C::OPERAND, now.k);
             float *sc = reinterpret_cast<float *>(smem + C::OFF_SC + 1024 * st);
             sc[r] = now.ks;
