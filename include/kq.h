@@ -402,7 +402,8 @@ kq_status kq_kv_gather(const kq_kv_cache *cache, const int64_t *slots, uint16_t 
  * a multiple of kv_heads with at most 1024 heads, T * q_heads < 2^31,
  * max_pages * page_size < 2^30, prefix_len < 2^30.
  * The scales in the cache are not negative and, where a query sees their row, finite;
- * rows that it does not see may hold anything.
+ * rows that it does not see may hold anything.  A value's scale is 0 or from 2^-100 to
+ * 2^96 (under a smaller one a weight loses bits, over a larger one sums may overflow).
  * Scores and softmax sums are fp32, and the products' accumulators too.  The same
  * inputs give the same bits.  Nothing is read back to the host: sequences may
  * grow between replays of a captured graph.

@@ -474,9 +474,8 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     ks[mt][k] = sc[16 * mt + og + 8 * k];
-                    // a scale of 0 (a row of zeros) counts as 2^-100 here: its codes are 0 anyway; an infinite
-                    // one as 2^128, so that a score of -inf leaves that key out too
-                    lv[mt][k] = fminf(fmaxf(lg2(sc[CH + 16 * mt + og + 8 * k]), -100.0f), 128.0f);
+                    // an infinite scale as 2^128, so that a score of -inf leaves that key out too
+                    lv[mt][k] = fminf(lg2(sc[CH + 16 * mt + og + 8 * k]), 128.0f);
                 }
 #pragma unroll
                 for (int w = 0; w < W; ++w) {
@@ -502,6 +501,9 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
                         if (og + 8 * k >= left) ks[mt][k] = lv[mt][k] = 0.0f;
                 }
             }
+            // For the reference a scale under 2^-100, or of 0 (a row of zeros), counts as 2^-100: the sum of exp(x)
+            // is relative to the same reference and must not pass fp32's range.
+            auto floored = [](float l) { return fmaxf(l, -100.0f); };
             float top = -INFINITY;  // of a weight's exponent
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
@@ -544,8 +546,8 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
-                    top = fmax3(top, fmaxf(x[mt][nt][0], x[mt][nt][1]) + lv[mt][0],
-                                fmaxf(x[mt][nt][2], x[mt][nt][3]) + lv[mt][1]);
+                    top = fmax3(top, fmaxf(x[mt][nt][0], x[mt][nt][1]) + floored(lv[mt][0]),
+                                fmaxf(x[mt][nt][2], x[mt][nt][3]) + floored(lv[mt][1]));
             if (__any_sync(0xffffffffu, top > 14.0f || seen != kAllSeen)) {
                 // move the references to 6 under the maxima so far
 #pragma unroll
@@ -555,7 +557,7 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
                         float up = -INFINITY;
 #pragma unroll
                         for (int mt = 0; mt < MT; ++mt)
-                            up = fmax3(up, x[mt][nt][k] + lv[mt][0], x[mt][nt][k + 2] + lv[mt][1]);
+                            up = fmax3(up, x[mt][nt][k] + floored(lv[mt][0]), x[mt][nt][k + 2] + floored(lv[mt][1]));
                         up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 4));
                         up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 8));
                         up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 16));

@@ -2,7 +2,8 @@
 import pytest
 import torch
 
-from test_kv_attention_gpu import kq, make, verify  # noqa: F401  (the fixture)
+from kv_testutil import attention
+from test_kv_attention_gpu import kq, launch, make, verify  # noqa: F401  (the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -35,3 +36,27 @@ def test_value_scales_of_all_sizes_in_one_row(kq, nqs):
     e = torch.randint(-95, 90, s["pool"][3].shape, generator=g, device="cuda").float()
     s["pool"][3] *= torch.exp2(e)
     verify(kq, s)
+
+
+@pytest.mark.parametrize("nqs", [[1, 3], [150, 200]])
+def test_the_smallest_value_scales(kq, nqs):
+    """Under 2^-100 the row kernel's weights lose bits, but not their size: within 2^-6 of the terms."""
+    for mid, bits in ((1e-29, 7.5), (1e-33, 6), (1e-35, 3)):
+        s = make([300, 140], nqs, 4, 2, 128, 16, 4)
+        s["pool"][3] *= mid
+        out, _ = launch(kq, s)
+        torch.cuda.synchronize()
+        T = s["T"]
+        ref, _, mean, _, _ = attention(s["q"][:T], s["pool"], s["tables"], s["keys"], s["nqs"], s["scale"])
+        # bf16's half steps of the result and of a weight, 2^-8 each, or what is left of the weight's bits
+        assert ((out[:T].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -bits * mean + 1e-40).all(), mid
+
+
+@pytest.mark.parametrize("prefix", [0, 200])
+@pytest.mark.parametrize("nqs", [[1, 3], [150, 200]])
+def test_codes_under_a_scale_of_zero_count_nothing(kq, nqs, prefix):
+    s = make([300, 140], nqs, 4, 2, 128, 16, 5, prefix=prefix)
+    s["pool"][3][~torch.isnan(s["pool"][3])] = 0.0
+    out, _ = launch(kq, s)
+    torch.cuda.synchronize()
+    assert (out[:s["T"]] == 0).all()
