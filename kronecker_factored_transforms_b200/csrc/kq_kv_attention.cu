@@ -412,7 +412,10 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<D, NT>::OCC) kq_kv_rows_kernel
                 tot += __shfl_xor_sync(0xffffffffu, tot, 2);
                 // The score's multiplier: the softmax scale, and what the operands were scaled by.
                 const float back = __uint_as_float(uint32_t(127 - up) << 23);  // 1 / f
-                const float mul = (CAP ? a.scale / a.softcap : a.scale * kLog2e) * back * 0x1p24f;
+                float mul = (CAP ? a.scale / a.softcap : a.scale * kLog2e) * back * 0x1p24f;
+                // a zero score is one under any scale; a cap far under the scores is passed at 2^100 as anywhere
+                if (big == 0.0f) mul = 0.0f;
+                if (CAP) mul = fminf(fmaxf(mul, -0x1p100f), 0x1p100f);
                 int rl = 0, rh = 0;
                 if (real) {
                     rh = min(n, max(0, shift + i + 1));

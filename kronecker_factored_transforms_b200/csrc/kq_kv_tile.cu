@@ -520,6 +520,8 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         // ---------------- codes into operands: a key per thread ----------------
         const int r = tid & 127;
         const float factor = CAP ? a.scale / a.softcap : a.scale * kLog2e;
+        // of a key's scale times that: finite, so that a zero score stays one; a tanh is 1 long before
+        constexpr float kMost = CAP ? 0x1p100f : 0x1.fffffep127f;
         constexpr int W = D / 32;  // 16-byte pieces of a row of codes
         struct Row {
             uint4 k[W], v[W];
@@ -542,7 +544,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
                     const uint4 *v = reinterpret_cast<const uint4 *>(a.c.v_codes + row * (D / 2));
 #pragma unroll
                     for (int i = 0; i < W; ++i) w.k[i] = k[i], w.v[i] = v[i];
-                    w.ks = a.c.k_scale[row] * factor;
+                    w.ks = fminf(fmaxf(a.c.k_scale[row] * factor, -kMost), kMost);
                     w.vs = fminf(a.c.v_scale[row], 0x1.fffffep127f);  // a weight of 0 leaves any row out
                 } else {
                     w.ks = -INFINITY;  // no such page: the mark by which the softmax leaves the key out
