@@ -321,8 +321,9 @@ typedef struct kq_kv_transform {
  *     s = alpha max|y| / 7,  code = clamp(round_half_even(y / s), -8, 7)
  *
  * The rotation is not rounded before the product.  Codes are those of exact
- * arithmetic: rows with a value too near a rounding border for fp32 are redone
- * in fp64.
+ * arithmetic, whatever the factor: those too near a rounding border for fp32 are
+ * computed again in fp64 (rows that the factor nearly cancels whole, which takes
+ * many times as long).  A scale is right to 2^-12 at least.
  *
  * cache     the pages; written only at the slots given.
  * tf        factors, clip ratios, rotary table.
@@ -342,7 +343,9 @@ typedef struct kq_kv_transform {
  * A slot past the last page, or a position outside the table, is never followed:
  * nothing of that token is stored (and, for a bad position, its queries are
  * written as zeros), and kq_device_error reports 65536.
- * A row with a NaN or an infinity gets unspecified codes, in that row alone.
+ * A row with a NaN, an infinity or a result past 3e38 gets unspecified codes, in
+ * that row alone.  A row of elements under 2^-75 whose products cancel in fp32
+ * counts as zero.
  * Returns KQ_ERR_SHAPE, KQ_ERR_UNSUPPORTED (head_dim, page_size, rope_dim, an
  * alpha below 2^-19), KQ_ERR_NULL, KQ_ERR_ALIGN, KQ_ERR_ARG (alpha outside
  * (0, 1], a stride too short, overlapping buffers), KQ_ERR_CUDA.  Asynchronous

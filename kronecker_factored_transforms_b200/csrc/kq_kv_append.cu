@@ -24,15 +24,20 @@
 //     addition).
 //   - one block an SM, all its tiles of one kind, so that it needs one factor.
 //
-// Codes of exact arithmetic: fp32 leaves y / s uncertain by up to kBorder of its
-// largest value; a row with a value nearer than that to a rounding border (a row in a
-// few hundred) is computed again by its warp in fp64, scale and all.
+// Codes of exact arithmetic: where y / s lies nearer to a rounding border than fp32 can
+// tell, the code is computed again by its warp in fp64.  How near that is follows from
+// the row and the factor: |x| |P_j| (of two-norms, the largest column's) is the most
+// that products add up to on the way to a sum that cancels (see error_of).  The warps
+// that make terms sum a row's squares on the way, the block its factor's columns'.
+// A row in ten has such a value, three of the 32 of a warp, so they are done four at a
+// time, eight lanes each, with the row and its row of the table brought to shared memory
+// (5000 clocks; one after another, from L2, they took 6000 each).
 //
-// Measured: 104-110 us for 8192 tokens of 64 query and 8 key heads of 128 with a rotary
-// table (3.0 TB/s of 6.55; 12000 clocks a tile and team, of which the product takes 1000),
-// the read-back of their keys and values 13 us more; issue slots 44 % busy, DRAM 30 %.  Both
-// teams' chains (rows, rotation, terms, product, codes) are waiting most of the time, and
-// 24 warps at 80 registers are all that an SM holds.
+// Measured: 129-133 us for 8192 tokens of 64 query and 8 key heads of 128 with a rotary
+// table (2.7 TB/s of 6.55), with the read-back of their keys and values, 13 us of that;
+// 116 us when a border of 2^-19 of max|y| sent one row in 250 back, which a factor that
+// cancels does not keep to.  Both teams' chains (rows, rotation, terms, product, codes)
+// are waiting most of the time, and 24 warps at 80 registers are all that an SM holds.
 #include <mutex>
 
 #include "kq_common.cuh"
@@ -46,7 +51,15 @@ namespace {
 using namespace tc;
 
 constexpr int A_THREADS = 768;     // per team eight warps that make terms and four that take rows
-constexpr float kBorder = 0x1p-19f;  // of max|y|: bound of fp32's error in a row
+// What a row's fp32 values may be off by, from the two-norms of the rotated row and of the factor's largest column.
+// A step of 16 products cuts them and the sum so far at 2^-25 of the largest (2^-25 is kept, 2^-26 lost, as measured),
+// and the new sum is truncated to fp32: 16 times 2^-25 and 2^-23 of at most |x||P_j| in each of D / 16 steps, 5/8 D
+// 2^-24; the smaller terms of keys and the rotation add less than 6 2^-24.  0.7 D covers both and the norms' own
+// rounding.  The small parts stand for squares and sums that underflow.
+template <int D>
+__device__ __forceinline__ float error_of(float squares, float column) {
+    return 0.7f * D * 0x1p-24f * (sqrtf(squares) + 0x1p-59f) * (column + 0x1p-59f) + 0x1p-118f;
+}
 enum : unsigned { kSiteKvAppendWait = 524288u };
 
 template <int D>
@@ -54,9 +67,14 @@ struct ACfg {
     static constexpr int ROW = D * 2 + 16;            // a row's place in shared memory, padded
     static constexpr int STAGE = 128 * ROW;
     static constexpr int OFF_X = D * D * 2;           // after the factor
-    static constexpr int OFF_Y = OFF_X + 4 * STAGE;   // 4 KB for each warp that takes rows
-    static constexpr int OFF_BAR = OFF_Y + 8 * 4096;
-    static constexpr int OFF_MISC = OFF_BAR + 8 * 6;  // of each pair: products done, rows ready, rows taken
+    // an undecided row: its fp32 values, the row itself, the table's row; padded, so that four rows lie in different banks
+    static constexpr int ROW_X = D * 4, ROW_CS = ROW_X + D * 2, ROW_PLACE = ROW_CS + D * 4 + 32;
+    static constexpr int OWN = 4 * ROW_PLACE > 4096 ? 4 * ROW_PLACE : 4096;
+    static constexpr int OFF_Y = OFF_X + 4 * STAGE;   // OWN bytes for each warp that takes rows
+    static constexpr int OFF_NORM = OFF_Y + 8 * OWN;  // [pair][turn][half of the pieces][row]: sums of squares
+    static constexpr int OFF_COL = OFF_NORM + 2 * 2 * 2 * 128 * 4;  // [warp][column]: the same of the factor's rows
+    static constexpr int OFF_BAR = OFF_COL + (A_THREADS / 32) * D * 4;
+    static constexpr int OFF_MISC = OFF_BAR + 8 * 6;  // of each pair: products done, rows and their norms ready, rows taken
     static constexpr int SMEM = OFF_MISC + 16 + 1024;
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
@@ -71,77 +89,168 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// One row's exact codes and scale, by a whole warp, from the row in fp32: `y32` in shared memory,
-// off by at most kBorder of its largest value `m`.  A lane has the columns D / 32 lane and on, and as
-// many elements of the rotated row; a column is computed again, in fp64, where its code or the
-// scale depends on it.
+// round_half_even(y * inv) as an int for |y * inv| < 2^22 (alpha >= 2^-19): the low mantissa bits
+// after adding 1.5 * 2^23; `off` keeps the largest distance to the rounded value.
+__device__ __forceinline__ int round_off(uint32_t ybits, float inv, float &off) {
+    const float y = __uint_as_float(ybits), b = fmaf(y, inv, 12582912.0f);
+    off = fmaxf(off, fabsf(fmaf(y, inv, -(b - 12582912.0f))));
+    return int(__float_as_uint(b)) - 0x4B400000;
+}
+
+__device__ __forceinline__ void unpack8(const uint4 &u, float (&v)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+
+// ---- rows that fp32 does not decide, in fp64 ----
+// Shared memory by its 32-bit address, as these are out of line (and all that they read there is written before the
+// call): a row, its row of the table, the factor.
+struct ExactRow {
+    uint32_t x, cs, factor;
+    int rope_dim;
+    bool inter;
+};
+__device__ __forceinline__ float shared_f32(uint32_t at) {
+    float v;
+    asm("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at));
+    return v;
+}
+__device__ __forceinline__ double shared_bf16(uint32_t at) {
+    uint16_t w;
+    asm("ld.shared.u16 %0, [%1];" : "=h"(w) : "r"(at));
+    return double(bf16_bits_to_float(w));
+}
+// Where the factor's element (k, n) lies: (row_place(k) ^ column n's swizzle) + column n's place.
+__device__ __forceinline__ uint32_t row_place(int k) { return uint32_t(k * 128 + ((k & 7) << 4)); }
 template <int D>
-__device__ __noinline__ void exact_row(const uint16_t *x, const unsigned char *factor, const float *y32, float m,
-                                       const float *cs, int rope_dim, bool inter, float alpha, uint8_t *codes,
-                                       float *scale) {
-    constexpr int N = D / 32;
-    const int lane = threadIdx.x & 31, half = rope_dim >> 1;
-    double xs[N];
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-        const int i = N * lane + e;
-        double v = double(bf16_bits_to_float(x[i]));
-        if (i < rope_dim) {
-            const int k = inter ? i >> 1 : (i < half ? i : i - half);  // the pair's angle
-            const bool first = inter ? (i & 1) == 0 : i < half;
-            const int j = inter ? i ^ 1 : (first ? i + half : i - half);
-            const double w = double(bf16_bits_to_float(x[j])), c = double(cs[k]), s = double(cs[half + k]);
-            v = first ? v * c - w * s : w * s + v * c;
-        }
-        xs[e] = v;
+struct Column {
+    uint32_t at, swizzle;
+    __device__ __forceinline__ Column(uint32_t factor, int n)
+        : at(factor + uint32_t((n >> 6) * D * 128 + 2 * (n & 7))), swizzle(uint32_t(((n & 63) >> 3) << 4)) {}
+    __device__ __forceinline__ double operator()(uint32_t row) const { return shared_bf16(at + (row ^ swizzle)); }
+};
+__device__ __forceinline__ int exact_code(double y, double s) {
+    return s > 0.0 ? int(rint(fmin(fmax(y / s, -8.0), 7.0))) : 0;
+}
+// The elements of the rotated row from the sub-th of each eight pairs, and of each eight that do not turn, on: calls
+// use(value, place of its row of the factor), for eight lanes from 0 on as often.  Their rows lie in different banks.
+template <int D, typename F>
+__device__ __forceinline__ void exact_elements(const ExactRow &a, int sub, F use) {
+    const int half = a.rope_dim >> 1, i0 = a.inter ? 2 * sub : sub, i1 = a.inter ? i0 + 1 : sub + half;
+    const int step = a.inter ? 16 : 8;  // a multiple of eight rows: row_place goes on evenly
+    uint32_t x0 = a.x + 2 * i0, x1 = a.x + 2 * i1, c = a.cs + 4 * sub, k0 = row_place(i0), k1 = row_place(i1);
+#pragma unroll 1
+    for (int p = 0; p < half; p += 8) {
+        const double u = shared_bf16(x0), w = shared_bf16(x1), cc = double(shared_f32(c)), ss = double(shared_f32(c + 4 * half));
+        use(fma(u, cc, -(w * ss)), k0);
+        use(fma(w, cc, u * ss), k1);
+        x0 += 2 * step, x1 += 2 * step, c += 32;
+        k0 += 128 * step, k1 += 128 * step;
     }
-    auto column = [&](int n) -> double {
-        double y = 0.0;
+    uint32_t x = a.x + 2 * (a.rope_dim + sub), k = row_place(a.rope_dim + sub);
+#pragma unroll 2
+    for (int i = a.rope_dim; i < D; i += 8) {
+        use(shared_bf16(x), k);
+        x += 16, k += 1024;
+    }
+}
+
+// Four rows (`there`: this lane's is one) of which fp32 leaves few codes open, eight lanes a row.  `y32`: its fp32 values
+// in shared memory, off by at most `err`, the largest `m`; the codes that they gave are stored already.  A value y_n lies
+// over the border b, b + 1/2 whole, where 7 y_n - b alpha |y_t| > 0, y_t the largest: one sum over the row.  Returns
+// false where the largest is not sure.
+template <int D>
+__device__ __noinline__ bool border_rows(ExactRow a, uint8_t *codes, float alpha, bool there, uint32_t y32, float m,
+                                         float err, float inv, float limit) {
+    auto value = [&](int n) { return shared_f32(y32 + 4 * n); };
+    const int sub = threadIdx.x & 7;
+    uint32_t may = 0, near = 0;  // of this lane's columns, sub + 8 i
+    const float large = m - 2.5f * err, past = __fdividef(8.0f, inv);
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-            const int k = N * lane + e;
-            const uint16_t w = *reinterpret_cast<const uint16_t *>(factor + (n >> 6) * D * 128 + k * 128 +
-                                                                   ((((n & 63) >> 3) ^ (k & 7)) << 4) + 2 * (n & 7));
-            y = fma(xs[e], double(bf16_bits_to_float(w)), y);
-        }
+    for (int i = 0; i < D / 8; ++i) {
+        const float y = value(sub + 8 * i);
+        float off = 0.0f;
+        round_off(__float_as_uint(y), inv, off);
+        if (fabsf(y) >= large) may |= 1u << i;
+        if (off > limit && fabsf(y) < past) near |= 1u << i;
+    }
+    constexpr int NONE = 1 << 20;
+    auto next = [&](uint32_t &mask) -> int {  // the row's next column
+        const int n = mask ? sub + 8 * (__ffs(mask) - 1) : NONE;
+        int least = n;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-        return y;
+        for (int o = 4; o; o >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
+        if (n == least) mask &= mask - 1;
+        return least;
     };
-    float y[N];
-    double top = 0.0;
+    if (!there) may = near = 0;
+    // (indexes are columns of the row whatever there is: a load may be done ahead of the test that it hangs on)
+    const int first = next(may), top = first & (D - 1);
+    const bool sure = next(may) == NONE;
+    if (!sure) near = 0;
+    for (;;) {
+        const int found = next(near), n = found & (D - 1);
+        if (!__any_sync(0xffffffffu, found != NONE)) break;
+        double d = 0.0;
+        const float border = floorf(value(n) * inv) + 0.5f;
+        if (found != NONE) {
+            const double share = -double(copysignf(border, value(top) * border)) * double(alpha);
+            const Column<D> largest(a.factor, top), column(a.factor, n);
+            exact_elements<D>(a, sub, [&](double v, uint32_t k) { d = fma(v, fma(share, largest(k), 7.0 * column(k)), d); });
+        }
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-        y[e] = y32[N * lane + e];
-        uint32_t may = __ballot_sync(0xffffffffu, fabsf(y[e]) >= m * (1.0f - 2.5f * kBorder));  // the largest, maybe
-        while (may) {
-            const int l = __ffs(may) - 1;
-            may &= may - 1;
-            top = fmax(top, fabs(column(N * l + e)));
+        for (int o = 4; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+        if (sub == 0 && found != NONE) {
+            const int under = int(border - 0.5f), code = under + (d > 0.0 || (d == 0.0 && (under & 1)));
+            float off = 0.0f;
+            if (code != round_off(__float_as_uint(value(n)), inv, off)) {
+                const int shift = 4 * (n & 1), c = min(max(code, -8), 7);
+                codes[n >> 1] = uint8_t((codes[n >> 1] & ~(15 << shift)) | (c & 15) << shift);
+            }
         }
     }
+    __syncwarp();
+    return sure;
+}
+
+// A row of which every column may matter: the products cancel, or the scale is very small.
+template <int D>
+__device__ __noinline__ void whole_row(ExactRow a, uint8_t *codes, float *scale, float alpha) {
+    constexpr int N = D / 32;  // columns of a lane, side by side
+    const int lane = threadIdx.x & 31;
+    double y[N] = {}, top = 0.0;
+    exact_elements<D>(a, lane & 7, [&](double v, uint32_t k) {
+#pragma unroll 2
+        for (int l = 0; l < 8; ++l) {
+            const double x = __shfl_sync(0xffffffffu, v, l);
+            const uint32_t row = __shfl_sync(0xffffffffu, k, l);
+#pragma unroll
+            for (int e = 0; e < N; ++e) y[e] = fma(x, Column<D>(a.factor, N * lane + e)(row), y[e]);
+        }
+    });
+#pragma unroll
+    for (int e = 0; e < N; ++e) top = fmax(top, fabs(y[e]));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o));
     const double s = double(alpha) * top / 7.0;
-    uint32_t byte = 0;
+    uint32_t word = 0;
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-        const double r = s > 0.0 ? double(y[e]) / s : 0.0;
-        int c = int(rint(fmin(fmax(r, -8.0), 7.0)));
-        const float off = float(fabs(r - rint(r)));
-        uint32_t near = __ballot_sync(0xffffffffu, fabs(r) < 9.0 && off > 0.5f - 14.0f * kBorder / alpha);
-        while (near) {
-            const int l = __ffs(near) - 1;
-            near &= near - 1;
-            const double q = column(N * l + e);
-            if (lane == l) c = s > 0.0 ? int(rint(fmin(fmax(q / s, -8.0), 7.0))) : 0;
-        }
-        byte |= uint32_t(c & 15) << (4 * e);
-    }
-    if constexpr (N == 4) reinterpret_cast<uint16_t *>(codes)[lane] = uint16_t(byte);
-    else codes[lane] = uint8_t(byte);
+    for (int e = 0; e < N; ++e) word |= uint32_t(exact_code(y[e], s) & 15) << (4 * e);
+    __syncwarp();
+    if constexpr (N == 4) reinterpret_cast<uint16_t *>(codes)[lane] = uint16_t(word);
+    else codes[lane] = uint8_t(word);
     if (lane == 0) *scale = float(s);
     __syncwarp();
 }
 
+template <typename T>
+__device__ __forceinline__ T *from_lane(T *p, int lane) {
+    return reinterpret_cast<T *>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(p), lane));
+}
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
     uint64_t d;
     asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
@@ -168,12 +277,14 @@ __device__ __forceinline__ void take_term(float (&v)[8], uint32_t (&w)[4]) {
                 v[2 * i], v[2 * i + 1]);
     }
 }
-__device__ __forceinline__ void unpack8(const uint4 &u, float (&v)[8]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// Squares of eight bf16 values, added to eight sums.
+__device__ __forceinline__ void add_squares(const uint4 &u, uint64_t (&s)[4]) {
+    float v[8];
+    unpack8(u, v);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int e = 0; e < 4; ++e) {
+        const uint64_t p = pack2(v[2 * e], v[2 * e + 1]);
+        s[e] = f32x2_fma(p, p, s[e]);
     }
 }
 
@@ -243,14 +354,6 @@ __device__ __forceinline__ void rotated_row(const unsigned char *xrow, const flo
     }
 }
 
-// round_half_even(y * inv) as an int for |y * inv| < 2^22 (alpha >= 2^-19): the low mantissa bits
-// after adding 1.5 * 2^23; `off` keeps the largest distance to the rounded value.
-__device__ __forceinline__ int round_off(uint32_t ybits, float inv, float &off) {
-    const float y = __uint_as_float(ybits), b = fmaf(y, inv, 12582912.0f);
-    off = fmaxf(off, fabsf(fmaf(y, inv, -(b - 12582912.0f))));
-    return int(__float_as_uint(b)) - 0x4B400000;
-}
-
 template <int D>
 __global__ void __launch_bounds__(A_THREADS, 1)
     kq_kv_append_kernel(const __grid_constant__ KvAppendArgs a, int blocks_q, int blocks_k, int blocks_v) {
@@ -264,7 +367,7 @@ __global__ void __launch_bounds__(A_THREADS, 1)
     const uint32_t done = bar(pair), ready = bar(2 + pair), taken = bar(4 + pair);
     volatile int *s_abort = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
     if (tid == 0) {
-        for (int i = 0; i < 4; ++i) mbar_init(bar(i), 1);
+        for (int i = 0; i < 4; ++i) mbar_init(bar(i), i < 2 ? 1 : 2);
         mbar_init(bar(4), 4);
         mbar_init(bar(5), 4);
         *s_abort = 0;
@@ -310,11 +413,28 @@ __global__ void __launch_bounds__(A_THREADS, 1)
     auto source = [&](int t, int h) { return rows_from + int64_t(t) * stride + int64_t(h) * D; };
     {  // the factor
         const uint16_t *P = kind == 0 ? a.Pq : kind == 1 ? a.Pk : a.Pv;
+        uint64_t col[4] = {0, 0, 0, 0};  // squares of the eight columns that this thread has
+        static_assert(A_THREADS % (D / 8) == 0, "a thread's columns");
 #pragma unroll
         for (int u = tid; u < D * D / 8; u += A_THREADS) {
             const int k = u / (D / 8), n = 8 * (u % (D / 8));
-            *reinterpret_cast<uint4 *>(smem + (n >> 6) * D * 128 + k * 128 + ((((n & 63) >> 3) ^ (k & 7)) << 4)) =
-                __ldg(reinterpret_cast<const uint4 *>(P + k * D + n));
+            const uint4 p = __ldg(reinterpret_cast<const uint4 *>(P + k * D + n));
+            *reinterpret_cast<uint4 *>(smem + (n >> 6) * D * 128 + k * 128 + ((((n & 63) >> 3) ^ (k & 7)) << 4)) = p;
+            add_squares(p, col);
+        }
+        if (kind != 0) {
+            float c[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) unpack2(col[e], c[2 * e], c[2 * e + 1]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+#pragma unroll
+                for (int o = D / 8; o < 32; o <<= 1) c[e] += __shfl_xor_sync(0xffffffffu, c[e], o);
+            if (lane < D / 8) {
+                float4 *to = reinterpret_cast<float4 *>(smem + C::OFF_COL + (warp * D + 8 * lane) * 4);
+                to[0] = make_float4(c[0], c[1], c[2], c[3]);
+                to[1] = make_float4(c[4], c[5], c[6], c[7]);
+            }
         }
         fence_proxy_async_smem();
     }
@@ -376,7 +496,10 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                                    sdesc_nmajor_sw128(sbase + uint32_t(2048 * k), D * 128), idesc,
                                    accumulate || term + 1 < terms || k);
                     tc_commit(done);
-                    if (last) tc_commit(ready);
+                    if (last) {
+                        tc_commit(ready);
+                        mbar_arrive(ready);  // the rows' norms, written before the barrier
+                    }
                 }
                 __syncwarp();
             }
@@ -403,13 +526,31 @@ __global__ void __launch_bounds__(A_THREADS, 1)
             cp_async_wait<1>();
             named_barrier_sync(3 + pair, 256);  // the other warp's pieces
             multiplied();
+            float *norm = reinterpret_cast<float *>(smem + C::OFF_NORM) + ((2 * pair + stage) * 2 + which) * 128 + r;
             if (kind == 2) {
-                one_term();
+                uint64_t sq[4] = {0, 0, 0, 0};
+#pragma unroll 1
+                for (int i = 0; i < D / 16; ++i) {
+                    const uint4 u = reinterpret_cast<const uint4 *>(x)[2 * i + which];
+                    tmem_st_32x32b_x4(ta + uint32_t(4 * (2 * i + which)), u.x, u.y, u.z, u.w);
+                    add_squares(u, sq);
+                }
+                float s[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) unpack2(sq[e], s[2 * e], s[2 * e + 1]);
+                *norm = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
                 multiply(1, false, true);
             } else {
+                uint64_t sq = 0;
                 // queries: both terms; keys: the second and third, and then the first, which waits in the row's place
                 rotated_row<D>(x, cs, a.rope_dim, inter, which, [&](int i, float (&v)[8]) {
                     uint32_t w[4];
+                    if (kind == 1)
+#pragma unroll
+                        for (int e = 0; e < 8; e += 2) {
+                            const uint64_t p = pack2(v[e], v[e + 1]);
+                            sq = f32x2_fma(p, p, sq);
+                        }
                     take_term(v, w);
                     if (kind == 1) {
                         *reinterpret_cast<uint4 *>(x + 2 * i) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -419,6 +560,11 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                     tmem_st_32x32b_x4(ta + 64 + uint32_t(i >> 1), pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
                                       pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
                 });
+                if (kind == 1) {
+                    float even, odd;
+                    unpack2(sq, even, odd);
+                    *norm = even + odd;
+                }
                 multiply(2, false, kind == 0);
                 if (kind == 1) {
                     multiplied();
@@ -435,8 +581,20 @@ __global__ void __launch_bounds__(A_THREADS, 1)
     } else {
         // ---------------- rows out ----------------
         const uint32_t td = tmem + lanes + 128;
-        unsigned char *const own = smem + C::OFF_Y + (warp - 16) * 4096;
+        unsigned char *const own = smem + C::OFF_Y + (warp - 16) * C::OWN;
         __syncthreads();  // the factor
+        float column = 0.0f;  // the two-norm of its largest column
+        if (kind != 0) {
+            constexpr int N = D / 32;  // columns of a lane
+            float c[N] = {};
+            for (int w = 0; w < A_THREADS / 32; ++w)
+#pragma unroll
+                for (int e = 0; e < N; ++e)
+                    c[e] += reinterpret_cast<const float *>(smem + C::OFF_COL)[w * D + N * lane + e];
+#pragma unroll
+            for (int e = 0; e < N; ++e) column = fmaxf(column, c[e]);
+            column = sqrtf(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(column))));
+        }
         // This thread's row of a tile, its slot and position, loaded a tile ahead of their use.
         struct Row {
             int t, h, pos;
@@ -544,35 +702,68 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                     }
                     if (store) *scale = sc;
                     // ---- rows with a value too near a border for fp32, again in fp64 ----
-                    // (scales that leave fp32's normal range are among them; a NaN or an infinity is not)
-                    const bool near = store && m < 3.0e38f &&
-                                      (off > 0.5f - 7.0f * kBorder / alpha || (m > 0.0f && sc < 1e-30f));
-                    uint32_t again = __ballot_sync(0xffffffffu, near);
+                    // (scales that leave fp32's normal range, or would keep under 12 bits, are among them; a NaN or
+                    // an infinity is not).  y is off by err, and so is m: y / s by 7 / alpha + |y / s| times err / m,
+                    // and by three roundings; past 8 no border matters.
+                    const float *norms = reinterpret_cast<const float *>(smem + C::OFF_NORM) +
+                                         (2 * pair + int(turns & 1u)) * 256 + r;
+                    const float squares = norms[0] + norms[128], err = error_of<D>(squares, column);
+                    const float limit = 0.5f - 0x1p-19f - (7.0f / alpha + fminf(7.0f / alpha, 8.5f)) * __fdividef(err, m);
+                    const bool open = store && m < 3.0e38f && (m > 0.0f ? off > limit || sc < 1e-30f || err > m * 0x1p-12f
+                                                                         : squares > 0.0f);
+                    const bool few = m > 0.0f && sc >= 1e-30f && err <= m * 0x1p-12f && limit > 0.25f;
+                    uint32_t again = __ballot_sync(0xffffffffu, open && few);
+                    uint32_t wholes = __ballot_sync(0xffffffffu, open && !few);
                     const uint16_t *x = source(t, h);
-                    while (again) {
-                        const int src = __ffs(again) - 1;
-                        again &= again - 1;
+                    const int rope_dim = kind == 1 ? a.rope_dim : 0;
+                    // Lane group `at` of 8 or 32 lanes brings the row of lane `src`, and the table's.
+                    auto bring = [&](int at, int src, int from, int lanes) {
+                        const uint32_t to = smem_u32(own) + uint32_t(at * C::ROW_PLACE);
+                        const uint64_t px = reinterpret_cast<uint64_t>(from_lane(x, src));
+                        const uint64_t pc = reinterpret_cast<uint64_t>(from_lane(cs, src));
+                        for (int u = from; u < D / 8; u += lanes) cp_async16(to + C::ROW_X + 16 * u, px + 16 * u, 16u);
+                        for (int u = from; u < rope_dim / 4; u += lanes) cp_async16(to + C::ROW_CS + 16 * u, pc + 16 * u, 16u);
+                        cp_async_commit();
+                        return ExactRow{to + C::ROW_X, to + C::ROW_CS, sbase, rope_dim, a.rope_interleaved != 0};
+                    };
+                    while (again) {  // four at a time: a lane's row is the (lane / 8)th of them
+                        const int rank = __popc(again & ((1u << lane) - 1)), rows4 = min(4, __popc(again));
+                        const bool mine = (again >> lane & 1u) && rank < 4;
+                        int src = 0;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (k < rows4) {
+                                if (k == 0 || k == lane >> 3) src = __ffs(again) - 1;
+                                again &= again - 1;
+                            }
+                        const ExactRow row = bring(lane >> 3, src, lane & 7, 8);
 #pragma unroll
                         for (int c = 0; c < D / 32; ++c) {
                             uint32_t v[32];
                             tmem_ld_32x32b_x32(td + uint32_t(32 * c), v);
                             tmem_wait_ld();
-                            if (lane == src)
+                            if (mine)
 #pragma unroll
                                 for (int e = 0; e < 8; ++e)
-                                    *reinterpret_cast<uint4 *>(own + 128 * c + 16 * e) =
+                                    *reinterpret_cast<uint4 *>(own + rank * C::ROW_PLACE + 128 * c + 16 * e) =
                                         make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
                         }
-                        const uint64_t pc = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(codes), src);
-                        const uint64_t ps = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(scale), src);
-                        const uint64_t pt = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(cs), src);
-                        const uint64_t px = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(x), src);
-                        const float mm = __shfl_sync(0xffffffffu, m, src);
+                        cp_async_wait<0>();
                         __syncwarp();
-                        exact_row<D>(reinterpret_cast<const uint16_t *>(px), smem, reinterpret_cast<const float *>(own),
-                                     mm, reinterpret_cast<const float *>(pt), kind == 1 ? a.rope_dim : 0,
-                                     a.rope_interleaved != 0, alpha, reinterpret_cast<uint8_t *>(pc),
-                                     reinterpret_cast<float *>(ps));
+                        const bool sure =
+                            border_rows<D>(row, from_lane(codes, src), alpha, lane >> 3 < rows4,
+                                           row.x - C::ROW_X,
+                                           __shfl_sync(0xffffffffu, m, src), __shfl_sync(0xffffffffu, err, src),
+                                           __shfl_sync(0xffffffffu, inv, src), __shfl_sync(0xffffffffu, limit, src));
+                        __syncwarp();
+                        wholes |= __reduce_or_sync(0xffffffffu, lane >> 3 < rows4 && !sure ? 1u << src : 0u);
+                    }
+                    for (; wholes; wholes &= wholes - 1) {
+                        const int src = __ffs(wholes) - 1;
+                        const ExactRow row = bring(0, src, lane, 32);
+                        cp_async_wait<0>();
+                        __syncwarp();
+                        whole_row<D>(row, from_lane(codes, src), from_lane(scale, src), alpha);
                     }
                     tc_fence_before();
                     __syncwarp();
@@ -644,13 +835,16 @@ static cudaError_t launch_append_inst(const KvAppendArgs &a, int num_sms, int de
     });
     if (attr_err[device] != cudaSuccess) return attr_err[device];
     // Blocks for each kind: one more at a time to the kind whose blocks have the most to do.  A tile of keys
-    // takes about 1.4 times, one of values 1.0 times what one of queries does, and the rotation more the fewer
-    // heads there are: a warp's rows then read as many rows of the table (65536 tokens of 8 query heads on one
-    // key head: 149 us without the terms for that, 112 with them).
+    // takes about 2.1 times, one of values 1.7 times what one of queries does (1.8 and 1.4 at head_dim 64), with the
+    // rows that are computed again, and the rotation more the fewer heads there are: a warp's rows then read as many
+    // rows of the table.  (16 heads of each kind, 8192 tokens: 125 us at 2.1 and 1.7, 137 at 1.9 and 1.35; at
+    // head_dim 64 61 and 56; 65536 tokens of 8 query heads on one key head: 149 us without the terms for the rotation,
+    // 112 with them, before rows were computed again as often.)
     const int64_t tiles[3] = {(a.T * a.q_heads + 127) / 128, (a.T * a.c.heads + 127) / 128,
                               (a.T * a.c.heads + 127) / 128};
     const double turn = double(a.rope_dim) / D;
-    const double cost[3] = {1.0 + (a.q_heads ? 0.5 * turn / a.q_heads : 0.0), 1.4 + 1.5 * turn / a.c.heads, 1.0};
+    const double cost[3] = {1.0 + (a.q_heads ? 0.5 * turn / a.q_heads : 0.0),
+                            (D == 128 ? 2.1 : 1.8) + 1.5 * turn / a.c.heads, D == 128 ? 1.7 : 1.4};
     int blocks[3] = {tiles[0] > 0, 1, 1};
     for (int n = blocks[0] + 2; n < num_sms; ++n) {
         int most = -1;
