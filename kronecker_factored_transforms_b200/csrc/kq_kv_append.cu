@@ -391,15 +391,17 @@ __global__ void __launch_bounds__(A_THREADS, 1)
     griddep_wait();
     griddep_launch_dependents();
 
-    auto wait = [&](uint32_t b, uint32_t parity) {
+    // A wait that gives up raises the block's abort flag: no product is issued after it and no row stored.  The warps
+    // that make terms go through their tiles all the same, as they meet at barriers, but wait for nothing more.
+    auto wait = [&](uint32_t b, uint32_t parity, bool ignore_abort) -> bool {
         // looks 60 ns apart at first, which leave the issue slots to the other warps
         bool ok = mbar_try_wait(b, parity);
-        for (int i = 0; i < 200 && !ok; ++i) {
+        for (int i = 0; i < 200 && !ok && !*s_abort; ++i) {
             __nanosleep(60);
             ok = mbar_try_wait(b, parity);
         }
-        if (!ok) wait_bounded_err(b, parity, s_abort, kSiteKvAppendWait, kWaitLimitNs, false, a.err);
-        __syncwarp();
+        if (!ok) ok = wait_bounded_err(b, parity, s_abort, kSiteKvAppendWait, kWaitLimitNs, ignore_abort, a.err);
+        return __all_sync(0xffffffffu, ok);
     };
     // This thread's row of a tile: token and head; false past the last row.
     auto row_of = [&](int64_t tile, int &t, int &h) -> bool {
@@ -485,9 +487,9 @@ __global__ void __launch_bounds__(A_THREADS, 1)
             tc_fence_before();
             named_barrier_sync(1 + pair, 256);
             if ((warp & 7) == 0) {
-                if (!accumulate) wait(taken, (turns & 1u) ^ 1u);  // the last tile's rows
+                const bool ok = accumulate || wait(taken, (turns & 1u) ^ 1u, false);  // the last tile's rows
                 tc_fence_after();
-                if (elect_one()) {
+                if (elect_one() && ok && !*s_abort) {
                     // the smallest term first: the sum is truncated at every addition
                     for (int term = terms - 1; term >= 0; --term)
 #pragma unroll
@@ -506,8 +508,9 @@ __global__ void __launch_bounds__(A_THREADS, 1)
             ++products;
         };
         // the terms' columns are free once the last product is done
-        auto multiplied = [&] {
-            if (products) wait(done, (products - 1) & 1u);
+        // (where they are not in time the abort flag is up, and the next product is not issued)
+        auto multiplied = [&](bool ignore_abort) {
+            if (products) (void)wait(done, (products - 1) & 1u, ignore_abort);
             tc_fence_after();
         };
         const bool inter = a.rope_interleaved != 0;
@@ -525,7 +528,7 @@ __global__ void __launch_bounds__(A_THREADS, 1)
             look(tile + 4 * step, x2, pos2);
             cp_async_wait<1>();
             named_barrier_sync(3 + pair, 256);  // the other warp's pieces
-            multiplied();
+            multiplied(false);
             float *norm = reinterpret_cast<float *>(smem + C::OFF_NORM) + ((2 * pair + stage) * 2 + which) * 128 + r;
             if (kind == 2) {
                 uint64_t sq[4] = {0, 0, 0, 0};
@@ -567,7 +570,7 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                 }
                 multiply(2, false, kind == 0);
                 if (kind == 1) {
-                    multiplied();
+                    multiplied(false);
                     one_term();
                     multiply(1, true, true);
                 }
@@ -577,7 +580,8 @@ __global__ void __launch_bounds__(A_THREADS, 1)
             pos1 = pos2;
         }
         cp_async_wait<0>();
-        multiplied();
+        // the products in flight end before their TMEM is given back
+        multiplied(true);
     } else {
         // ---------------- rows out ----------------
         const uint32_t td = tmem + lanes + 128;
@@ -626,7 +630,7 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                     atomicOr(a.err, kSiteKvAppend);
                     slot = -1;
                 }
-                wait(ready, turns & 1u);
+                if (!wait(ready, turns & 1u, false) || __any_sync(0xffffffffu, *s_abort != 0)) break;
                 tc_fence_after();
                 if (kind == 0) {
                     // ---- queries: bf16, 64 columns at a time through the warp's 4 KB (32 rows of 128 bytes,

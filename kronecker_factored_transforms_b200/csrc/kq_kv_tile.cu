@@ -639,7 +639,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         // every product has ended before the block's TMEM is given back
         if (elect_one()) tc_commit(bar(C::DONE));
         __syncwarp();
-        wait_bounded_err(bar(C::DONE), 0u, s_abort, kSiteKvWait, kWaitLimitNs, true, a.err);
+        (void)wait_bounded_err(bar(C::DONE), 0u, s_abort, kSiteKvWait, kWaitLimitNs, true, a.err);
         __syncwarp();
     }
     tc_fence_before();
