@@ -177,8 +177,9 @@ def kq_w4a4_gemm_bf16(qx, sx, qw, sw, y, M: int, N: int, K: int, stream=None) ->
 class _Handle:
     """A C struct the caller fills in once: its address, and the tensors it points into."""
 
-    def __init__(self, struct, tensors):
+    def __init__(self, struct, tensors, head_dim):
         self._struct = struct
+        self.head_dim = head_dim
         self._tensors = [t for t in tensors if t is not None]  # kept alive with the handle
         self.ptr = ctypes.addressof(struct)
         devices = {t.device for t in self._tensors}
@@ -202,7 +203,7 @@ def kv_cache(k_codes, k_scale, v_codes, v_scale) -> _Handle:
             raise ValueError("k_scale and v_scale are float32 [pages, kv_heads, page_size]")
     st = _KVCacheStruct(k_codes.data_ptr(), k_scale.data_ptr(), v_codes.data_ptr(), v_scale.data_ptr(), pages, page,
                         heads, 2 * half)
-    return _Handle(st, [k_codes, k_scale, v_codes, v_scale])
+    return _Handle(st, [k_codes, k_scale, v_codes, v_scale], 2 * half)
 
 
 def kv_transform(Pq, Pk, Pv, alpha_k: float, alpha_v: float, rope=None, interleaved: bool = False) -> _Handle:
@@ -217,7 +218,7 @@ def kv_transform(Pq, Pk, Pv, alpha_k: float, alpha_v: float, rope=None, interlea
     n, r = (0, 0) if rope is None else rope.shape
     st = _KVTransformStruct(_ptr(Pq), _ptr(Pk), _ptr(Pv), float(alpha_k), float(alpha_v), _ptr(rope), n, r,
                             int(bool(interleaved)))
-    return _Handle(st, [Pq, Pk, Pv, rope])
+    return _Handle(st, [Pq, Pk, Pv, rope], Pk.shape[0])
 
 
 # torch's current device and the raw current stream of a device: looked up on the first call.
@@ -258,6 +259,9 @@ def _enter(fn: str, cache, stream, tensors):
 
 def kq_kv_append(cache, tf, q, q_stride: int, k, k_stride: int, v, v_stride: int, positions, slots, q_out, T: int,
                  q_heads: int, stream=None) -> None:
+    if tf.device != cache.device or tf.head_dim != cache.head_dim:
+        raise ValueError("kq_kv_append: the transform is of head_dim %d on cuda:%d, the cache of %d on cuda:%d"
+                         % (tf.head_dim, tf.device, cache.head_dim, cache.device))
     st, (q, k, v, positions, slots, q_out) = _enter("kq_kv_append", cache, stream, (q, k, v, positions, slots, q_out))
     r = lib.kq_kv_append(cache.ptr, tf.ptr, q, q_stride, k, k_stride, v, v_stride, positions, slots, q_out, T, q_heads, st)
     if r:
