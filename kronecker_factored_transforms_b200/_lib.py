@@ -211,7 +211,8 @@ def kv_transform(Pq, Pk, Pv, alpha_k: float, alpha_v: float, rope=None, interlea
     and a rotary table fp32 [positions, rotated elements] (cosines, then sines) or None."""
     import torch
     for P in (Pq, Pk, Pv):
-        if P is not None and (P.shape != Pk.shape or P.dim() != 2 or P.shape[0] != P.shape[1] or P.element_size() != 2):
+        if P is not None and (P.shape != Pk.shape or P.dim() != 2 or P.shape[0] != P.shape[1]
+                              or P.dtype not in (torch.bfloat16, torch.int16, torch.uint16)):
             raise ValueError("the factors are square matrices of one size, in bf16")
     if rope is not None and (rope.dim() != 2 or rope.dtype != torch.float32):
         raise ValueError("the rotary table is float32 [positions, rotated elements]")

@@ -96,3 +96,11 @@ def test_handles_know_their_head_dim(kq):
     finally:
         kq._Handle = base
     assert kept == [128, 64]
+
+
+def test_fp16_factors(kq):
+    """Two bytes an element, but other numbers."""
+    P = torch.zeros(64, 64, dtype=B16)
+    for bad in ((P.half(), P, P), (P, P.half(), P), (P, P, P.half())):
+        with pytest.raises(ValueError, match="bf16"):
+            kq.kv_transform(*bad, 0.9, 0.9)
