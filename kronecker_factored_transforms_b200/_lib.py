@@ -222,37 +222,55 @@ def kv_transform(Pq, Pk, Pv, alpha_k: float, alpha_v: float, rope=None, interlea
     return _Handle(st, [Pq, Pk, Pv, rope], Pk.shape[0])
 
 
-# torch's current device and the raw current stream of a device: looked up on the first call.
+# torch's current device and the raw current stream of a device, the types of the calls' tensors, and those that are the
+# same bits (for none, a workspace: any): looked up on the first call.
 _current_device = None
 _raw_stream = None
+_append_kinds = _gather_kinds = _attention_kinds = _shared_kinds = _same_bits = None
 
 
 def _device_calls():
-    global _current_device, _raw_stream
+    global _current_device, _raw_stream, _append_kinds, _gather_kinds, _attention_kinds, _shared_kinds, _same_bits
     import torch
+    bf16, int32, int64, fp32 = torch.bfloat16, torch.int32, torch.int64, torch.float32
+    _same_bits = {bf16: (torch.int16, torch.uint16), int32: (torch.uint32,), int64: (torch.uint64,), fp32: ()}
+    _append_kinds = (bf16, bf16, bf16, int32, int64, bf16)
+    _gather_kinds = (int64, bf16, bf16)
+    _attention_kinds = (bf16, int32, int32, int32, bf16, fp32, torch.uint8)
+    _shared_kinds = (bf16, int32, int32, int32, int32, bf16, fp32, torch.uint8)
     _current_device = torch.cuda.current_device
     # the public way makes a Stream object, which takes as long as the launch
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
         (lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
-def _enter(fn: str, cache, stream, tensors):
-    """The stream (a C entry works on the current device: another one is an error here) and the tensors' addresses.
+def _unusual(fn: str, cache, t, at: int, kind, rows: bool):
+    """The address of a tensor that is not of its kind's type, or not dense, where it may be so."""
+    if t.get_device() != cache.device:
+        raise ValueError("%s: a tensor on %s, the cache on cuda:%d" % (fn, t.device, cache.device))
+    if t.dtype is not kind and kind in _same_bits and t.dtype not in _same_bits[kind]:
+        raise ValueError("%s: tensor %d is %s, not %s" % (fn, at, t.dtype, kind))
+    if not (t.stride(-1) == 1 if rows else t.is_contiguous()):
+        raise ValueError("%s: tensor %d is not dense (strides %s)" % (fn, at, t.stride()))
+    return t.data_ptr()
+
+
+def _enter(fn: str, cache, stream, tensors, kinds, rows=0):
+    """The stream (a C entry works on the current device: another one is an error here) and the tensors' addresses,
+    where these are the numbers that the entry will read there (the first `rows`: rows a stride apart).
 
     These calls take microseconds on the GPU for small batches, so this is kept short."""
-    if _raw_stream is None:
-        _device_calls()
     device = cache.device
     if _current_device() != device:
         raise ValueError("%s: the cache lies on cuda:%d, the current device is cuda:%d" % (fn, device, _current_device()))
     ptrs = []
-    for t in tensors:
+    for t, kind in zip(tensors, kinds):
         if t is None or t.__class__ is int:
             ptrs.append(t)
-        elif t.get_device() != device:
-            raise ValueError("%s: a tensor on %s, the cache on cuda:%d" % (fn, t.device, device))
-        else:
+        elif t.get_device() == device and t.dtype is kind and t.is_contiguous():  # the usual case
             ptrs.append(t.data_ptr())
+        else:
+            ptrs.append(_unusual(fn, cache, t, len(ptrs), kind, len(ptrs) < rows))
     if stream is None:
         return _raw_stream(device) or None, ptrs
     return _stream(stream), ptrs
@@ -263,14 +281,19 @@ def kq_kv_append(cache, tf, q, q_stride: int, k, k_stride: int, v, v_stride: int
     if tf.device != cache.device or tf.head_dim != cache.head_dim:
         raise ValueError("kq_kv_append: the transform is of head_dim %d on cuda:%d, the cache of %d on cuda:%d"
                          % (tf.head_dim, tf.device, cache.head_dim, cache.device))
-    st, (q, k, v, positions, slots, q_out) = _enter("kq_kv_append", cache, stream, (q, k, v, positions, slots, q_out))
+    if _raw_stream is None:
+        _device_calls()
+    st, (q, k, v, positions, slots, q_out) = _enter(
+        "kq_kv_append", cache, stream, (q, k, v, positions, slots, q_out), _append_kinds, 3)
     r = lib.kq_kv_append(cache.ptr, tf.ptr, q, q_stride, k, k_stride, v, v_stride, positions, slots, q_out, T, q_heads, st)
     if r:
         _check("kq_kv_append", r)
 
 
 def kq_kv_gather(cache, slots, k_out, v_out, T: int, stream=None) -> None:
-    st, (slots, k_out, v_out) = _enter("kq_kv_gather", cache, stream, (slots, k_out, v_out))
+    if _raw_stream is None:
+        _device_calls()
+    st, (slots, k_out, v_out) = _enter("kq_kv_gather", cache, stream, (slots, k_out, v_out), _gather_kinds)
     r = lib.kq_kv_gather(cache.ptr, slots, k_out, v_out, T, st)
     if r:
         _check("kq_kv_gather", r)
@@ -284,8 +307,10 @@ def kq_kv_attention_workspace_bytes(T: int, B: int, q_heads: int, kv_heads: int,
 def kq_kv_attention(cache, q, q_start, page_table, max_pages: int, kv_len, scale: float, softcap: float, window: int,
                     out, lse, workspace, workspace_bytes: int, T: int, B: int, q_heads: int, max_q: int,
                     stream=None) -> None:
+    if _raw_stream is None:
+        _device_calls()
     st, (q, q_start, page_table, kv_len, out, lse, workspace) = _enter(
-        "kq_kv_attention", cache, stream, (q, q_start, page_table, kv_len, out, lse, workspace))
+        "kq_kv_attention", cache, stream, (q, q_start, page_table, kv_len, out, lse, workspace), _attention_kinds)
     r = lib.kq_kv_attention(cache.ptr, q, q_start, page_table, max_pages, kv_len, scale, softcap, window, out, lse,
                             workspace, workspace_bytes, T, B, q_heads, max_q, st)
     if r:
@@ -295,8 +320,11 @@ def kq_kv_attention(cache, q, q_start, page_table, max_pages: int, kv_len, scale
 def kq_kv_attention_shared(cache, q, q_start, prefix_pages, prefix_len: int, page_table, max_pages: int, kv_len,
                            scale: float, softcap: float, window: int, out, lse, workspace, workspace_bytes: int,
                            T: int, B: int, q_heads: int, max_q: int, stream=None) -> None:
+    if _raw_stream is None:
+        _device_calls()
     st, (q, q_start, prefix_pages, page_table, kv_len, out, lse, workspace) = _enter(
-        "kq_kv_attention_shared", cache, stream, (q, q_start, prefix_pages, page_table, kv_len, out, lse, workspace))
+        "kq_kv_attention_shared", cache, stream, (q, q_start, prefix_pages, page_table, kv_len, out, lse, workspace),
+        _shared_kinds)
     r = lib.kq_kv_attention_shared(cache.ptr, q, q_start, prefix_pages, prefix_len, page_table, max_pages, kv_len, scale,
                                    softcap, window, out, lse, workspace, workspace_bytes, T, B, q_heads, max_q, st)
     if r:

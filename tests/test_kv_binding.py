@@ -104,3 +104,35 @@ def test_fp16_factors(kq):
     for bad in ((P.half(), P, P), (P, P.half(), P), (P, P, P.half())):
         with pytest.raises(ValueError, match="bf16"):
             kq.kv_transform(*bad, 0.9, 0.9)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(pos=torch.zeros(T, dtype=I64)), dict(pos=torch.zeros(T)), dict(slot=torch.zeros(T, dtype=I32)),
+    dict(pos=torch.zeros(2 * T, dtype=I32)[::2]), dict(slot=torch.zeros(2 * T, dtype=I64)[::2]),
+    dict(q=torch.zeros(T, H, D)), dict(k=torch.zeros(T, HK, D, dtype=torch.float16)),
+    dict(v=torch.zeros(T, D, HK, dtype=B16).transpose(1, 2)), dict(out=torch.zeros(T, H, D)),
+    dict(out=torch.zeros(T, 2 * H, D, dtype=B16)[:, :H])])
+def test_append_types_and_strides(kq, kw):
+    refused(kq, append, **kw)
+
+
+@pytest.mark.parametrize("kw", [dict(slot=torch.zeros(T, dtype=I32)), dict(k=torch.zeros(T, HK, D)),
+                                dict(v=torch.zeros(T, 2 * HK, D, dtype=B16)[:, :HK])])
+def test_gather_types_and_strides(kq, kw):
+    refused(kq, gather, **kw)
+
+
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("kw", [
+    dict(table=torch.zeros(2, 5, dtype=I64)), dict(table=torch.zeros(2, 10, dtype=I32)[:, :5]), dict(len=torch.zeros(2, dtype=I64)),
+    dict(len=torch.zeros(4, dtype=I32)[::2]), dict(start=torch.zeros(3, dtype=I64)), dict(start=torch.zeros(6, dtype=I32)[::2]),
+    dict(q=torch.zeros(T, 2 * H, D, dtype=B16)[:, :H]), dict(q=torch.zeros(T, H, D, dtype=torch.float16)),
+    dict(out=torch.zeros(T, H, D, dtype=torch.float16)), dict(out=torch.zeros(H, T, D, dtype=B16).transpose(0, 1)),
+    dict(lse=torch.zeros(T, H, dtype=torch.float64)), dict(lse=torch.zeros(H, T).T), dict(ws=torch.zeros(2000, dtype=torch.uint8)[::2])])
+def test_attention_types_and_strides(kq, kw, shared):
+    refused(kq, lambda kq, **a: attend(kq, shared, **a), **kw)
+
+
+def test_prefix_types_and_strides(kq):
+    for pre in (torch.zeros(2, dtype=I64), torch.zeros(4, dtype=I32)[::2]):
+        refused(kq, lambda kq, **a: attend(kq, True, **a), pre=pre)
