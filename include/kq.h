@@ -407,8 +407,12 @@ kq_status kq_kv_gather(const kq_kv_cache *cache, const int64_t *slots, uint16_t 
  * The scales in the cache are not negative and, where a query sees their row, finite;
  * rows that it does not see may hold anything.  A value's scale is 0 or from 2^-100 to
  * 2^96 (under a smaller one a weight loses bits, over a larger one sums may overflow).
- * Scores and softmax sums are fp32, and the products' accumulators too.  The same
- * inputs give the same bits.  Nothing is read back to the host: sequences may
+ * Scores and softmax sums are fp32, and the products' accumulators too.  A weight is
+ * rounded once before it meets its value: to fp16's 11 bits where a key head has up to 48
+ * rows of queries of a sequence (up to 32 in all over a shared prefix), to bf16's 8 where
+ * it has more (an error of 1.4 times that of the result's own rounding).  So |scale q| 2^11
+ * and the sums of |q| times a code of up to 8 are to fit fp32.  The same inputs give the
+ * same bits.  Nothing is read back to the host: sequences may
  * grow between replays of a captured graph.
  * Returns KQ_ERR_SHAPE, KQ_ERR_UNSUPPORTED (head_dim, page_size), KQ_ERR_NULL,
  * KQ_ERR_ALIGN, KQ_ERR_ARG (scale, softcap, window, max_q, workspace too small,
@@ -427,7 +431,10 @@ kq_status kq_kv_attention(const kq_kv_cache *cache, const uint16_t *q, const int
  * the prefix is read and multiplied once for the queries of all sequences, and
  * joined with each sequence's own keys.
  *
- * prefix_pages [ceil(prefix_len / page_size)] device int32: the prefix's pages.
+ * prefix_pages [ceil(prefix_len / page_size)] device int32: the prefix's pages, all of
+ *              which are read and multiplied whatever the window: where it leaves
+ *              nothing of the prefix's beginning to any query, give a later part of it
+ *              (whole pages, and prefix_len less by their keys).
  * prefix_len   host; 0 is kq_kv_attention.
  * kv_len and page_table describe the keys after the prefix: key t of sequence b
  * is at position prefix_len + t.  Every query sees the whole prefix, except that

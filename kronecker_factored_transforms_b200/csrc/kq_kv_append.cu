@@ -37,7 +37,8 @@
 // table (2.7 TB/s of 6.55), with the read-back of their keys and values, 13 us of that;
 // 116 us when a border of 2^-19 of max|y| sent one row in 250 back, which a factor that
 // cancels does not keep to.  Both teams' chains (rows, rotation, terms, product, codes)
-// are waiting most of the time, and 24 warps at 80 registers are all that an SM holds.
+// are waiting most of the time, and 24 warps at 80 registers (head_dim 128: with 80 bytes
+// of spills) are all that an SM holds.
 #include <mutex>
 
 #include "kq_common.cuh"

@@ -39,9 +39,9 @@
 // which kq_kv_combine_kernel joins in a fixed order.
 //
 // Measured, head_dim 128 and 8 key heads: 4 sequences of 65 to 131 thousand keys, 4 query
-// heads a key head, 97 us (4.4 TB/s of 6.55; issue slots 56 % busy, ALU 52 %: some 500
+// heads a key head, 97-104 us (4.2-4.4 TB/s of 6.55; issue slots 56 % busy, ALU 52 %: some 500
 // instructions for 32 keys and warp); 64 sequences of 60 to 8192 keys, 8 query heads a key
-// head, 37 us (2.6 TB/s); one token on 1531 keys 10 us.
+// head, 37-39 us; one token on 1531 keys 10 us.  With capped scores 42 us for 40 without.
 #include <cuda_fp16.h>
 
 #include <mutex>
@@ -853,6 +853,7 @@ int row_tile(int64_t rows) { return rows <= 8 ? 8 : 16; }
 // kernel, head_dim 128, 24 sequences of 100 to 4100 keys on 4 key heads: 20 rows 28 against 41, 40 rows 35
 // against 42, 64 rows 50 against 46.  A prefix on 8 key heads: 32 rows 17 against 19 (1000 keys) and 28
 // against 29 (8000), 64 rows 20 against 21 (1000) but 70 against 37 (16000).
+// (All at head_dim 128; at 64 nothing was measured, and the prefix's length is not asked.)
 constexpr int kManyRows = 48;
 bool many_rows(int64_t rows) { return rows > kManyRows; }
 bool many_prefix_rows(int64_t rows) { return rows > 32; }

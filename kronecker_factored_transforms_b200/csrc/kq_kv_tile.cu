@@ -35,7 +35,8 @@
 // Measured, head_dim 128: two chunks of 1024 and fewer queries on 2500 to 6000 keys, 32 heads
 // on 8 key heads, 199 us (690 TFLOP/s; tensor pipe and exponentials both 40 % busy): a step
 // of 256 rows x 128 keys takes 4500 clocks, in which a row tile's softmax (2400 to 2850) and
-// its products (1600) wait for one another; a second set of scores has no place in TMEM.
+// its products (1600) wait for one another; a second set of scores has no place in TMEM
+// there (at head_dim 64, where 128 columns are free, the order is the same).
 // A prefix of 16384 keys for 64 sequences of 8 heads a key head: 68 us with the own keys.
 #include <mutex>
 
